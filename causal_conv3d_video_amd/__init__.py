@@ -29,6 +29,10 @@ __all__ = [
     "causal_conv3d_forward_packed_noalloc",
     "causal_conv3d_forward_u8", "causal_conv3d_status_string", "causal_conv3d_counters", "library_path",
     "EXPORTED_SYMBOLS", "VARIANTS",
+    "make_conv1d_desc", "causal_conv1d_plan", "causal_conv1d_forward", "causal_conv1d_backward",
+    "make_scan_desc", "selective_scan_plan", "selective_scan_forward", "selective_scan_backward",
+    "make_join_desc", "norm_join_plan", "norm_join_forward", "norm_join_backward",
+    "SEQ_EXPORTED_SYMBOLS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -366,3 +370,11 @@ def causal_conv3d_counters(reset=False):
     c = Counters()
     _lib.causal_conv3d_counters(ctypes.byref(c), int(bool(reset)))
     return {name: getattr(c, name) for name, _ in Counters._fields_}
+
+
+# The sequence operators (include/cc3d_seq.h) share this module's library
+# handle, status codes and error class.
+from .seq import (  # noqa: E402
+    SEQ_EXPORTED_SYMBOLS, causal_conv1d_backward, causal_conv1d_forward, causal_conv1d_plan, make_conv1d_desc,
+    make_join_desc, make_scan_desc, norm_join_backward, norm_join_forward, norm_join_plan, selective_scan_backward,
+    selective_scan_forward, selective_scan_plan)

@@ -1,0 +1,116 @@
+// Device helpers of the sequence operators' kernels.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "cc3d_seq_internal.h"
+
+namespace {
+
+typedef unsigned u32x4_s __attribute__((ext_vector_type(4)));
+typedef float f32x4_s __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Storage types: bf16 is held as its 16 bits.
+using bf16_s = unsigned short;
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16_s v) { return __uint_as_float(unsigned(v) << 16); }
+
+template <class T>
+__device__ __forceinline__ T from_f32(float v) {
+  if constexpr (std::is_same_v<T, float>) return v;
+  else return __builtin_bit_cast(bf16_s, static_cast<__bf16>(v));  // to nearest even
+}
+
+// Eight consecutive elements as they are stored; 16 bytes a register quad.
+template <class T>
+struct Raw8 {
+  u32x4_s q[sizeof(T) / 2];
+};
+
+template <class T>
+__device__ __forceinline__ Raw8<T> load8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < int(sizeof(T) / 2); ++i) r.q[i] = reinterpret_cast<const u32x4_s*>(p)[i];
+  return r;
+}
+
+template <class T>
+__device__ __forceinline__ Raw8<T> zero8() {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < int(sizeof(T) / 2); ++i) r.q[i] = u32x4_s{0, 0, 0, 0};
+  return r;
+}
+
+template <class T>
+__device__ __forceinline__ float get8(const Raw8<T>& r, int j) {
+  if constexpr (std::is_same_v<T, float>) return __uint_as_float(r.q[j / 4][j % 4]);
+  else return __uint_as_float(j & 1 ? r.q[0][j / 2] & 0xffff0000u : r.q[0][j / 2] << 16);
+}
+
+__device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
+  return unsigned(from_f32<bf16_s>(lo)) | (unsigned(from_f32<bf16_s>(hi)) << 16);
+}
+
+template <class T>
+__device__ __forceinline__ void store8(T* p, const float* v) {
+  if constexpr (std::is_same_v<T, float>) {
+    reinterpret_cast<f32x4_s*>(p)[0] = f32x4_s{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<f32x4_s*>(p)[1] = f32x4_s{v[4], v[5], v[6], v[7]};
+  } else {
+    *reinterpret_cast<u32x4_s*>(p) =
+        u32x4_s{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+  }
+}
+
+// 1 / (1 + exp(-v)): the exponential of a large -v is infinite and its
+// reciprocal zero.
+__device__ __forceinline__ float sigmoid_f32(float v) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * kLog2e));
+}
+
+// log(1 + exp(v)), v itself above 20 (where exp(-v) is below half a unit in
+// the last place of v).  log2 of a number near 1 loses the small one, so
+// below -4, where e = exp(v) < 0.02, the series e - e^2/2 + e^3/3 - e^4/4
+// (its next term is below 2^-25 of the first).
+__device__ __forceinline__ float softplus_f32(float v) {
+  const float e = __builtin_amdgcn_exp2f(v * kLog2e);
+  const float series = e * (1.f + e * (-0.5f + e * (0.33333333f - 0.25f * e)));
+  const float full = kLn2 * __builtin_amdgcn_logf(1.f + e);
+  return v > 20.f ? v : v < -4.f ? series : full;
+}
+
+// v from lane ^ X of the wave, X = 1, 2, 4 or 8 (reached by mirroring half a
+// row of 16 and then the row, once the lower bits are equal).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float(unsigned(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v)), CTRL, 0xf, 0xf, true)));
+}
+
+// Sum over aligned groups of G lanes of a wave, in every lane of the group;
+// the same order whatever the lane.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+  if constexpr (G >= 2) v += dpp<0xB1>(v);    // quad_perm [1, 0, 3, 2]
+  if constexpr (G >= 4) v += dpp<0x4E>(v);    // quad_perm [2, 3, 0, 1]
+  if constexpr (G >= 8) v += dpp<0x141>(v);   // row_half_mirror
+  if constexpr (G >= 16) v += dpp<0x140>(v);  // row_mirror
+  if constexpr (G >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (G >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
+}
+
+}  // namespace

@@ -1,0 +1,70 @@
+// Shared by the host side of the sequence operators (cc3d_seq_plan.cpp:
+// plans, argument checks, C entry points) and their kernel files: the plans
+// and the launch functions.
+#pragma once
+#include "cc3d_internal.h"
+#include "cc3d_seq.h"
+
+struct cc3d_conv1d_plan {
+  cc3d_conv1d_desc_t d{};
+  cc3d_seq_info_t info{};
+  int32_t seg = 0;        // forward: tokens per thread
+  int32_t bwd_seg = 0;    // backward: tokens per step of a thread
+  int64_t bwd_rows = 0;   // backward: partial sums of dw and db
+};
+
+struct cc3d_scan_plan {
+  cc3d_scan_desc_t d{};
+  cc3d_seq_info_t info{};
+  int32_t chunk = 0;      // forward: tokens per chunk (a multiple of 4; T rounded up when not split)
+  int32_t bwd_chunk = 0;
+  int32_t bwd_workers = 0;  // backward: workgroups per channel tile (each takes every bwd_workers-th chunk)
+};
+
+struct cc3d_join_plan {
+  cc3d_join_desc_t d{};
+  cc3d_seq_info_t info{};
+  int64_t bwd_parts = 0;    // backward: workgroups, each with a row of partial sums
+  int64_t gate_parts = 0;   // backward: workgroups per gate row (0: whole gate rows per workgroup)
+};
+
+namespace cc3d {
+
+// Lanes that hold one row of the block join (8 channels each), a power of two.
+constexpr int kJoinThreads = 256;
+inline int join_lanes(int c) {
+  int l = 8;
+  while (l * 8 < c) l *= 2;
+  return l;
+}
+
+// Channels per workgroup row of the convolution's backward pass and of the
+// scan, and states per wave of the scan.
+constexpr int kScanLanes = 64;
+constexpr int kScanFwdStates = 16;
+constexpr int kScanBwdStates = 8;
+constexpr int kScanMaxStates = 64;
+
+inline int scan_tiles_per_group(const cc3d_scan_desc_t& d) {
+  return (d.d / d.groups + kScanLanes - 1) / kScanLanes;
+}
+// States a wave holds, and waves that share one tile of channels.
+inline int scan_fwd_ns(const cc3d_scan_desc_t& d) { return d.states <= 4 ? 4 : d.states <= 8 ? 8 : 16; }
+inline int scan_fwd_waves(const cc3d_scan_desc_t& d) { return (d.states + scan_fwd_ns(d) - 1) / scan_fwd_ns(d); }
+inline int scan_bwd_ns(const cc3d_scan_desc_t& d) { return d.states <= 4 ? 4 : 8; }
+inline int scan_bwd_waves(const cc3d_scan_desc_t& d) { return (d.states + scan_bwd_ns(d) - 1) / scan_bwd_ns(d); }
+
+// Each returns 0, or the runtime's error code when it rejected a launch.
+// Arguments have been checked.
+int launch_conv1d_forward(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& a, void* stream);
+int launch_conv1d_backward(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& a, void* stream);
+int launch_scan_forward(const cc3d_scan_plan& p, const cc3d_scan_args_t& a, void* stream);
+int launch_scan_backward(const cc3d_scan_plan& p, const cc3d_scan_args_t& a, void* stream);
+int launch_join_forward(const cc3d_join_plan& p, const cc3d_join_args_t& a, void* stream);
+int launch_join_backward(const cc3d_join_plan& p, const cc3d_join_args_t& a, void* stream);
+
+// out[m] = sum over r of part[r][m], r = 0 .. rows - 1 in a fixed order; a
+// null out is skipped (cc3d_seq_conv1d.hip).
+int launch_sum_rows(const float* part, int64_t rows, int64_t cols, int64_t stride, float* out, void* stream);
+
+}  // namespace cc3d
