@@ -17,7 +17,6 @@ struct cc3d_scan_plan {
   cc3d_scan_desc_t d{};
   cc3d_seq_info_t info{};
   int32_t chunk = 0;      // forward: tokens per chunk (a multiple of 4; T rounded up when not split)
-  int32_t bwd_chunk = 0;
   int32_t bwd_workers = 0;  // backward: workgroups per channel tile (each takes every bwd_workers-th chunk)
 };
 
@@ -42,7 +41,6 @@ inline int join_lanes(int c) {
 // scan, and states per wave of the scan.
 constexpr int kScanLanes = 64;
 constexpr int kScanFwdStates = 16;
-constexpr int kScanBwdStates = 8;
 constexpr int kScanMaxStates = 64;
 
 inline int scan_tiles_per_group(const cc3d_scan_desc_t& d) {
@@ -51,8 +49,32 @@ inline int scan_tiles_per_group(const cc3d_scan_desc_t& d) {
 // States a wave holds, and waves that share one tile of channels.
 inline int scan_fwd_ns(const cc3d_scan_desc_t& d) { return d.states <= 4 ? 4 : d.states <= 8 ? 8 : 16; }
 inline int scan_fwd_waves(const cc3d_scan_desc_t& d) { return (d.states + scan_fwd_ns(d) - 1) / scan_fwd_ns(d); }
-inline int scan_bwd_ns(const cc3d_scan_desc_t& d) { return d.states <= 4 ? 4 : 8; }
-inline int scan_bwd_waves(const cc3d_scan_desc_t& d) { return (d.states + scan_bwd_ns(d) - 1) / scan_bwd_ns(d); }
+
+// The backward pass' layout.  A lane holds two neighbouring channels with
+// four states each; `sg` groups of lanes of a wave hold different states, so a
+// wave covers 4 * sg states of 128 / sg channels.  A workgroup is `waves`
+// waves of further states by `wc` waves of further channels.
+struct ScanBwdShape {
+  int sg;       // 1, 2 or 4
+  int sub;      // tokens walked back at a time
+  int waves, wc;
+  int tiles_per_group;
+  int chunk;
+};
+inline ScanBwdShape scan_bwd_shape(const cc3d_scan_desc_t& d) {
+  ScanBwdShape v;
+  v.sg = d.states <= 4 ? 1 : d.states <= 8 ? 2 : 4;
+  v.sub = v.sg == 1 ? 4 : 8;
+  v.waves = (d.states + 4 * v.sg - 1) / (4 * v.sg);
+  const int wide = d.d / d.groups, each = 128 / v.sg;
+  v.wc = 1;
+  while (v.wc * 2 * v.waves <= 4 && v.wc * each < wide) v.wc *= 2;
+  v.tiles_per_group = (wide + each * v.wc - 1) / (each * v.wc);
+  // 64 tokens keep seven states a lane's element between them, 32 those of four-token walks
+  const int most = v.sg == 1 ? 32 : 64;
+  v.chunk = d.t >= most ? most : (d.t + v.sub - 1) / v.sub * v.sub;
+  return v;
+}
 
 // Each returns 0, or the runtime's error code when it rejected a launch.
 // Arguments have been checked.

@@ -42,6 +42,9 @@ constexpr int64_t kSimds = 1024;
 // Workgroups of one launch, and the addresses a view may span.
 constexpr int64_t kMaxBlocks = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSpan = int64_t(1) << 46;
+// Elements between two tokens of the scan's backward pass: offsets inside a
+// chunk of 64 tokens are 32 bits.
+constexpr int64_t kMaxRow = (int64_t(1) << 25) - 1;
 // Tokens of one call: token counters are 32 bits and run a chunk past the end.
 constexpr int32_t kMaxTokens = 1 << 30;
 
@@ -267,8 +270,9 @@ extern "C" cc3d_status_t selective_scan_plan(const cc3d_scan_desc_t* d, cc3d_sca
     chunk = ceildiv(ceildiv(d->t, pieces), 4) * 4;
   }
   const int64_t chunks = ceildiv(d->t, chunk);
-  const int64_t bwd_chunk = std::min<int64_t>(cc3d::scan_bwd_waves(*d) > 4 ? 32 : 64, ceildiv(d->t, 8) * 8);
-  const int64_t bwd_chunks = ceildiv(d->t, bwd_chunk);
+  const cc3d::ScanBwdShape bw = cc3d::scan_bwd_shape(*d);
+  const int64_t bwd_chunks = ceildiv(d->t, bw.chunk);
+  const int64_t bwd_tiles = int64_t(d->groups) * bw.tiles_per_group;
   if (int64_t(d->n) * std::max(chunks, bwd_chunks) > kMaxBlocks / tiles ||
       int64_t(d->n) * d->states > kMaxBlocks / ceildiv(d->d, 64))
     return refuse(CC3D_ERR_UNSUPPORTED);
@@ -276,19 +280,17 @@ extern "C" cc3d_status_t selective_scan_plan(const cc3d_scan_desc_t* d, cc3d_sca
   if (!p) return CC3D_ERR_NO_MEMORY;
   p->chunk = int32_t(chunk);
   p->info.chunks = int32_t(chunks);
-  p->bwd_chunk = int32_t(bwd_chunk);
   p->info.backward_chunks = int32_t(bwd_chunks);
   // carries [n][chunk][S][C] and the chunks' sums of delta [n][chunk][C]
   const int64_t state = int64_t(d->states) * d->d, nc = int64_t(d->n);
   if (chunks > 1) p->info.workspace_bytes = nc * chunks * (state + d->d) * 4;
-  const int64_t items = nc * bwd_chunks;
-  p->bwd_workers = int32_t(std::min<int64_t>(items, std::max<int64_t>(1, ceildiv(2 * kSimds, tiles * cc3d::scan_bwd_waves(*d)))));
-  // partial sums: dA [worker][S][C], dD and ddt_bias [worker * waves][C], dB and dC [tile][n][t][2][S']
-  const int64_t waves = cc3d::scan_bwd_waves(*d), sp = waves * cc3d::scan_bwd_ns(*d);
+  // backward: two waves a SIMD, each workgroup taking every bwd_workers-th chunk
+  p->bwd_workers = int32_t(std::min<int64_t>(nc * bwd_chunks, ceildiv(2 * kSimds, bwd_tiles * bw.waves * bw.wc)));
+  // partial sums: dA [worker][C][S], dD and ddt_bias [worker * waves][C], dB and dC [tile][n][t][waves][2][4 sg]
   int64_t ws = 0;
   if (bwd_chunks > 1) ws += nc * bwd_chunks * (2 * state + d->d);
-  ws += int64_t(p->bwd_workers) * (state + 2 * waves * d->d);
-  ws += tiles * nc * d->t * 2 * sp;
+  ws += int64_t(p->bwd_workers) * (state + 2 * bw.waves * d->d);
+  ws += bwd_tiles * nc * d->t * bw.waves * 8 * bw.sg;
   p->info.backward_workspace_bytes = ws * 4;
   *out = p;
   return CC3D_OK;
@@ -353,6 +355,9 @@ extern "C" cc3d_status_t selective_scan_backward(cc3d_scan_plan_t p, const cc3d_
   c.require(!a->ddt_bias || a->dt_bias);
   c.workspace(a->workspace, a->workspace_bytes, p->info.backward_workspace_bytes);
   if (!c.ok()) return refuse(CC3D_ERR_INVALID_ARG);
+  if (d.t > 1)
+    for (const cc3d_rows_t* v : {&a->u, &a->dt, &a->b, &a->c, &a->z, &a->dy, &a->du, &a->ddt, &a->dz})
+      if (v->p && v->row > kMaxRow) return refuse(CC3D_ERR_UNSUPPORTED);
   return launched(cc3d::launch_scan_backward(*p, *a, stream));
 }
 

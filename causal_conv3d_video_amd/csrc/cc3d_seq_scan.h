@@ -22,7 +22,7 @@ struct ScanArgs {
   float* part_a;   // backward partial sums: [worker][C][S]
   float* part_d;   // [worker * waves][C]
   float* part_bias;
-  float* part_bc;  // [tile][n][t][2][waves * states of a wave]
+  float* part_bc;  // [tile][n][t][waves][2][states of a wave]
   int n, t, ch, s, groups, wide;  // wide: channels of a group
   int tiles_per_group, chunk, chunks, waves, workers;
   int softplus;

@@ -59,7 +59,7 @@ int main() {
             expect(!p, "no plan after a refusal");
             continue;
           }
-          expect(int64_t(p->chunk) * p->info.chunks >= t && int64_t(p->bwd_chunk) * p->info.backward_chunks >= t,
+          expect(int64_t(p->chunk) * p->info.chunks >= t && int64_t(cc3d::scan_bwd_shape(d).chunk) * p->info.backward_chunks >= t,
                  "chunks cover the tokens");
           expect(p->bwd_workers >= 1 && p->info.workspace_bytes >= 0 && p->info.backward_workspace_bytes > 0, "scan plan");
           // two halves of one projection are read and written in place of each other's columns
