@@ -71,6 +71,49 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Inputs of four tokens, as they are stored: those of the lane's channel, and
+// the lane's share of the rows of B (and C) that the wave spreads through LDS.
+template <class T, int NS, int ROWS>
+struct Feed {
+  static constexpr int kEach = (4 * NS * ROWS + 63) / 64;
+  T dt[4], x[4], z[4], bc[kEach];
+};
+
+// Loads the four tokens from tb on.  Tokens past the last valid one (te - 1)
+// and states past the last are read from there instead, never used: no
+// branch stands between the loads.
+template <class T, int NS, int ROWS>
+__device__ __forceinline__ void feed(Feed<T, NS, ROWS>& f, int tb, int te, const T* dt, int64_t dt_row, const T* x,
+                                     int64_t x_row, const T* z, int64_t z_row, const T* b, int64_t b_row, const T* c,
+                                     int64_t c_row, int states, int lane, int chan) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t t = min(tb + j, te - 1);
+    f.dt[j] = (dt + t * dt_row)[chan];
+    f.x[j] = (x + t * x_row)[chan];
+    f.z[j] = z ? (z + t * z_row)[chan] : T(0);
+  }
+#pragma unroll
+  for (int r = 0; r < Feed<T, NS, ROWS>::kEach; ++r) {
+    const int i = lane + 64 * r, which = ROWS == 2 ? i / (4 * NS) : 0;
+    const int64_t t = min(tb + i / NS % 4, te - 1);
+    const int s = min(i % NS, states - 1);
+    f.bc[r] = ROWS == 2 && which ? c[t * c_row + s] : b[t * b_row + s];
+  }
+}
+
+// The rows of B (and C) of four tokens into LDS, [ROWS][4][NS], zero past the
+// valid tokens and the last state.
+template <class T, int NS, int ROWS>
+__device__ __forceinline__ void spread_rows(const Feed<T, NS, ROWS>& f, float* box, int tb, int te, int states, int lane) {
+#pragma unroll
+  for (int r = 0; r < Feed<T, NS, ROWS>::kEach; ++r) {
+    const int i = lane + 64 * r;
+    if (4 * NS * ROWS % 64 == 0 || i < 4 * NS * ROWS)
+      box[i] = tb + i / NS % 4 < te && i % NS < states ? to_f32(f.bc[r]) : 0.f;
+  }
+}
+
 // What a chunk adds to the state, starting from zero: the forward recurrence
 //   h = exp(delta A) h + delta u B
 // or, REV, the gradient's from the chunk's last token back,
@@ -78,56 +121,58 @@ __device__ __forceinline__ void wave_fence() {
 // and the chunk's sum of delta, whose exponential is the whole chunk's decay.
 template <class T, int NS, bool REV>
 __global__ __launch_bounds__(64 * (cc3d::kScanMaxStates / NS)) void scan_carry(ScanArgs a) {
-  __shared__ __attribute__((aligned(16))) float box[cc3d::kScanMaxStates / NS][4 * NS];
+  __shared__ __attribute__((aligned(16))) float box_all[cc3d::kScanMaxStates / NS][4 * NS];
   const Place at(a);
+  float* box = box_all[at.wave];
   const int n = int(at.item / a.chunks), ch = int(at.item - int64_t(n) * a.chunks);
   const int t0 = ch * a.chunk, te = min(min(t0 + a.chunk, a.t), valid_tokens(a, n));
-  const int s0 = at.wave * NS;
+  const int s0 = at.wave * NS, states = min(a.s - s0, NS);
   const ScanRows& coef = REV ? a.c : a.b;
-  const T* cf = rows<T>(coef, n) + at.group * a.s;
-  const T* dt = rows<T>(a.dt, n) + at.chan;
-  const T* xin = rows<T>(REV ? a.dy : a.u, n) + at.chan;
-  const T* zin = REV && a.z.p ? rows<T>(a.z, n) + at.chan : nullptr;
+  const ScanRows& in = REV ? a.dy : a.u;
+  const T* cf = rows<T>(coef, n) + at.group * a.s + s0;
+  const T *dt = rows<T>(a.dt, n), *xin = rows<T>(in, n), *zin = REV && a.z.p ? rows<T>(a.z, n) : nullptr;
   const float bias = a.bias ? a.bias[at.chan] : 0.f;
   float h[NS], a2[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     h[i] = 0.f;
-    a2[i] = s0 + i < a.s ? a.a[int64_t(at.chan) * a.s + s0 + i] * kLog2e : 0.f;
+    a2[i] = i < states ? a.a[int64_t(at.chan) * a.s + s0 + i] * kLog2e : 0.f;
   }
   float total = 0.f;
   const int groups = te > t0 ? (te - t0 + 3) / 4 : 0;
-  for (int q = 0; q < groups; ++q) {
-    const int tb = t0 + 4 * (REV ? groups - 1 - q : q);
+  Feed<T, NS, 1> next;
+  auto fetch = [&](int q) {
+    feed(next, t0 + 4 * q, te, dt, a.dt.row, xin, in.row, zin, a.z.row, cf, coef.row, cf, coef.row, states, at.lane, at.chan);
+  };
+  if (groups) fetch(REV ? groups - 1 : 0);
+  for (int k = 0; k < groups; ++k) {
+    const int q = REV ? groups - 1 - k : k, tb = t0 + 4 * q;
     wave_fence();
-    for (int i = at.lane; i < 4 * NS; i += 64) {
-      const int t = tb + i / NS, s = s0 + i % NS;
-      box[at.wave][i] = t < te && s < a.s ? to_f32(cf[int64_t(t) * coef.row + s]) : 0.f;
-    }
+    spread_rows(next, box, tb, te, states, at.lane);
     float delta[4], x[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int t = tb + j;
-      delta[j] = x[j] = 0.f;
-      if (t < te) {
-        delta[j] = delta_of(a, to_f32(dt[int64_t(t) * a.dt.row]) + bias);
-        x[j] = to_f32(xin[int64_t(t) * (REV ? a.dy.row : a.u.row)]);
-        if (!REV) x[j] *= delta[j];
-        if (REV && zin) {
-          const float z = to_f32(zin[int64_t(t) * a.z.row]);
-          x[j] *= z * sigmoid_f32(z);
-        }
+      const bool valid = tb + j < te;
+      delta[j] = valid ? delta_of(a, to_f32(next.dt[j]) + bias) : 0.f;
+      x[j] = to_f32(next.x[j]);
+      if (!REV) x[j] *= delta[j];
+      if (REV && zin) {
+        const float z = to_f32(next.z[j]);
+        x[j] *= z * sigmoid_f32(z);
       }
+      x[j] = valid ? x[j] : 0.f;
       total += delta[j];
     }
     wave_fence();
+    if (k + 1 < groups) fetch(REV ? q - 1 : q + 1);
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj) {
       const int j = REV ? 3 - jj : jj;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        const float decay = __builtin_amdgcn_exp2f(delta[j] * a2[i]), add = x[j] * box[at.wave][j * NS + i];
-        h[i] = REV ? decay * (h[i] + add) : fmaf(decay, h[i], add);
+        const float decay = __builtin_amdgcn_exp2f(delta[j] * a2[i]);
+        if (REV) h[i] = decay * fmaf(x[j], box[j * NS + i], h[i]);
+        else h[i] = fmaf(decay, h[i], x[j] * box[j * NS + i]);
       }
     }
   }
@@ -136,7 +181,7 @@ __global__ __launch_bounds__(64 * (cc3d::kScanMaxStates / NS)) void scan_carry(S
   float* out = (REV ? a.gcarry : a.carry) + (at.item * a.s + s0) * channels + at.chan;
 #pragma unroll
   for (int i = 0; i < NS; ++i)
-    if (s0 + i < a.s) out[int64_t(i) * channels] = h[i];
+    if (i < states) out[int64_t(i) * channels] = h[i];
   if (!REV && at.wave == 0) a.sums[at.item * channels + at.chan] = total;
 }
 
@@ -159,17 +204,17 @@ __global__ __launch_bounds__(256) void scan_join(ScanArgs a) {
   float* carry = (REV ? a.gcarry : a.carry) + (int64_t(n) * a.chunks * a.s + s) * channels + chan;
   const float* sums = a.sums + int64_t(n) * a.chunks * channels + chan;
   const int64_t step = int64_t(a.s) * channels;
-  for (int c0 = 0; c0 < a.chunks; c0 += 8) {
-    float add[8], sum[8];
+  for (int c0 = 0; c0 < a.chunks; c0 += 16) {
+    float add[16], sum[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
       const int c = REV ? a.chunks - 1 - (c0 + i) : c0 + i;
       const bool in = c0 + i < a.chunks;
       add[i] = in ? carry[c * step] : 0.f;
       sum[i] = in ? sums[int64_t(c) * channels] : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
       const int c = REV ? a.chunks - 1 - (c0 + i) : c0 + i;
       if (c0 + i < a.chunks) carry[c * step] = h;
       h = fmaf(__builtin_amdgcn_exp2f(sum[i] * a2), h, add[i]);

@@ -20,64 +20,60 @@ namespace {
 template <class T, int NS, bool MULTI>
 __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void scan_fwd(ScanArgs a) {
   constexpr int kWaves = MULTI ? cc3d::kScanMaxStates / NS : 1;
-  __shared__ __attribute__((aligned(16))) float box[kWaves][2][4 * NS];
+  __shared__ __attribute__((aligned(16))) float box_all[kWaves][2 * 4 * NS];
   __shared__ float part[MULTI ? 2 : 1][kWaves][MULTI ? 4 : 1][64];
   const Place at(a);
+  float* box = box_all[at.wave];
   const int n = int(at.item / a.chunks), ch = int(at.item - int64_t(n) * a.chunks);
   const int t0 = ch * a.chunk, t1 = min(t0 + a.chunk, a.t), te = min(t1, valid_tokens(a, n));
-  const int s0 = at.wave * NS;
+  const int s0 = at.wave * NS, states = min(a.s - s0, NS);
   const int channels = a.groups * a.wide;
-  const T* bp = rows<T>(a.b, n) + at.group * a.s;
-  const T* cp = rows<T>(a.c, n) + at.group * a.s;
-  const T* dt = rows<T>(a.dt, n) + at.chan;
-  const T* u = rows<T>(a.u, n) + at.chan;
-  const T* z = a.z.p ? rows<T>(a.z, n) + at.chan : nullptr;
-  T* y = out_rows<T>(a.y, n) + at.chan;
+  const T *bp = rows<T>(a.b, n) + at.group * a.s + s0, *cp = rows<T>(a.c, n) + at.group * a.s + s0;
+  const T *dt = rows<T>(a.dt, n), *u = rows<T>(a.u, n), *z = a.z.p ? rows<T>(a.z, n) : nullptr;
+  T* y = out_rows<T>(a.y, n);
   const float bias = a.bias ? a.bias[at.chan] : 0.f, skip = a.d ? a.d[at.chan] : 0.f;
   const int64_t state_at = (int64_t(n) * channels + at.chan) * a.s + s0;
 
   float h[NS], a2[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    const bool in = s0 + i < a.s;
-    a2[i] = in ? a.a[int64_t(at.chan) * a.s + s0 + i] * kLog2e : 0.f;
+    a2[i] = i < states ? a.a[int64_t(at.chan) * a.s + s0 + i] * kLog2e : 0.f;
     h[i] = 0.f;
-    if (in) {
+    if (i < states) {
       if (a.chunks > 1) h[i] = a.carry[(at.item * a.s + s0 + i) * channels + at.chan];
       else if (a.h_in) h[i] = a.h_in[state_at + i];
     }
   }
 
+  Feed<T, NS, 2> next;
+  auto fetch = [&](int tb) {
+    feed(next, tb, te, dt, a.dt.row, u, a.u.row, z, a.z.row, bp, a.b.row, cp, a.c.row, states, at.lane, at.chan);
+  };
+  if (t0 < te) fetch(t0);
   int turn = 0;
   for (int tb = t0; tb < te; tb += 4) {
     wave_fence();
-    for (int i = at.lane; i < 4 * NS; i += 64) {
-      const int t = tb + i / NS, s = s0 + i % NS;
-      const bool in = t < te && s < a.s;
-      box[at.wave][0][i] = in ? to_f32(bp[int64_t(t) * a.b.row + s]) : 0.f;
-      box[at.wave][1][i] = in ? to_f32(cp[int64_t(t) * a.c.row + s]) : 0.f;
-    }
-    float delta[4], du[4], uu[4];
+    spread_rows(next, box, tb, te, states, at.lane);
+    float delta[4], uu[4];
+    T zz[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int t = tb + j;
-      delta[j] = uu[j] = 0.f;
-      if (t < te) {
-        delta[j] = delta_of(a, to_f32(dt[int64_t(t) * a.dt.row]) + bias);
-        uu[j] = to_f32(u[int64_t(t) * a.u.row]);
-      }
-      du[j] = delta[j] * uu[j];
+      delta[j] = tb + j < te ? delta_of(a, to_f32(next.dt[j]) + bias) : 0.f;
+      uu[j] = tb + j < te ? to_f32(next.x[j]) : 0.f;
+      zz[j] = next.z[j];
     }
     wave_fence();
+    if (tb + 4 < te) fetch(tb + 4);
     float sum[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      const float du = delta[j] * uu[j];
       sum[j] = 0.f;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const float decay = __builtin_amdgcn_exp2f(delta[j] * a2[i]);
-        h[i] = fmaf(decay, h[i], du[j] * box[at.wave][0][j * NS + i]);
-        sum[j] = fmaf(h[i], box[at.wave][1][j * NS + i], sum[j]);
+        h[i] = fmaf(decay, h[i], du * box[j * NS + i]);
+        sum[j] = fmaf(h[i], box[(4 + j) * NS + i], sum[j]);
       }
     }
     if (MULTI) {
@@ -96,22 +92,106 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
       if (t < te && at.on) {
         float v = fmaf(skip, uu[j], sum[j]);
         if (z) {
-          const float zz = to_f32(z[int64_t(t) * a.z.row]);
-          v *= zz * sigmoid_f32(zz);
+          const float g = to_f32(zz[j]);
+          v *= g * sigmoid_f32(g);
         }
-        y[int64_t(t) * a.y.row] = from_f32<T>(v);
+        (y + int64_t(t) * a.y.row)[at.chan] = from_f32<T>(v);
       }
     }
     turn ^= 1;
   }
   if (!at.on) return;
   if (at.wave == 0)
-    for (int t = max(t0, te); t < t1; ++t) y[int64_t(t) * a.y.row] = from_f32<T>(0.f);
+    for (int t = max(t0, te); t < t1; ++t) (y + int64_t(t) * a.y.row)[at.chan] = from_f32<T>(0.f);
   if (a.h_out && ch == a.chunks - 1) {
 #pragma unroll
     for (int i = 0; i < NS; ++i)
-      if (s0 + i < a.s) a.h_out[state_at + i] = h[i];
+      if (i < states) a.h_out[state_at + i] = h[i];
   }
+}
+
+// One token: the states are read and written once and little else is moved.
+// A lane holds four states of one channel, so a channel's states are one
+// stretch of memory across LP lanes, and its sum over states LP lanes wide.
+template <class T, int LP, bool VEC>
+__global__ __launch_bounds__(256) void scan_step(ScanArgs a) {
+  const int64_t id = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LP;
+  const int part = threadIdx.x % LP;
+  const int channels = a.groups * a.wide;
+  const bool on = id < int64_t(a.n) * channels;  // the same for a channel's LP lanes; all take part in the sum
+  const int n = on ? int(id / channels) : 0, chan = on ? int(id - int64_t(n) * channels) : 0;
+  const int s0 = part * 4, left = a.s - s0;  // may be negative
+  const int64_t state_at = (int64_t(n) * channels + chan) * a.s + s0;
+  const int group = chan / a.wide;
+  const bool valid = valid_tokens(a, n) > 0;
+  float h[4] = {}, sum = 0.f, uu = 0.f;
+  if (a.h_in && left > 0) {
+    if constexpr (VEC) {
+      const f32x4_s v = *reinterpret_cast<const f32x4_s*>(a.h_in + state_at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) h[i] = a.h_in[state_at + i];
+    }
+  }
+  if (valid) {
+    const float bias = a.bias ? a.bias[chan] : 0.f;
+    const float delta = delta_of(a, to_f32(rows<T>(a.dt, n)[chan]) + bias);
+    uu = to_f32(rows<T>(a.u, n)[chan]);
+    const float du = delta * uu;
+    const T *b = rows<T>(a.b, n) + group * a.s + s0, *c = rows<T>(a.c, n) + group * a.s + s0;
+    const float* aa = a.a + int64_t(chan) * a.s + s0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) {
+        h[i] = fmaf(__builtin_amdgcn_exp2f(delta * (aa[i] * kLog2e)), h[i], du * to_f32(b[i]));
+        sum = fmaf(h[i], to_f32(c[i]), sum);
+      }
+  }
+  sum = group_sum<LP>(sum);
+  if (!on) return;
+  if (a.h_out && left > 0) {
+    if constexpr (VEC) {
+      *reinterpret_cast<f32x4_s*>(a.h_out + state_at) = f32x4_s{h[0], h[1], h[2], h[3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) a.h_out[state_at + i] = h[i];
+    }
+  }
+  if (part == 0) {
+    float v = 0.f;
+    if (valid) {
+      v = a.d ? fmaf(a.d[chan], uu, sum) : sum;
+      if (a.z.p) {
+        const float g = to_f32(rows<T>(a.z, n)[chan]);
+        v *= g * sigmoid_f32(g);
+      }
+    }
+    out_rows<T>(a.y, n)[chan] = from_f32<T>(v);
+  }
+}
+
+template <class T, int LP>
+int run_step(const ScanArgs& a, hipStream_t s) {
+  const int64_t threads = int64_t(a.n) * a.groups * a.wide * LP;
+  const unsigned blocks = unsigned((threads + 255) / 256);
+  if (a.s % 4 == 0 && reinterpret_cast<uintptr_t>(a.h_in) % 16 == 0 && reinterpret_cast<uintptr_t>(a.h_out) % 16 == 0)
+    scan_step<T, LP, true><<<blocks, 256, 0, s>>>(a);
+  else
+    scan_step<T, LP, false><<<blocks, 256, 0, s>>>(a);
+  return int(hipGetLastError());
+}
+
+template <class T>
+int pick_step(const ScanArgs& a, hipStream_t s) {
+  if (a.s <= 4) return run_step<T, 1>(a, s);
+  if (a.s <= 8) return run_step<T, 2>(a, s);
+  if (a.s <= 16) return run_step<T, 4>(a, s);
+  if (a.s <= 32) return run_step<T, 8>(a, s);
+  return run_step<T, 16>(a, s);
 }
 
 template <class T, int NS>
@@ -134,6 +214,7 @@ int run_scan(const cc3d_scan_plan& p, ScanArgs& a, hipStream_t s) {
 
 template <class T>
 int pick_states(const cc3d_scan_plan& p, ScanArgs& a, hipStream_t s) {
+  if (a.t == 1) return pick_step<T>(a, s);
   switch (cc3d::scan_fwd_ns(p.d)) {
     case 4: return run_scan<T, 4>(p, a, s);
     case 8: return run_scan<T, 8>(p, a, s);
