@@ -42,8 +42,8 @@ constexpr int64_t kSimds = 1024;
 // Workgroups of one launch, and the addresses a view may span.
 constexpr int64_t kMaxBlocks = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSpan = int64_t(1) << 46;
-// Elements between two tokens of the scan's backward pass: offsets inside a
-// chunk of 64 tokens are 32 bits.
+// Elements between two tokens of the scan: offsets inside a chunk of 64
+// tokens are 32 bits.
 constexpr int64_t kMaxRow = (int64_t(1) << 25) - 1;
 // Tokens of one call: token counters are 32 bits and run a chunk past the end.
 constexpr int32_t kMaxTokens = 1 << 30;
@@ -318,6 +318,12 @@ void scan_inputs(Check& c, const cc3d_scan_desc_t& d, const cc3d_scan_args_t* a)
   c.dense(a->h_in, int64_t(d.n) * d.d * d.states * 4, 4, false, false);
   c.dense(a->lengths, int64_t(d.n) * 4, 4, false, false);
 }
+
+bool far_rows(const cc3d_scan_desc_t& d, std::initializer_list<const cc3d_rows_t*> views) {
+  for (const cc3d_rows_t* v : views)
+    if (d.t > 1 && v->p && v->row > kMaxRow) return true;
+  return false;
+}
 }  // namespace
 
 extern "C" cc3d_status_t selective_scan_forward(cc3d_scan_plan_t p, const cc3d_scan_args_t* a, void* stream) {
@@ -330,6 +336,7 @@ extern "C" cc3d_status_t selective_scan_forward(cc3d_scan_plan_t p, const cc3d_s
   c.same_allowed(a->h_in, a->h_out);
   c.workspace(a->workspace, a->workspace_bytes, p->info.workspace_bytes);
   if (!c.ok()) return refuse(CC3D_ERR_INVALID_ARG);
+  if (far_rows(d, {&a->u, &a->dt, &a->b, &a->c, &a->z, &a->y})) return refuse(CC3D_ERR_UNSUPPORTED);
   return launched(cc3d::launch_scan_forward(*p, *a, stream));
 }
 
@@ -355,9 +362,7 @@ extern "C" cc3d_status_t selective_scan_backward(cc3d_scan_plan_t p, const cc3d_
   c.require(!a->ddt_bias || a->dt_bias);
   c.workspace(a->workspace, a->workspace_bytes, p->info.backward_workspace_bytes);
   if (!c.ok()) return refuse(CC3D_ERR_INVALID_ARG);
-  if (d.t > 1)
-    for (const cc3d_rows_t* v : {&a->u, &a->dt, &a->b, &a->c, &a->z, &a->dy, &a->du, &a->ddt, &a->dz})
-      if (v->p && v->row > kMaxRow) return refuse(CC3D_ERR_UNSUPPORTED);
+  if (far_rows(d, {&a->u, &a->dt, &a->b, &a->c, &a->z, &a->dy, &a->du, &a->ddt, &a->dz})) return refuse(CC3D_ERR_UNSUPPORTED);
   return launched(cc3d::launch_scan_backward(*p, *a, stream));
 }
 

@@ -31,6 +31,7 @@ struct ScanArgs {
 // A wave holds 64 channels of one group; blockIdx.x = tile + tiles * item.
 struct Place {
   int lane, wave, tile, group, chan;
+  int first, live;  // the wave's first channel and how many it has
   bool on;
   int64_t item;
   __device__ __forceinline__ Place(const ScanArgs& a) {
@@ -41,8 +42,12 @@ struct Place {
     item = blockIdx.x / tiles;
     group = tile / a.tiles_per_group;
     const int in_group = (tile - group * a.tiles_per_group) * 64 + lane;
+    // lanes past the group's last channel compute that one too: what they
+    // store is the same value to the same place
     on = in_group < a.wide;
-    chan = group * a.wide + (on ? in_group : 0);
+    chan = group * a.wide + min(in_group, a.wide - 1);
+    first = group * a.wide + in_group - lane;
+    live = min(a.wide - (in_group - lane), 64);
   }
 };
 
@@ -71,6 +76,79 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// A wave's states [64 channels][NS] of a tensor [C][S], each lane its channel:
+// read and written as whole stretches of memory and turned through LDS (rows
+// padded by 16 bytes), not as 64 rows at once.
+template <int NS>
+struct StateBox {
+  static constexpr int kRow = NS + 4, kSize = 64 * kRow;
+};
+
+template <int NS>
+__device__ __forceinline__ void load_states(const float* p, int row, int states, int live, int lane, float* box, float (&v)[NS]) {
+  using B = StateBox<NS>;
+  wave_fence();
+  if (row % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+#pragma unroll
+    for (int k = 0; k < NS / 4; ++k) {
+      const int i = lane + 64 * k, c = i / (NS / 4), s = i % (NS / 4) * 4;
+      f32x4_s x{0.f, 0.f, 0.f, 0.f};
+      if (c < live && s < states) x = *reinterpret_cast<const f32x4_s*>(p + int64_t(c) * row + s);
+      *reinterpret_cast<f32x4_s*>(box + c * B::kRow + s) = x;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      const int i = lane + 64 * k, c = i / NS, s = i % NS;
+      box[c * B::kRow + s] = c < live && s < states ? p[int64_t(c) * row + s] : 0.f;
+    }
+  }
+  wave_fence();
+#pragma unroll
+  for (int i = 0; i < NS; ++i) v[i] = box[min(lane, live - 1) * B::kRow + i];
+  wave_fence();
+}
+
+template <int NS>
+__device__ __forceinline__ void store_states(float* p, int row, int states, int live, int lane, float* box, const float (&v)[NS]) {
+  using B = StateBox<NS>;
+  wave_fence();
+#pragma unroll
+  for (int i = 0; i < NS; ++i) box[lane * B::kRow + i] = v[i];
+  wave_fence();
+  if (row % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+#pragma unroll
+    for (int k = 0; k < NS / 4; ++k) {
+      const int i = lane + 64 * k, c = i / (NS / 4), s = i % (NS / 4) * 4;
+      if (c < live && s < states)
+        *reinterpret_cast<f32x4_s*>(p + int64_t(c) * row + s) = *reinterpret_cast<const f32x4_s*>(box + c * B::kRow + s);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      const int i = lane + 64 * k, c = i / NS, s = i % NS;
+      if (c < live && s < states) p[int64_t(c) * row + s] = box[c * B::kRow + s];
+    }
+  }
+  wave_fence();
+}
+
+// One stream of tokens of a lane's channel: the wave's address of token `t0`
+// of a chunk, moved on by whole groups of four tokens, with the lane's four
+// tokens at 32-bit offsets behind it.
+template <class T>
+struct Stream {
+  T* p;
+  int64_t row;
+  unsigned off[4];
+  __device__ __forceinline__ Stream(const ScanRows& v, int n, int t0, int chan)
+      : p(v.p ? static_cast<T*>(v.p) + int64_t(n) * v.batch + int64_t(t0) * v.row : nullptr), row(v.row) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) off[j] = unsigned(j) * unsigned(v.row) + unsigned(chan);
+  }
+  __device__ __forceinline__ void move(int groups) { p += int64_t(groups) * 4 * row; }
+};
+
 // Inputs of four tokens, as they are stored: those of the lane's channel, and
 // the lane's share of the rows of B (and C) that the wave spreads through LDS.
 template <class T, int NS, int ROWS>
@@ -79,26 +157,24 @@ struct Feed {
   T dt[4], x[4], z[4], bc[kEach];
 };
 
-// Loads the four tokens from tb on.  Tokens past the last valid one (te - 1)
-// and states past the last are read from there instead, never used: no
-// branch stands between the loads.
+// Loads the four tokens at the streams' places, `left` of them valid (at
+// least one).  For those past the valid ones the first is read, for states
+// past the last the last: never used, and no branch between the loads.
 template <class T, int NS, int ROWS>
-__device__ __forceinline__ void feed(Feed<T, NS, ROWS>& f, int tb, int te, const T* dt, int64_t dt_row, const T* x,
-                                     int64_t x_row, const T* z, int64_t z_row, const T* b, int64_t b_row, const T* c,
-                                     int64_t c_row, int states, int lane, int chan) {
+__device__ __forceinline__ void feed(Feed<T, NS, ROWS>& f, int left, const Stream<T>& dt, const Stream<T>& x,
+                                     const Stream<T>& z, const Stream<T>& b, const Stream<T>& c, int states, int lane) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int64_t t = min(tb + j, te - 1);
-    f.dt[j] = (dt + t * dt_row)[chan];
-    f.x[j] = (x + t * x_row)[chan];
-    f.z[j] = z ? (z + t * z_row)[chan] : T(0);
+    const int k = j < left ? j : 0;
+    f.dt[j] = dt.p[dt.off[k]];
+    f.x[j] = x.p[x.off[k]];
+    f.z[j] = z.p ? z.p[z.off[k]] : T(0);
   }
 #pragma unroll
   for (int r = 0; r < Feed<T, NS, ROWS>::kEach; ++r) {
     const int i = lane + 64 * r, which = ROWS == 2 ? i / (4 * NS) : 0;
-    const int64_t t = min(tb + i / NS % 4, te - 1);
-    const int s = min(i % NS, states - 1);
-    f.bc[r] = ROWS == 2 && which ? c[t * c_row + s] : b[t * b_row + s];
+    const unsigned t = unsigned(min(i / NS % 4, left - 1)), s = unsigned(min(i % NS, states - 1));
+    f.bc[r] = ROWS == 2 && which ? c.p[t * unsigned(c.row) + s] : b.p[t * unsigned(b.row) + s];
   }
 }
 
@@ -121,50 +197,55 @@ __device__ __forceinline__ void spread_rows(const Feed<T, NS, ROWS>& f, float* b
 // and the chunk's sum of delta, whose exponential is the whole chunk's decay.
 template <class T, int NS, bool REV>
 __global__ __launch_bounds__(64 * (cc3d::kScanMaxStates / NS)) void scan_carry(ScanArgs a) {
-  __shared__ __attribute__((aligned(16))) float box_all[cc3d::kScanMaxStates / NS][4 * NS];
+  __shared__ __attribute__((aligned(16))) float box_all[cc3d::kScanMaxStates / NS][StateBox<NS>::kSize];
   const Place at(a);
   float* box = box_all[at.wave];
   const int n = int(at.item / a.chunks), ch = int(at.item - int64_t(n) * a.chunks);
   const int t0 = ch * a.chunk, te = min(min(t0 + a.chunk, a.t), valid_tokens(a, n));
   const int s0 = at.wave * NS, states = min(a.s - s0, NS);
-  const ScanRows& coef = REV ? a.c : a.b;
-  const ScanRows& in = REV ? a.dy : a.u;
-  const T* cf = rows<T>(coef, n) + at.group * a.s + s0;
-  const T *dt = rows<T>(a.dt, n), *xin = rows<T>(in, n), *zin = REV && a.z.p ? rows<T>(a.z, n) : nullptr;
   const float bias = a.bias ? a.bias[at.chan] : 0.f;
   float h[NS], a2[NS];
+  load_states<NS>(a.a + int64_t(at.first) * a.s + s0, a.s, states, at.live, at.lane, box, a2);
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     h[i] = 0.f;
-    a2[i] = i < states ? a.a[int64_t(at.chan) * a.s + s0 + i] * kLog2e : 0.f;
+    a2[i] *= kLog2e;
   }
   float total = 0.f;
-  const int groups = te > t0 ? (te - t0 + 3) / 4 : 0;
+  const int groups = te > t0 ? (te - t0 + 3) / 4 : 0, step = REV ? -1 : 1;
+  const int begin = REV ? groups - 1 : 0;
+  Stream<T> dt(a.dt, n, t0 + 4 * begin, at.chan), x_in(REV ? a.dy : a.u, n, t0 + 4 * begin, at.chan),
+      z_in(REV ? a.z : ScanRows{}, n, t0 + 4 * begin, at.chan), cf(REV ? a.c : a.b, n, t0 + 4 * begin, 0);
+  cf.p += at.group * a.s + s0;
   Feed<T, NS, 1> next;
-  auto fetch = [&](int q) {
-    feed(next, t0 + 4 * q, te, dt, a.dt.row, xin, in.row, zin, a.z.row, cf, coef.row, cf, coef.row, states, at.lane, at.chan);
-  };
-  if (groups) fetch(REV ? groups - 1 : 0);
+  if (groups) feed(next, te - t0 - 4 * begin, dt, x_in, z_in, cf, cf, states, at.lane);
   for (int k = 0; k < groups; ++k) {
-    const int q = REV ? groups - 1 - k : k, tb = t0 + 4 * q;
+    const int tb = t0 + 4 * (REV ? groups - 1 - k : k);
     wave_fence();
     spread_rows(next, box, tb, te, states, at.lane);
     float delta[4], x[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bool valid = tb + j < te;
-      delta[j] = valid ? delta_of(a, to_f32(next.dt[j]) + bias) : 0.f;
-      x[j] = to_f32(next.x[j]);
+      delta[j] = tb + j < te ? delta_of(a, to_f32(next.dt[j]) + bias) : 0.f;
+      x[j] = tb + j < te ? to_f32(next.x[j]) : 0.f;
       if (!REV) x[j] *= delta[j];
-      if (REV && zin) {
-        const float z = to_f32(next.z[j]);
-        x[j] *= z * sigmoid_f32(z);
-      }
-      x[j] = valid ? x[j] : 0.f;
       total += delta[j];
     }
+    if (REV && z_in.p) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float z = tb + j < te ? to_f32(next.z[j]) : 0.f;
+        x[j] *= z * sigmoid_f32(z);
+      }
+    }
     wave_fence();
-    if (k + 1 < groups) fetch(REV ? q - 1 : q + 1);
+    if (k + 1 < groups) {
+      dt.move(step);
+      x_in.move(step);
+      z_in.move(z_in.p ? step : 0);
+      cf.move(step);
+      feed(next, te - tb - 4 * step, dt, x_in, z_in, cf, cf, states, at.lane);
+    }
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj) {
       const int j = REV ? 3 - jj : jj;
@@ -176,7 +257,6 @@ __global__ __launch_bounds__(64 * (cc3d::kScanMaxStates / NS)) void scan_carry(S
       }
     }
   }
-  if (!at.on) return;
   const int channels = a.groups * a.wide;
   float* out = (REV ? a.gcarry : a.carry) + (at.item * a.s + s0) * channels + at.chan;
 #pragma unroll

@@ -20,7 +20,7 @@ namespace {
 template <class T, int NS, bool MULTI>
 __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void scan_fwd(ScanArgs a) {
   constexpr int kWaves = MULTI ? cc3d::kScanMaxStates / NS : 1;
-  __shared__ __attribute__((aligned(16))) float box_all[kWaves][2 * 4 * NS];
+  __shared__ __attribute__((aligned(16))) float box_all[kWaves][StateBox<NS>::kSize];
   __shared__ float part[MULTI ? 2 : 1][kWaves][MULTI ? 4 : 1][64];
   const Place at(a);
   float* box = box_all[at.wave];
@@ -28,28 +28,28 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
   const int t0 = ch * a.chunk, t1 = min(t0 + a.chunk, a.t), te = min(t1, valid_tokens(a, n));
   const int s0 = at.wave * NS, states = min(a.s - s0, NS);
   const int channels = a.groups * a.wide;
-  const T *bp = rows<T>(a.b, n) + at.group * a.s + s0, *cp = rows<T>(a.c, n) + at.group * a.s + s0;
-  const T *dt = rows<T>(a.dt, n), *u = rows<T>(a.u, n), *z = a.z.p ? rows<T>(a.z, n) : nullptr;
-  T* y = out_rows<T>(a.y, n);
   const float bias = a.bias ? a.bias[at.chan] : 0.f, skip = a.d ? a.d[at.chan] : 0.f;
-  const int64_t state_at = (int64_t(n) * channels + at.chan) * a.s + s0;
+  const int64_t state_at = (int64_t(n) * channels + at.first) * a.s + s0;
 
-  float h[NS], a2[NS];
+  Stream<T> dt(a.dt, n, t0, at.chan), u(a.u, n, t0, at.chan), z(a.z, n, t0, at.chan), y(a.y, n, t0, at.chan);
+  Stream<T> bs(a.b, n, t0, 0), cs(a.c, n, t0, 0);
+  bs.p += at.group * a.s + s0;
+  cs.p += at.group * a.s + s0;
+  Feed<T, NS, 2> next;
+  if (t0 < te) feed(next, te - t0, dt, u, z, bs, cs, states, at.lane);
+
+  float h[NS] = {}, a2[NS];
+  load_states<NS>(a.a + int64_t(at.first) * a.s + s0, a.s, states, at.live, at.lane, box, a2);
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    a2[i] = i < states ? a.a[int64_t(at.chan) * a.s + s0 + i] * kLog2e : 0.f;
-    h[i] = 0.f;
-    if (i < states) {
-      if (a.chunks > 1) h[i] = a.carry[(at.item * a.s + s0 + i) * channels + at.chan];
-      else if (a.h_in) h[i] = a.h_in[state_at + i];
-    }
+  for (int i = 0; i < NS; ++i) a2[i] *= kLog2e;
+  if (a.chunks > 1) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (i < states) h[i] = a.carry[(at.item * a.s + s0 + i) * channels + at.chan];
+  } else if (a.h_in) {
+    load_states<NS>(a.h_in + state_at, a.s, states, at.live, at.lane, box, h);
   }
 
-  Feed<T, NS, 2> next;
-  auto fetch = [&](int tb) {
-    feed(next, tb, te, dt, a.dt.row, u, a.u.row, z, a.z.row, bp, a.b.row, cp, a.c.row, states, at.lane, at.chan);
-  };
-  if (t0 < te) fetch(t0);
   int turn = 0;
   for (int tb = t0; tb < te; tb += 4) {
     wave_fence();
@@ -63,7 +63,14 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
       zz[j] = next.z[j];
     }
     wave_fence();
-    if (tb + 4 < te) fetch(tb + 4);
+    if (tb + 4 < te) {
+      dt.move(1);
+      u.move(1);
+      z.move(z.p ? 1 : 0);
+      bs.move(1);
+      cs.move(1);
+      feed(next, te - tb - 4, dt, u, z, bs, cs, states, at.lane);
+    }
     float sum[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -80,75 +87,95 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
 #pragma unroll
       for (int j = 0; j < 4; ++j) part[turn][at.wave][j][at.lane] = sum[j];
       __syncthreads();
-    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (MULTI && j % a.waves != at.wave) continue;
-      if (MULTI) {
+      for (int j = 0; j < 4; ++j) {
         sum[j] = 0.f;
-        for (int w = 0; w < a.waves; ++w) sum[j] += part[turn][w][j][at.lane];
+        if (j % a.waves == at.wave)
+          for (int w = 0; w < a.waves; ++w) sum[j] += part[turn][w][j][at.lane];
       }
-      const int t = tb + j;
-      if (t < te && at.on) {
-        float v = fmaf(skip, uu[j], sum[j]);
-        if (z) {
-          const float g = to_f32(zz[j]);
-          v *= g * sigmoid_f32(g);
-        }
-        (y + int64_t(t) * a.y.row)[at.chan] = from_f32<T>(v);
+      turn ^= 1;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = fmaf(skip, uu[j], sum[j]);
+    if (z.p) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float g = to_f32(zz[j]);
+        sum[j] *= g * sigmoid_f32(g);
       }
     }
-    turn ^= 1;
-  }
-  if (!at.on) return;
-  if (at.wave == 0)
-    for (int t = max(t0, te); t < t1; ++t) (y + int64_t(t) * a.y.row)[at.chan] = from_f32<T>(0.f);
-  if (a.h_out && ch == a.chunks - 1) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-      if (i < states) a.h_out[state_at + i] = h[i];
+    for (int j = 0; j < 4; ++j)
+      if (tb + j < te && (!MULTI || j % a.waves == at.wave)) y.p[y.off[j]] = from_f32<T>(sum[j]);
+    y.move(1);
   }
+  if (at.wave == 0) {
+    T* out = out_rows<T>(a.y, n) + at.chan;
+    for (int t = max(t0, te); t < t1; ++t) out[int64_t(t) * a.y.row] = from_f32<T>(0.f);
+  }
+  if (a.h_out && ch == a.chunks - 1) store_states<NS>(a.h_out + state_at, a.s, states, at.live, at.lane, box, h);
 }
 
 // One token: the states are read and written once and little else is moved.
 // A lane holds four states of one channel, so a channel's states are one
 // stretch of memory across LP lanes, and its sum over states LP lanes wide.
+// VEC: states and rows of B and C are aligned to four.
 template <class T, int LP, bool VEC>
-__global__ __launch_bounds__(256) void scan_step(ScanArgs a) {
-  const int64_t id = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LP;
+__global__ __launch_bounds__(256) void scan_step(ScanArgs a, unsigned per_sequence) {
+  const unsigned n = blockIdx.x / per_sequence;
+  const int at = int((blockIdx.x - n * per_sequence) * (256 / LP) + threadIdx.x / LP);
   const int part = threadIdx.x % LP;
   const int channels = a.groups * a.wide;
-  const bool on = id < int64_t(a.n) * channels;  // the same for a channel's LP lanes; all take part in the sum
-  const int n = on ? int(id / channels) : 0, chan = on ? int(id - int64_t(n) * channels) : 0;
+  const bool on = at < channels;  // the same for a channel's LP lanes; all take part in the sum
+  const int chan = on ? at : channels - 1;
   const int s0 = part * 4, left = a.s - s0;  // may be negative
   const int64_t state_at = (int64_t(n) * channels + chan) * a.s + s0;
-  const int group = chan / a.wide;
-  const bool valid = valid_tokens(a, n) > 0;
+  const int group = a.groups == 1 ? 0 : chan / a.wide;
   float h[4] = {}, sum = 0.f, uu = 0.f;
-  if (a.h_in && left > 0) {
+  const bool valid = valid_tokens(a, int(n)) > 0;
+  if (left > 0) {
+    const T *b = rows<T>(a.b, int(n)) + group * a.s + s0, *c = rows<T>(a.c, int(n)) + group * a.s + s0;
+    const float* aa = a.a + int64_t(chan) * a.s + s0;
+    float a4[4] = {}, b4[4] = {}, c4[4] = {};
     if constexpr (VEC) {
-      const f32x4_s v = *reinterpret_cast<const f32x4_s*>(a.h_in + state_at);
+      using U = std::conditional_t<sizeof(T) == 4, f32x4_s, unsigned long long>;
+      const f32x4_s va = *reinterpret_cast<const f32x4_s*>(aa);
+      const U vb = *reinterpret_cast<const U*>(b), vc = *reinterpret_cast<const U*>(c);
+      f32x4_s vh{0.f, 0.f, 0.f, 0.f};
+      if (a.h_in) vh = *reinterpret_cast<const f32x4_s*>(a.h_in + state_at);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = v[i];
+      for (int i = 0; i < 4; ++i) {
+        h[i] = vh[i];
+        a4[i] = va[i];
+        if constexpr (sizeof(T) == 4) {
+          b4[i] = vb[i];
+          c4[i] = vc[i];
+        } else {
+          b4[i] = to_f32(bf16_s(vb >> (16 * i)));
+          c4[i] = to_f32(bf16_s(vc >> (16 * i)));
+        }
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i < left) h[i] = a.h_in[state_at + i];
+        if (i < left) {
+          if (a.h_in) h[i] = a.h_in[state_at + i];
+          a4[i] = aa[i];
+          b4[i] = to_f32(b[i]);
+          c4[i] = to_f32(c[i]);
+        }
     }
-  }
-  if (valid) {
-    const float bias = a.bias ? a.bias[chan] : 0.f;
-    const float delta = delta_of(a, to_f32(rows<T>(a.dt, n)[chan]) + bias);
-    uu = to_f32(rows<T>(a.u, n)[chan]);
-    const float du = delta * uu;
-    const T *b = rows<T>(a.b, n) + group * a.s + s0, *c = rows<T>(a.c, n) + group * a.s + s0;
-    const float* aa = a.a + int64_t(chan) * a.s + s0;
+    if (valid) {
+      const float delta = delta_of(a, to_f32(rows<T>(a.dt, int(n))[chan]) + (a.bias ? a.bias[chan] : 0.f));
+      uu = to_f32(rows<T>(a.u, int(n))[chan]);
+      const float du = delta * uu;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) {
-        h[i] = fmaf(__builtin_amdgcn_exp2f(delta * (aa[i] * kLog2e)), h[i], du * to_f32(b[i]));
-        sum = fmaf(h[i], to_f32(c[i]), sum);
-      }
+      for (int i = 0; i < 4; ++i)
+        if (VEC || i < left) {
+          h[i] = fmaf(__builtin_amdgcn_exp2f(delta * (a4[i] * kLog2e)), h[i], du * b4[i]);
+          sum = fmaf(h[i], c4[i], sum);
+        }
+    }
   }
   sum = group_sum<LP>(sum);
   if (!on) return;
@@ -166,22 +193,25 @@ __global__ __launch_bounds__(256) void scan_step(ScanArgs a) {
     if (valid) {
       v = a.d ? fmaf(a.d[chan], uu, sum) : sum;
       if (a.z.p) {
-        const float g = to_f32(rows<T>(a.z, n)[chan]);
+        const float g = to_f32(rows<T>(a.z, int(n))[chan]);
         v *= g * sigmoid_f32(g);
       }
     }
-    out_rows<T>(a.y, n)[chan] = from_f32<T>(v);
+    out_rows<T>(a.y, int(n))[chan] = from_f32<T>(v);
   }
 }
 
 template <class T, int LP>
 int run_step(const ScanArgs& a, hipStream_t s) {
-  const int64_t threads = int64_t(a.n) * a.groups * a.wide * LP;
-  const unsigned blocks = unsigned((threads + 255) / 256);
-  if (a.s % 4 == 0 && reinterpret_cast<uintptr_t>(a.h_in) % 16 == 0 && reinterpret_cast<uintptr_t>(a.h_out) % 16 == 0)
-    scan_step<T, LP, true><<<blocks, 256, 0, s>>>(a);
-  else
-    scan_step<T, LP, false><<<blocks, 256, 0, s>>>(a);
+  const unsigned per_sequence = unsigned((int64_t(a.groups) * a.wide * LP + 255) / 256);
+  const unsigned blocks = per_sequence * unsigned(a.n);
+  bool vec = a.s % 4 == 0;
+  for (const void* p : {static_cast<const void*>(a.a), static_cast<const void*>(a.h_in), static_cast<const void*>(a.h_out)})
+    vec = vec && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+  for (const ScanRows* v : {&a.b, &a.c})
+    vec = vec && reinterpret_cast<uintptr_t>(v->p) % (4 * sizeof(T)) == 0 && (a.n == 1 || v->batch % 4 == 0);
+  if (vec) scan_step<T, LP, true><<<blocks, 256, 0, s>>>(a, per_sequence);
+  else scan_step<T, LP, false><<<blocks, 256, 0, s>>>(a, per_sequence);
   return int(hipGetLastError());
 }
 

@@ -141,8 +141,8 @@ cc3d_status_t causal_conv1d_backward(cc3d_conv1d_plan_t plan, const cc3d_conv1d_
  *   dz = dy * (sum_s C * h + D * u) * silu'(z);  dh_in = exp(delta[0] * A) * g[0]
  * The states are computed again from h_in; nothing is kept by the forward
  * call.  Any gradient may be left out (NULL).  With A >= 0 the recurrence
- * grows and may overflow, as the formula does.  The backward call refuses
- * views whose tokens are 2^25 elements or more apart as unsupported.
+ * grows and may overflow, as the formula does.  Views whose tokens are 2^25
+ * elements or more apart are refused as unsupported (but with T = 1).
  * ------------------------------------------------------------------------ */
 typedef struct cc3d_scan_desc {
   int32_t n, t, d;    /* sequences, tokens, channels; >= 1 */
