@@ -266,7 +266,7 @@ extern "C" cc3d_status_t selective_scan_plan(const cc3d_scan_desc_t* d, cc3d_sca
   const int64_t base = int64_t(d->n) * tiles * cc3d::scan_fwd_waves(*d);
   int64_t chunk = ceildiv(d->t, 4) * 4;
   if (base < kSimds && d->t > 64) {
-    const int64_t pieces = std::min<int64_t>(ceildiv(2 * kSimds, base), ceildiv(d->t, 32));
+    const int64_t pieces = std::min<int64_t>(ceildiv(4 * kSimds, base), ceildiv(d->t, 32));
     chunk = ceildiv(ceildiv(d->t, pieces), 4) * 4;
   }
   const int64_t chunks = ceildiv(d->t, chunk);
@@ -274,7 +274,7 @@ extern "C" cc3d_status_t selective_scan_plan(const cc3d_scan_desc_t* d, cc3d_sca
   const int64_t bwd_chunks = ceildiv(d->t, bw.chunk);
   const int64_t bwd_tiles = int64_t(d->groups) * bw.tiles_per_group;
   if (int64_t(d->n) * std::max(chunks, bwd_chunks) > kMaxBlocks / tiles ||
-      int64_t(d->n) * ceildiv(d->states, 4) > kMaxBlocks / ceildiv(d->d, 16))
+      int64_t(d->n) * d->states > kMaxBlocks / ceildiv(d->d, 64) || int64_t(d->n) * ceildiv(d->d, 16) > kMaxBlocks / 4)
     return refuse(CC3D_ERR_UNSUPPORTED);
   auto* p = make_plan<cc3d_scan_plan>(d);
   if (!p) return CC3D_ERR_NO_MEMORY;

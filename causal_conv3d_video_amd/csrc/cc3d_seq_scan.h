@@ -195,9 +195,10 @@ __device__ __forceinline__ void spread_rows(const Feed<T, NS, ROWS>& f, float* b
 // or, REV, the gradient's from the chunk's last token back,
 //   g = exp(delta A) (g + gy C),  gy = dy silu(z),
 // and the chunk's sum of delta, whose exponential is the whole chunk's decay.
-template <class T, int NS, bool REV>
-__global__ __launch_bounds__(64 * (cc3d::kScanMaxStates / NS)) void scan_carry(ScanArgs a) {
-  __shared__ __attribute__((aligned(16))) float box_all[cc3d::kScanMaxStates / NS][StateBox<NS>::kSize];
+template <class T, int NS, bool REV, bool MULTI>
+__global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void scan_carry(ScanArgs a) {
+  // (LDS for the waves there are: it would limit how many workgroups a compute unit holds)
+  __shared__ __attribute__((aligned(16))) float box_all[MULTI ? cc3d::kScanMaxStates / NS : 1][StateBox<NS>::kSize];
   const Place at(a);
   float* box = box_all[at.wave];
   const int n = int(at.item / a.chunks), ch = int(at.item - int64_t(n) * a.chunks);
@@ -267,39 +268,77 @@ __global__ __launch_bounds__(64 * (cc3d::kScanMaxStates / NS)) void scan_carry(S
 
 // Turns what every chunk adds into the state that enters it, from the
 // sequence's first state on (REV: the gradient that enters it from the right).
+// A workgroup takes 64 channels of one state; each wave loads 16 chunks at
+// once and joins them, and the waves' joined stretches meet in LDS, so the
+// loads of a long sequence are not one after another.
+constexpr int kJoinChunks = 16, kJoinWaves = 16;
+
 template <bool REV>
-__global__ __launch_bounds__(256) void scan_join(ScanArgs a) {
-  const int channels = a.groups * a.wide;
-  const int tiles = (channels + 63) / 64;
-  // blockIdx.x = (n * ceil(S / 4) + states / 4) * tiles + tile
-  const int tile = blockIdx.x % tiles;
-  const int per = (a.s + 3) / 4;
+__global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a) {
+  __shared__ float add_of[kJoinWaves][64], sum_of[kJoinWaves][64];
+  const int channels = a.groups * a.wide, tiles = (channels + 63) / 64;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, waves = blockDim.x / 64;
+  // blockIdx.x = (n * S + state) * tiles + tile
   const int64_t rest = blockIdx.x / tiles;
-  const int n = int(rest / per), s = int(rest - int64_t(n) * per) * 4 + threadIdx.x / 64;
-  const int chan = tile * 64 + threadIdx.x % 64;
-  if (chan >= channels || s >= a.s) return;
+  const int tile = int(blockIdx.x - rest * tiles), n = int(rest / a.s), s = int(rest - int64_t(n) * a.s);
+  const bool on = tile * 64 + lane < channels;
+  const int chan = on ? tile * 64 + lane : channels - 1;
   const float a2 = a.a[int64_t(chan) * a.s + s] * kLog2e;
   const float* first = REV ? a.dh_out : a.h_in;
-  float h = first ? first[(int64_t(n) * channels + chan) * a.s + s] : 0.f;
+  float enter = first ? first[(int64_t(n) * channels + chan) * a.s + s] : 0.f;
   float* carry = (REV ? a.gcarry : a.carry) + (int64_t(n) * a.chunks * a.s + s) * channels + chan;
   const float* sums = a.sums + int64_t(n) * a.chunks * channels + chan;
   const int64_t step = int64_t(a.s) * channels;
-  for (int c0 = 0; c0 < a.chunks; c0 += 16) {
-    float add[16], sum[16];
+  for (int base = 0; base < a.chunks; base += kJoinChunks * waves) {
+    const int c0 = base + wave * kJoinChunks;
+    float add[kJoinChunks], decay[kJoinChunks], total = 0.f, h = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int c = REV ? a.chunks - 1 - (c0 + i) : c0 + i;
-      const bool in = c0 + i < a.chunks;
-      add[i] = in ? carry[c * step] : 0.f;
-      sum[i] = in ? sums[int64_t(c) * channels] : 0.f;
+    for (int i = 0; i < kJoinChunks; ++i) {
+      const int k = min(c0 + i, a.chunks - 1), c = REV ? a.chunks - 1 - k : k;
+      add[i] = carry[c * step];
+      decay[i] = sums[int64_t(c) * channels];
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int c = REV ? a.chunks - 1 - (c0 + i) : c0 + i;
-      if (c0 + i < a.chunks) carry[c * step] = h;
-      h = fmaf(__builtin_amdgcn_exp2f(sum[i] * a2), h, add[i]);
+    for (int i = 0; i < kJoinChunks; ++i) {
+      const bool in = c0 + i < a.chunks;
+      add[i] = in ? add[i] : 0.f;
+      decay[i] = in ? decay[i] : 0.f;
+      total += decay[i];
+      decay[i] = __builtin_amdgcn_exp2f(decay[i] * a2);
+      h = fmaf(decay[i], h, add[i]);
+    }
+    __syncthreads();
+    add_of[wave][lane] = h;
+    sum_of[wave][lane] = total;
+    __syncthreads();
+    float mine = enter;
+    for (int w = 0; w < waves; ++w) {
+      if (w == wave) mine = enter;
+      enter = fmaf(__builtin_amdgcn_exp2f(sum_of[w][lane] * a2), enter, add_of[w][lane]);
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinChunks; ++i) {
+      const int k = c0 + i, c = REV ? a.chunks - 1 - k : k;
+      if (k < a.chunks && on) carry[c * step] = mine;
+      mine = fmaf(decay[i], mine, add[i]);
     }
   }
+}
+
+template <bool REV>
+int run_join(const ScanArgs& a, hipStream_t s) {
+  const int waves = a.chunks >= kJoinChunks * kJoinWaves ? kJoinWaves : (a.chunks + kJoinChunks - 1) / kJoinChunks;
+  const unsigned blocks = unsigned(int64_t(a.n) * a.s * ((a.groups * a.wide + 63) / 64));
+  scan_join<REV><<<blocks, 64 * waves, 0, s>>>(a);
+  return int(hipGetLastError());
+}
+
+template <class T, int NS, bool REV>
+int run_carry(const ScanArgs& a, hipStream_t s) {
+  const unsigned blocks = unsigned(int64_t(a.groups) * a.tiles_per_group * a.n * a.chunks);
+  if (a.waves > 1) scan_carry<T, NS, REV, true><<<blocks, 64 * a.waves, 0, s>>>(a);
+  else scan_carry<T, NS, REV, false><<<blocks, 64, 0, s>>>(a);
+  return int(hipGetLastError());
 }
 
 inline ScanRows view_of(const cc3d_rows_t& v) { return {v.p, v.batch, v.row}; }
@@ -324,10 +363,6 @@ inline ScanArgs scan_args(const cc3d_scan_plan& p, const cc3d_scan_args_t& c) {
   a.tiles_per_group = cc3d::scan_tiles_per_group(p.d);
   a.softplus = p.d.softplus;
   return a;
-}
-
-inline unsigned join_blocks(const cc3d_scan_desc_t& d) {
-  return unsigned(int64_t(d.n) * ((d.states + 3) / 4) * ((d.d + 63) / 64));
 }
 
 }  // namespace

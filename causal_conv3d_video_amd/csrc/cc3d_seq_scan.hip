@@ -230,11 +230,9 @@ int run_scan(const cc3d_scan_plan& p, ScanArgs& a, hipStream_t s) {
   const int64_t tiles = int64_t(a.groups) * a.tiles_per_group;
   const unsigned blocks = unsigned(tiles * a.n * a.chunks);
   if (a.chunks > 1) {
-    scan_carry<T, NS, false><<<blocks, 64 * a.waves, 0, s>>>(a);
-    int e = int(hipGetLastError());
+    int e = run_carry<T, NS, false>(a, s);
     if (e) return e;
-    scan_join<false><<<join_blocks(p.d), 256, 0, s>>>(a);
-    e = int(hipGetLastError());
+    e = run_join<false>(a, s);
     if (e) return e;
   }
   if (a.waves > 1) scan_fwd<T, NS, true><<<blocks, 64 * a.waves, 0, s>>>(a);

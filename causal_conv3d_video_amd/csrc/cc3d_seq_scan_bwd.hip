@@ -517,14 +517,11 @@ template <class T, int NS>
 int run_carries(const cc3d_scan_plan& p, ScanArgs a, hipStream_t s) {
   a.waves = cc3d::scan_fwd_waves(p.d);
   a.tiles_per_group = cc3d::scan_tiles_per_group(p.d);
-  const unsigned blocks = unsigned(int64_t(a.groups) * a.tiles_per_group * a.n * a.chunks);
-  scan_carry<T, NS, false><<<blocks, 64 * a.waves, 0, s>>>(a);
-  scan_carry<T, NS, true><<<blocks, 64 * a.waves, 0, s>>>(a);
-  const int e = int(hipGetLastError());
-  if (e) return e;
-  scan_join<false><<<join_blocks(p.d), 256, 0, s>>>(a);
-  scan_join<true><<<join_blocks(p.d), 256, 0, s>>>(a);
-  return int(hipGetLastError());
+  int e = run_carry<T, NS, false>(a, s);
+  if (!e) e = run_carry<T, NS, true>(a, s);
+  if (!e) e = run_join<false>(a, s);
+  if (!e) e = run_join<true>(a, s);
+  return e;
 }
 
 template <class T>
