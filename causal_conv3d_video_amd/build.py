@@ -27,7 +27,7 @@ HIP_FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-Wall",
 # translation units: (source, compiler)
 HIP_SOURCES = (["cc3d_k_g32.hip", "cc3d_k_mfma.hip", "cc3d_k_misc.hip", "cc3d_launch.hip", "cc3d_noalloc.hip",
                 "cc3d_k_s1.hip", "cc3d_seq_conv1d.hip", "cc3d_seq_scan.hip", "cc3d_seq_scan_bwd.hip",
-                "cc3d_seq_join.hip"]
+                "cc3d_seq_join.hip", "cc3d_seq_join_bwd.hip", "cc3d_seq_sum.hip"]
                + ["cc3d_k_few%d.hip" % c for c in range(1, 6)])
 CXX_SOURCES = ["cc3d_plan.cpp", "cc3d_seq_plan.cpp"]
 

@@ -7,8 +7,7 @@
 // and one written: bound by memory.  A thread owns eight consecutive channels
 // (16-byte loads and stores of bf16, neighbouring threads on neighbouring
 // channels) and walks a run of tokens with the last K - 1 of them in
-// registers, so x is read once but for K - 1 tokens a run.  Where a pointer
-// or a stride does not allow 16-byte accesses a thread owns one channel.
+// registers, so x is read once but for K - 1 tokens a run.
 #include "cc3d_seq_device.h"
 
 namespace {
@@ -20,41 +19,39 @@ struct Conv1dArgs {
   float* part;  // backward: [rows][K + 1][C]
   int64_t xb, xr, yb, yr, dyb, dyr, dxb, dxr;
   int n, t, c, seg, nseg;
-  int vecs;      // channel vectors (of 8, or of 1)
+  int vecs;      // threads side by side along the channels
   int64_t rows;  // backward: workgroups along the tokens
   int64_t items; // n * nseg
 };
 
-// VEC channels of storage type T.
-template <class T, int VEC>
+constexpr int kAhead = 4, kBack = 2;
+
+// A thread's eight channels.  Where C is no multiple of eight the last thread
+// takes the last eight, some of which are the thread's before it too: both
+// compute and store the same values there.  FEW: C is less than eight.
+template <class T, bool FEW>
 struct Lane {
-  std::conditional_t<VEC == 8, Raw8<T>, T> r;
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (VEC == 8) r = load8(p);
-    else r = *p;
+  Raw8<T> r;
+  __device__ __forceinline__ void load(const T* p, int n) {
+    if (FEW) r = load_some(p, n);
+    else r = load8(p);
   }
-  __device__ __forceinline__ void zero() {
-    if constexpr (VEC == 8) r = zero8<T>();
-    else r = T(0);
-  }
-  __device__ __forceinline__ float get(int j) const {
-    if constexpr (VEC == 8) return get8(r, j);
-    else return to_f32(r);
-  }
-  static __device__ __forceinline__ void store(T* p, const float* v) {
-    if constexpr (VEC == 8) store8(p, v);
-    else *p = from_f32<T>(v[0]);
+  __device__ __forceinline__ void zero() { r = zero8<T>(); }
+  __device__ __forceinline__ float get(int j) const { return get8(r, j); }
+  static __device__ __forceinline__ void store(T* p, const float* v, int n) {
+    if (FEW) store_some(p, n, v);
+    else store8(p, v);
   }
 };
 
-template <class T, int K, int VEC, bool SILU>
+template <class T, int K, bool FEW, bool SILU>
 __global__ __launch_bounds__(256) void conv1d_fwd(Conv1dArgs a) {
   const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
   const int64_t item = id / a.vecs;
   if (item >= a.items) return;
   const int cv = int(id - item * a.vecs);
   const int n = int(item / a.nseg), sg = int(item - int64_t(n) * a.nseg);
-  const int c0 = cv * VEC;
+  const int c0 = FEW ? 0 : min(cv * 8, a.c - 8), left = a.c;
   const int len = a.lengths ? min(max(a.lengths[n], 0), a.t) : a.t;
   const T* x = static_cast<const T*>(a.x) + int64_t(n) * a.xb + c0;
   T* y = static_cast<T*>(a.y) + int64_t(n) * a.yb + c0;
@@ -62,50 +59,65 @@ __global__ __launch_bounds__(256) void conv1d_fwd(Conv1dArgs a) {
   const int64_t cache_at = int64_t(n) * (K - 1) * a.c + c0;
   const T* cin = a.cache_in ? static_cast<const T*>(a.cache_in) + cache_at : nullptr;
 
-  Lane<T, VEC> ld;
-  float wt[K][VEC], bias[VEC];
+  Lane<T, FEW> ld;
+  float wt[K][8], bias[8];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    ld.load(w + int64_t(k) * a.c);
+    ld.load(w + int64_t(k) * a.c, left);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) wt[k][j] = ld.get(j);
+    for (int j = 0; j < 8; ++j) wt[k][j] = ld.get(j);
   }
   ld.zero();
-  if (a.b) ld.load(static_cast<const T*>(a.b) + c0);
+  if (a.b) ld.load(static_cast<const T*>(a.b) + c0, left);
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) bias[j] = ld.get(j);
+  for (int j = 0; j < 8; ++j) bias[j] = ld.get(j);
 
   const int t0 = sg * a.seg, t1 = min(t0 + a.seg, a.t);
   // win[i]: token t0 - (K - 1) + i of x, or of the cache before token 0
-  Lane<T, VEC> win[K];
+  Lane<T, FEW> win[K];
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) {
     const int s = t0 - (K - 1) + i;
     win[i].zero();
     if (s >= 0) {
-      if (s < len) win[i].load(x + int64_t(s) * a.xr);
+      if (s < len) win[i].load(x + int64_t(s) * a.xr, left);
     } else if (cin) {
-      win[i].load(cin + int64_t(s + K - 1) * a.c);
+      win[i].load(cin + int64_t(s + K - 1) * a.c, left);
     }
   }
+  // kAhead tokens load while kAhead are computed; those past the last are read from it again
   const int te = min(t1, len);
   int t = t0;
-  for (; t < te; ++t) {
-    win[K - 1].load(x + int64_t(t) * a.xr);
-    float p[VEC];
+  Lane<T, FEW> next[kAhead];
+  auto fetch = [&](int from) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      float s = bias[j];
+    for (int i = 0; i < kAhead; ++i) next[i].load(x + int64_t(min(from + i, te - 1)) * a.xr, left);
+  };
+  if (t < te) fetch(t);
+  while (t < te) {
+    Lane<T, FEW> now[kAhead];
 #pragma unroll
-      for (int k = 0; k < K; ++k) s = fmaf(wt[k][j], win[k].get(j), s);
-      p[j] = SILU ? s * sigmoid_f32(s) : s;
+    for (int i = 0; i < kAhead; ++i) now[i] = next[i];
+    if (t + kAhead < te) fetch(t + kAhead);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i, ++t) {
+      if (t >= te) break;
+      win[K - 1] = now[i];
+      float p[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float s = bias[j];
+#pragma unroll
+        for (int k = 0; k < K; ++k) s = fmaf(wt[k][j], win[k].get(j), s);
+        p[j] = SILU ? s * sigmoid_f32(s) : s;
+      }
+      Lane<T, FEW>::store(y + int64_t(t) * a.yr, p, left);
+#pragma unroll
+      for (int q = 0; q < K - 1; ++q) win[q] = win[q + 1];
     }
-    Lane<T, VEC>::store(y + int64_t(t) * a.yr, p);
-#pragma unroll
-    for (int i = 0; i < K - 1; ++i) win[i] = win[i + 1];
   }
-  float none[VEC] = {};
-  for (; t < t1; ++t) Lane<T, VEC>::store(y + int64_t(t) * a.yr, none);
+  float none[8] = {};
+  for (; t < t1; ++t) Lane<T, FEW>::store(y + int64_t(t) * a.yr, none, left);
 
   if (K > 1 && sg == 0 && a.cache_out) {
     T* co = static_cast<T*>(a.cache_out) + cache_at;
@@ -113,12 +125,12 @@ __global__ __launch_bounds__(256) void conv1d_fwd(Conv1dArgs a) {
     for (int i = 0; i < K - 1; ++i) {
       const int s = len - (K - 1) + i;
       ld.zero();
-      if (s >= 0) ld.load(x + int64_t(s) * a.xr);
-      else if (cin) ld.load(cin + int64_t(s + K - 1) * a.c);
-      float v[VEC];
+      if (s >= 0) ld.load(x + int64_t(s) * a.xr, left);
+      else if (cin) ld.load(cin + int64_t(s + K - 1) * a.c, left);
+      float v[8];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] = ld.get(j);
-      Lane<T, VEC>::store(co + int64_t(i) * a.c, v);
+      for (int j = 0; j < 8; ++j) v[j] = ld.get(j);
+      Lane<T, FEW>::store(co + int64_t(i) * a.c, v, left);
     }
   }
 }
@@ -130,29 +142,29 @@ __global__ __launch_bounds__(256) void conv1d_fwd(Conv1dArgs a) {
 // all tokens: a thread keeps them in registers over every run that it takes,
 // the workgroup's rows add theirs in LDS, and each workgroup writes one row of
 // partial sums; sum_rows adds those in their order.
-template <class T, int K, int VEC, bool SILU>
+template <class T, int K, bool FEW, bool SILU>
 __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
-  __shared__ float red[256 * VEC];
+  __shared__ float red[256 * 8];
   const int lane = threadIdx.x % lanes, line = threadIdx.x / lanes, lines = 256 / lanes;
   const int tiles = (a.vecs + lanes - 1) / lanes;
   const int tile = int(blockIdx.x % tiles);
   const int64_t row = blockIdx.x / tiles;
   const int cv = tile * lanes + lane;
   const bool on = cv < a.vecs;
-  const int c0 = on ? cv * VEC : 0;
+  const int c0 = FEW || !on ? 0 : min(cv * 8, a.c - 8), left = a.c;
 
-  Lane<T, VEC> ld;
-  float wt[K][VEC], bias[VEC], dw[K][VEC] = {}, db[VEC] = {};
+  Lane<T, FEW> ld;
+  float wt[K][8], bias[8], dw[K][8] = {}, db[8] = {};
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    ld.load(static_cast<const T*>(a.w) + int64_t(k) * a.c + c0);
+    ld.load(static_cast<const T*>(a.w) + int64_t(k) * a.c + c0, left);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) wt[k][j] = ld.get(j);
+    for (int j = 0; j < 8; ++j) wt[k][j] = ld.get(j);
   }
   ld.zero();
-  if (a.b) ld.load(static_cast<const T*>(a.b) + c0);
+  if (a.b) ld.load(static_cast<const T*>(a.b) + c0, left);
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) bias[j] = ld.get(j);
+  for (int j = 0; j < 8; ++j) bias[j] = ld.get(j);
 
   for (int64_t item = row * lines + line; on && item < a.items; item += a.rows * lines) {
     const int n = int(item / a.nseg), sg = int(item - int64_t(n) * a.nseg);
@@ -166,28 +178,47 @@ __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
     T* dci = a.dcache_in ? static_cast<T*>(a.dcache_in) + cache_at : nullptr;
 
     const int t0 = sg * a.seg, t1 = min(t0 + a.seg, a.t);
-    Lane<T, VEC> win[K];
+    Lane<T, FEW> win[K];
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
       const int s = t0 - (K - 1) + i;
       win[i].zero();
       if (s >= 0) {
-        if (s < len) win[i].load(x + int64_t(s) * a.xr);
+        if (s < len) win[i].load(x + int64_t(s) * a.xr, left);
       } else if (cin) {
-        win[i].load(cin + int64_t(s + K - 1) * a.c);
+        win[i].load(cin + int64_t(s + K - 1) * a.c, left);
       }
     }
-    float dp[K][VEC] = {};  // dp[i]: token t - (K - 1) + i
-    for (int t = t0; t < t1 + K - 1; ++t) {
-      win[K - 1].zero();
+    float dp[K][8] = {};  // dp[i]: token t - (K - 1) + i
+    // kBack tokens load while kBack are computed; those past the valid ones are read from the last and not used
+    const int end = t1 + K - 1, last = max(min(end, len) - 1, 0);
+    Lane<T, FEW> next_x[kBack], next_d[kBack];
+    auto fetch = [&](int from) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) dp[K - 1][j] = 0.f;
-      if (t < len) {
-        win[K - 1].load(x + int64_t(t) * a.xr);
-        ld.load(dy + int64_t(t) * a.dyr);
+      for (int i = 0; i < kBack; ++i) {
+        const int64_t t = min(from + i, last);
+        next_x[i].load(x + t * a.xr, left);
+        next_d[i].load(dy + t * a.dyr, left);
+      }
+    };
+    fetch(t0);
+    for (int tb = t0; tb < end; tb += kBack) {
+      Lane<T, FEW> now_x[kBack], now_d[kBack];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          float g = ld.get(j);
+      for (int i = 0; i < kBack; ++i) {
+        now_x[i] = next_x[i];
+        now_d[i] = next_d[i];
+      }
+      if (tb + kBack < end) fetch(tb + kBack);
+#pragma unroll
+      for (int i = 0; i < kBack; ++i) {
+        const int t = tb + i;
+        if (t >= end) break;
+        win[K - 1] = now_x[i];
+        if (t >= len) win[K - 1].zero();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float g = now_d[i].get(j);
           if (SILU) {
             float s = bias[j];
 #pragma unroll
@@ -195,40 +226,40 @@ __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
             const float sg_ = sigmoid_f32(s);
             g *= sg_ * (1.f + s * (1.f - sg_));
           }
+          g = t < len ? g : 0.f;
           dp[K - 1][j] = g;
-          if (t < t1) {  // the K - 1 tokens after the run are another thread's
-            db[j] += g;
+          const float mine = t < t1 ? g : 0.f;  // the K - 1 tokens after the run are another thread's
+          db[j] += mine;
 #pragma unroll
-            for (int k = 0; k < K; ++k) dw[k][j] = fmaf(g, win[k].get(j), dw[k][j]);
+          for (int k = 0; k < K; ++k) dw[k][j] = fmaf(mine, win[k].get(j), dw[k][j]);
+        }
+        const int s = t - (K - 1);
+        if (s >= t0 || sg == 0) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float acc = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) acc = fmaf(wt[k][j], dp[K - 1 - k][j], acc);
+            v[j] = acc;
+          }
+          if (dco && s < len && s >= len - (K - 1)) {
+            ld.load(dco + int64_t(s - len + K - 1) * a.c, left);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += ld.get(j);
+          }
+          if (s >= 0) {
+            if (dx) Lane<T, FEW>::store(dx + int64_t(s) * a.dxr, v, left);
+          } else if (dci) {
+            Lane<T, FEW>::store(dci + int64_t(s + K - 1) * a.c, v, left);
           }
         }
-      }
-      const int s = t - (K - 1);
-      if (s >= t0 || sg == 0) {
-        float v[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          float acc = 0.f;
+        for (int q = 0; q < K - 1; ++q) {
+          win[q] = win[q + 1];
 #pragma unroll
-          for (int k = 0; k < K; ++k) acc = fmaf(wt[k][j], dp[K - 1 - k][j], acc);
-          v[j] = acc;
+          for (int j = 0; j < 8; ++j) dp[q][j] = dp[q + 1][j];
         }
-        if (dco && s < len && s >= len - (K - 1)) {
-          ld.load(dco + int64_t(s - len + K - 1) * a.c);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) v[j] += ld.get(j);
-        }
-        if (s >= 0) {
-          if (dx) Lane<T, VEC>::store(dx + int64_t(s) * a.dxr, v);
-        } else if (dci) {
-          Lane<T, VEC>::store(dci + int64_t(s + K - 1) * a.c, v);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < K - 1; ++i) {
-        win[i] = win[i + 1];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) dp[i][j] = dp[i + 1][j];
       }
     }
   }
@@ -238,91 +269,70 @@ __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
   for (int k = 0; k <= K; ++k) {
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) red[threadIdx.x * VEC + j] = k < K ? dw[k < K ? k : 0][j] : db[j];
+    for (int j = 0; j < 8; ++j) red[threadIdx.x * 8 + j] = k < K ? dw[k < K ? k : 0][j] : db[j];
     __syncthreads();
     if (line == 0 && on) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
+      for (int j = 0; j < 8; ++j) {
+        if (FEW && j >= left) continue;
         float s = 0.f;
-        for (int l = 0; l < lines; ++l) s += red[(l * lanes + lane) * VEC + j];
+        for (int l = 0; l < lines; ++l) s += red[(l * lanes + lane) * 8 + j];
         part[int64_t(k) * a.c + j] = s;
       }
     }
   }
 }
 
-// out[m] = sum over r of part[r * stride + m]: 16 rows at a time by 64 columns.
-__global__ __launch_bounds__(1024) void sum_rows(const float* part, int64_t rows, int64_t cols, int64_t stride, float* out) {
-  __shared__ float red[16][64];
-  const int lane = threadIdx.x % 64, line = threadIdx.x / 64;
-  const int64_t m = int64_t(blockIdx.x) * 64 + lane;
-  float s = 0.f;
-  if (m < cols)
-    for (int64_t r = line; r < rows; r += 16) s += part[r * stride + m];
-  red[line][lane] = s;
-  __syncthreads();
-  if (line == 0 && m < cols) {
-#pragma unroll
-    for (int l = 1; l < 16; ++l) s += red[l][lane];
-    out[m] = s;
+template <class T, int K, bool SILU, bool FEW>
+void run_conv1d(const Conv1dArgs& a, bool backward, hipStream_t s) {
+  if (backward) {
+    const int lanes = cc3d::conv1d_lanes(a.c);
+    conv1d_bwd<T, K, FEW, SILU><<<unsigned(a.rows * ((a.vecs + lanes - 1) / lanes)), 256, 0, s>>>(a, lanes);
+  } else {
+    conv1d_fwd<T, K, FEW, SILU><<<unsigned((a.items * a.vecs + 255) / 256), 256, 0, s>>>(a);
   }
-}
-
-bool vec_ok(const void* p, int64_t s0, int64_t s1) {
-  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && s0 % 8 == 0 && s1 % 8 == 0);
 }
 
 template <class T, int K, bool SILU>
-void run_conv1d(const Conv1dArgs& in, bool vec, bool backward, hipStream_t s) {
-  Conv1dArgs a = in;
-  a.vecs = vec ? a.c / 8 : a.c;
-  a.items = int64_t(a.n) * a.nseg;
-  if (!backward) {
-    const unsigned blocks = unsigned((a.items * a.vecs + 255) / 256);
-    if (vec) conv1d_fwd<T, K, 8, SILU><<<blocks, 256, 0, s>>>(a);
-    else conv1d_fwd<T, K, 1, SILU><<<blocks, 256, 0, s>>>(a);
-    return;
-  }
-  int lanes = 1;
-  while (lanes < 64 && lanes < a.vecs) lanes *= 2;
-  const int64_t lines = 256 / lanes;
-  const int64_t rows = (a.items + lines - 1) / lines;
-  if (rows < a.rows) a.rows = rows;
-  const unsigned blocks = unsigned(a.rows * ((a.vecs + lanes - 1) / lanes));
-  if (vec) conv1d_bwd<T, K, 8, SILU><<<blocks, 256, 0, s>>>(a, lanes);
-  else conv1d_bwd<T, K, 1, SILU><<<blocks, 256, 0, s>>>(a, lanes);
+void pick_few(const Conv1dArgs& a, bool backward, hipStream_t s) {
+  if (a.c < 8) run_conv1d<T, K, SILU, true>(a, backward, s);
+  else run_conv1d<T, K, SILU, false>(a, backward, s);
 }
 
 template <class T, bool SILU>
-void pick_taps(int k, const Conv1dArgs& a, bool vec, bool backward, hipStream_t s) {
+void pick_taps(int k, const Conv1dArgs& a, bool backward, hipStream_t s) {
   switch (k) {
-    case 1: return run_conv1d<T, 1, SILU>(a, vec, backward, s);
-    case 2: return run_conv1d<T, 2, SILU>(a, vec, backward, s);
-    case 3: return run_conv1d<T, 3, SILU>(a, vec, backward, s);
-    case 4: return run_conv1d<T, 4, SILU>(a, vec, backward, s);
-    case 5: return run_conv1d<T, 5, SILU>(a, vec, backward, s);
-    case 6: return run_conv1d<T, 6, SILU>(a, vec, backward, s);
-    case 7: return run_conv1d<T, 7, SILU>(a, vec, backward, s);
-    default: return run_conv1d<T, 8, SILU>(a, vec, backward, s);
+    case 1: return pick_few<T, 1, SILU>(a, backward, s);
+    case 2: return pick_few<T, 2, SILU>(a, backward, s);
+    case 3: return pick_few<T, 3, SILU>(a, backward, s);
+    case 4: return pick_few<T, 4, SILU>(a, backward, s);
+    case 5: return pick_few<T, 5, SILU>(a, backward, s);
+    case 6: return pick_few<T, 6, SILU>(a, backward, s);
+    case 7: return pick_few<T, 7, SILU>(a, backward, s);
+    default: return pick_few<T, 8, SILU>(a, backward, s);
   }
 }
 
-void pick_type(const cc3d_conv1d_desc_t& d, const Conv1dArgs& a, bool vec, bool backward, hipStream_t s) {
+void pick_type(const cc3d_conv1d_desc_t& d, const Conv1dArgs& a, bool backward, hipStream_t s) {
   const bool silu = d.act == CC3D_ACT_SILU;
   if (d.dtype == CC3D_BF16) {
-    if (silu) pick_taps<bf16_s, true>(d.k, a, vec, backward, s);
-    else pick_taps<bf16_s, false>(d.k, a, vec, backward, s);
+    if (silu) pick_taps<bf16_s, true>(d.k, a, backward, s);
+    else pick_taps<bf16_s, false>(d.k, a, backward, s);
   } else {
-    if (silu) pick_taps<float, true>(d.k, a, vec, backward, s);
-    else pick_taps<float, false>(d.k, a, vec, backward, s);
+    if (silu) pick_taps<float, true>(d.k, a, backward, s);
+    else pick_taps<float, false>(d.k, a, backward, s);
   }
 }
 
-Conv1dArgs base_args(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& c) {
+Conv1dArgs base_args(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& c, int seg) {
   Conv1dArgs a{};
   a.n = p.d.n;
   a.t = p.d.t;
   a.c = p.d.c;
+  a.vecs = (a.c + 7) / 8;
+  a.seg = seg;
+  a.nseg = (a.t + seg - 1) / seg;
+  a.items = int64_t(a.n) * a.nseg;
   a.x = c.x.p;
   a.xb = c.x.batch;
   a.xr = c.x.row;
@@ -337,28 +347,18 @@ Conv1dArgs base_args(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& c) {
 
 namespace cc3d {
 
-int launch_sum_rows(const float* part, int64_t rows, int64_t cols, int64_t stride, float* out, void* stream) {
-  if (!out) return 0;
-  sum_rows<<<unsigned((cols + 63) / 64), 1024, 0, static_cast<hipStream_t>(stream)>>>(part, rows, cols, stride, out);
-  return int(hipGetLastError());
-}
-
 int launch_conv1d_forward(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& c, void* stream) {
-  Conv1dArgs a = base_args(p, c);
+  Conv1dArgs a = base_args(p, c, p.seg);
   a.y = c.y.p;
   a.yb = c.y.batch;
   a.yr = c.y.row;
   a.cache_out = c.cache_out;
-  a.seg = p.seg;
-  a.nseg = (p.d.t + p.seg - 1) / p.seg;
-  const bool vec = p.d.c % 8 == 0 && vec_ok(c.x.p, c.x.batch, c.x.row) && vec_ok(c.y.p, c.y.batch, c.y.row) &&
-                   vec_ok(c.w, 0, 0) && vec_ok(c.b, 0, 0) && vec_ok(c.cache_in, 0, 0) && vec_ok(c.cache_out, 0, 0);
-  pick_type(p.d, a, vec, false, static_cast<hipStream_t>(stream));
+  pick_type(p.d, a, false, static_cast<hipStream_t>(stream));
   return int(hipGetLastError());
 }
 
 int launch_conv1d_backward(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& c, void* stream) {
-  Conv1dArgs a = base_args(p, c);
+  Conv1dArgs a = base_args(p, c, p.bwd_seg);
   a.dy = c.dy.p;
   a.dyb = c.dy.batch;
   a.dyr = c.dy.row;
@@ -368,24 +368,13 @@ int launch_conv1d_backward(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& 
   a.dcache_in = c.dcache_in;
   a.dcache_out = c.dcache_out;
   a.part = static_cast<float*>(c.workspace);
-  a.seg = p.bwd_seg;
-  a.nseg = (p.d.t + p.bwd_seg - 1) / p.bwd_seg;
   a.rows = p.bwd_rows;
-  const bool vec = p.d.c % 8 == 0 && vec_ok(c.x.p, c.x.batch, c.x.row) && vec_ok(c.dy.p, c.dy.batch, c.dy.row) &&
-                   vec_ok(c.dx.p, c.dx.batch, c.dx.row) && vec_ok(c.w, 0, 0) && vec_ok(c.b, 0, 0) &&
-                   vec_ok(c.cache_in, 0, 0) && vec_ok(c.dcache_in, 0, 0) && vec_ok(c.dcache_out, 0, 0);
-  // rows actually launched: as run_conv1d works them out
-  const int64_t vecs = vec ? p.d.c / 8 : p.d.c;
-  int64_t lanes = 1;
-  while (lanes < 64 && lanes < vecs) lanes *= 2;
-  const int64_t lines = 256 / lanes;
-  a.rows = std::min<int64_t>(a.rows, (int64_t(a.n) * a.nseg + lines - 1) / lines);
-  pick_type(p.d, a, vec, true, static_cast<hipStream_t>(stream));
-  int e = int(hipGetLastError());
-  const int64_t stride = int64_t(p.d.k + 1) * p.d.c;
-  if (!e) e = launch_sum_rows(a.part, a.rows, int64_t(p.d.k) * p.d.c, stride, c.dw, stream);
-  if (!e) e = launch_sum_rows(a.part + int64_t(p.d.k) * p.d.c, a.rows, p.d.c, stride, c.db, stream);
-  return e;
+  pick_type(p.d, a, true, static_cast<hipStream_t>(stream));
+  const int e = int(hipGetLastError());
+  if (e) return e;
+  const int64_t stride = int64_t(p.d.k + 1) * p.d.c, taps = int64_t(p.d.k) * p.d.c;
+  const SumJob jobs[] = {{a.part, c.dw, a.rows, taps, stride}, {a.part + taps, c.db, a.rows, p.d.c, stride}};
+  return launch_sums(jobs, 2, stream);
 }
 
 }  // namespace cc3d

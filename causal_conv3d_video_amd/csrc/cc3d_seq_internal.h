@@ -30,15 +30,24 @@ struct cc3d_join_plan {
 namespace cc3d {
 
 // Lanes that hold one row of the block join (8 channels each), a power of two.
-constexpr int kJoinThreads = 256;
 inline int join_lanes(int c) {
   int l = 8;
   while (l * 8 < c) l *= 2;
   return l;
 }
+// Threads of a workgroup: rows of up to a wave share one of four waves, wider
+// rows have their own.
+constexpr int join_threads(int lanes) { return lanes <= 64 ? 256 : lanes; }
 
-// Channels per workgroup row of the convolution's backward pass and of the
-// scan, and states per wave of the scan.
+// Threads side by side along the channels (eight each) in a workgroup of the
+// convolution's backward pass.
+inline int conv1d_lanes(int c) {
+  int l = 1;
+  while (l < 64 && l * 8 < c) l *= 2;
+  return l;
+}
+
+// Channels per wave of the scan, and states per wave of its forward pass.
 constexpr int kScanLanes = 64;
 constexpr int kScanFwdStates = 16;
 constexpr int kScanMaxStates = 64;
@@ -85,8 +94,15 @@ int launch_scan_backward(const cc3d_scan_plan& p, const cc3d_scan_args_t& a, voi
 int launch_join_forward(const cc3d_join_plan& p, const cc3d_join_args_t& a, void* stream);
 int launch_join_backward(const cc3d_join_plan& p, const cc3d_join_args_t& a, void* stream);
 
-// out[m] = sum over r of part[r][m], r = 0 .. rows - 1 in a fixed order; a
-// null out is skipped (cc3d_seq_conv1d.hip).
-int launch_sum_rows(const float* part, int64_t rows, int64_t cols, int64_t stride, float* out, void* stream);
+// Sums over rows of partial sums, up to kSumJobs of them in one launch:
+// dst[m] = sum over r of src[r * stride + m], the rows in a fixed order.  Jobs
+// without a dst are left out (cc3d_seq_sum.hip).
+struct SumJob {
+  const float* src;
+  float* dst;
+  int64_t rows, cols, stride;
+};
+constexpr int kSumJobs = 5;
+int launch_sums(const SumJob* jobs, int n, void* stream);
 
 }  // namespace cc3d

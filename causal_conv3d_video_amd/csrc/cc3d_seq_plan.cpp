@@ -189,15 +189,16 @@ extern "C" cc3d_status_t causal_conv1d_plan(const cc3d_conv1d_desc_t* d, cc3d_co
   int64_t seg = std::max<int64_t>(ceildiv(int64_t(d->n) * d->t, ceildiv(int64_t(1) << 18, vecs)), 1);
   seg = std::min<int64_t>(std::max<int64_t>(seg, 8), 64);
   seg = std::min<int64_t>(seg, d->t);
-  // the unaligned path runs one channel a thread
-  if (ceildiv(int64_t(d->n) * ceildiv(d->t, seg), 1) > kMaxBlocks / ceildiv(d->c, 64)) return refuse(CC3D_ERR_UNSUPPORTED);
+  if (int64_t(d->n) * ceildiv(d->t, seg) > kMaxBlocks / ceildiv(vecs, 256)) return refuse(CC3D_ERR_UNSUPPORTED);
   auto* p = make_plan<cc3d_conv1d_plan>(d);
   if (!p) return CC3D_ERR_NO_MEMORY;
   p->seg = int32_t(seg);
-  p->bwd_seg = int32_t(std::min<int64_t>(d->t, 32));
+  const int64_t bwd_seg = ceildiv(int64_t(d->n) * d->t, ceildiv(int64_t(1) << 18, vecs));
+  p->bwd_seg = int32_t(std::min<int64_t>(std::min<int64_t>(std::max<int64_t>(bwd_seg, 8), 32), d->t));
   // backward: partial sums of dw and db, one row for each of at most 512 workgroups along the tokens
   const int64_t items = int64_t(d->n) * ceildiv(d->t, p->bwd_seg);
-  p->bwd_rows = std::min<int64_t>(items, 512);
+  const int64_t lines = 256 / cc3d::conv1d_lanes(d->c);
+  p->bwd_rows = std::min<int64_t>(ceildiv(items, lines), 512);
   p->info.backward_workspace_bytes = p->bwd_rows * (d->k + 1) * int64_t(d->c) * 4;
   p->info.chunks = int32_t(ceildiv(d->t, p->seg));
   p->info.backward_chunks = int32_t(ceildiv(d->t, p->bwd_seg));
@@ -383,13 +384,13 @@ extern "C" cc3d_status_t norm_join_plan(const cc3d_join_desc_t* d, cc3d_join_pla
   p->d.gate_rows = std::min(d->gate_rows, d->rows);
   d = &p->d;
   p->info.chunks = p->info.backward_chunks = 1;
-  // Backward: at most four workgroups a compute unit, each with a row of partial sums
+  // Backward: at most two waves a SIMD, each workgroup with a row of partial sums
   // of the five parameter gradients.  Where a gate row serves several rows a
   // workgroup takes whole gate rows, or, where there are few of them, a part of one,
   // whose partial sums of the gate's gradient follow.
-  const int lanes = cc3d::join_lanes(d->c);
-  const int64_t at_once = std::max(1, cc3d::kJoinThreads / lanes);
-  const int64_t limit = lanes > cc3d::kJoinThreads ? 2 * kUnits : 4 * kUnits;
+  const int lanes = cc3d::join_lanes(d->c), threads = cc3d::join_threads(lanes);
+  const int64_t at_once = threads / lanes;
+  const int64_t limit = 2 * kSimds * 64 / threads;
   const int64_t gates = ceildiv(d->rows, d->gate_rows);
   if (d->gate_rows == 1) {
     p->bwd_parts = std::min(limit, ceildiv(d->rows, at_once));

@@ -581,10 +581,12 @@ int launch_scan_backward(const cc3d_scan_plan& p, const cc3d_scan_args_t& c, voi
   a.part_bc = a.part_bias + int64_t(a.workers) * a.waves * p.d.d;
   hipStream_t s = static_cast<hipStream_t>(stream);
   int e = p.d.dtype == CC3D_BF16 ? run_scan_bwd<bf16_s>(p, a, c, v, s) : run_scan_bwd<float>(p, a, c, v, s);
-  if (!e) e = launch_sum_rows(a.part_a, a.workers, state, state, c.da, stream);
-  if (!e) e = launch_sum_rows(a.part_d, int64_t(a.workers) * a.waves, p.d.d, p.d.d, c.dd, stream);
-  if (!e) e = launch_sum_rows(a.part_bias, int64_t(a.workers) * a.waves, p.d.d, p.d.d, c.ddt_bias, stream);
-  return e;
+  if (e) return e;
+  const int64_t rows = int64_t(a.workers) * a.waves;
+  const SumJob jobs[] = {{a.part_a, c.da, a.workers, state, state},
+                         {a.part_d, c.dd, rows, p.d.d, p.d.d},
+                         {a.part_bias, c.ddt_bias, rows, p.d.d, p.d.d}};
+  return launch_sums(jobs, 3, stream);
 }
 
 }  // namespace cc3d
