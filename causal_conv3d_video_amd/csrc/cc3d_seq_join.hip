@@ -85,7 +85,7 @@ struct Forward {
   static void run(const JoinArgs& a, hipStream_t s) {
     constexpr int kThreads = RowSum<LPR>::kThreads, kAtOnce = kThreads / LPR;
     // four waves a SIMD, the most its registers allow
-    const unsigned blocks = unsigned(std::min<int64_t>((a.rows + kAtOnce - 1) / kAtOnce, 4096 * 64 / kThreads));
+    const unsigned blocks = unsigned(std::min<int64_t>((a.rows + kAtOnce - 1) / kAtOnce, 8192 * 64 / kThreads));
     join_fwd<T, LPR, KIND><<<blocks, kThreads, 0, s>>>(a);
   }
 };

@@ -17,6 +17,7 @@ current torch stream); a refused one raises CC3DError, a tensor of the wrong
 kind TypeError or ValueError.
 """
 import ctypes
+import struct
 
 import torch
 
@@ -68,9 +69,12 @@ class JoinDesc(ctypes.Structure):
 
 
 def _args(name, rows, pointers):
-    """An argument block: views first, then pointers and the workspace."""
+    """An argument block: views first, then pointers and the workspace.  Every
+    field is 64 bits wide, so a call packs one as plain numbers (``pack``)."""
     fields = [(r, Rows) for r in rows] + [(p, _vp) for p in pointers] + [("workspace", _vp), ("workspace_bytes", _i64)]
-    return type(name, (ctypes.Structure,), {"_fields_": fields})
+    block = type(name, (ctypes.Structure,), {"_fields_": fields})
+    block.pack = struct.Struct("=%dQ" % (3 * len(rows) + len(pointers) + 2)).pack
+    return block
 
 
 Conv1dArgs = _args("Conv1dArgs", ("x", "y", "dy", "dx"),
@@ -90,7 +94,7 @@ for _op, _desc, _blk in (("causal_conv1d", Conv1dDesc, Conv1dArgs), ("selective_
     _f.argtypes, _f.restype = [_vp], None
     for _way in ("_forward", "_backward"):
         _f = getattr(_lib, _op + _way)
-        _f.argtypes, _f.restype = [_vp, ctypes.POINTER(_blk), _vp], ctypes.c_int
+        _f.argtypes, _f.restype = [_vp, _vp, _vp], ctypes.c_int  # the packed block, or a pointer to one
 
 
 class SeqPlan:
@@ -107,6 +111,7 @@ class SeqPlan:
         info = SeqInfo()
         getattr(_lib, op + "_plan_info")(self.handle, ctypes.byref(info))
         self.info = {name: getattr(info, name) for name, _ in SeqInfo._fields_}
+        self.shapes = _SHAPES[op](desc)
 
     def close(self):
         if self.handle:
@@ -120,103 +125,129 @@ class SeqPlan:
             pass
 
 
+# Shapes of a plan's tensors, worked out once.
+_SHAPES = {
+    "causal_conv1d": lambda d: {"seq": (d.n, d.t, d.c), "cache": (d.n, d.k - 1, d.c), "w": (d.k, d.c), "c": (d.c,),
+                                "n": (d.n,)},
+    "selective_scan": lambda d: {"seq": (d.n, d.t, d.d), "bc": (d.n, d.t, d.groups * d.states),
+                                 "split": (d.n, d.t, d.groups, d.states), "state": (d.n, d.d, d.states),
+                                 "a": (d.d, d.states), "c": (d.d,), "n": (d.n,)},
+    "norm_join": lambda d: {"rows": (d.rows, d.c), "gates": (-(-d.rows // d.gate_rows), d.c), "c": (d.c,)},
+}
+
+_F32, _I32 = torch.float32, torch.int32
+_Tensor = torch.Tensor
+
+
 def _plan_of(plan, op):
     if not isinstance(plan, SeqPlan) or plan.op != op:
         raise TypeError("expected a plan of %s_plan" % op)
-    return plan
+    return plan.shapes, plan.dtype
 
 
 def _check(t, name, dtype, device):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    """The reason a tensor is refused, or nothing when kind, type and device are right."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
     if t.dtype != dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.device != device:
-        raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, device))
+    if t.get_device() != device:
+        raise ValueError("%s is on %s, the other tensors on cuda:%d" % (name, t.device, device))
 
 
-def _set_dense(args, name, t, shape, dtype, device):
+def _device_of(t, name):
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    return t.get_device()
+
+
+def _dense(t, name, shape, dtype, device):
+    """The address of a dense tensor of exactly this shape; 0 for None."""
     if t is None:
-        return
-    _check(t, name, dtype, device)
-    if tuple(t.shape) != shape or not t.is_contiguous():
+        return 0
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device):
+        _check(t, name, dtype, device)
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s: expected a dense %s tensor, got shape %s strides %s"
                          % (name, shape, tuple(t.shape), tuple(t.stride())))
-    setattr(args, name, t.data_ptr())
+    return t.data_ptr()
 
 
-def _set_seq(args, name, t, shape, dtype, device, split=None):
-    """A view of [N, T, C]; split = (G, S) also takes [N, T, G, S]."""
+_NONE = (0, 0, 0)
+
+
+def _seq(t, name, shape, dtype, device, split=None):
+    """(address, batch stride, row stride) of a view of [N, T, C]; split: [N, T, G, S] is taken too."""
     if t is None:
-        return
-    _check(t, name, dtype, device)
+        return _NONE
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device):
+        _check(t, name, dtype, device)
     st = t.stride()
-    if split is not None and t.dim() == 4:
-        ok = tuple(t.shape) == shape[:2] + split and (st[3] == 1 or split[1] == 1) and (st[2] == split[1] or split[0] == 1)
+    if t.shape == shape:
+        ok = st[2] == 1 or shape[2] == 1
     else:
-        ok = tuple(t.shape) == shape and (st[2] == 1 or shape[2] == 1)
+        ok = split is not None and t.shape == split and (st[3] == 1 or split[3] == 1) and \
+            (st[2] == split[3] or split[2] == 1)
     if not ok:
         raise ValueError("%s: expected %s with a contiguous last dimension, got shape %s strides %s"
-                         % (name, shape if split is None else shape[:2] + split, tuple(t.shape), st))
-    v = getattr(args, name)
-    v.p, v.batch, v.row = t.data_ptr(), st[0], st[1]
+                         % (name, shape if split is None else split, tuple(t.shape), st))
+    return t.data_ptr(), st[0], st[1]
 
 
-def _set_rows(args, name, t, rows, c, dtype, device):
-    """A view of [rows, C] of a tensor [..., C] whose leading dimensions step evenly."""
+def _rows(t, name, shape, dtype, device):
+    """(address, 0, row stride) of a view of [rows, C] of a tensor [..., C] whose leading dimensions step evenly."""
     if t is None:
-        return
-    _check(t, name, dtype, device)
-    shape, st = t.shape, t.stride()
-    ok = t.dim() >= 1 and shape[-1] == c and t.numel() == rows * c and (st[-1] == 1 or c == 1)
+        return _NONE
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device):
+        _check(t, name, dtype, device)
+    rows, c = shape
+    if t.is_contiguous() and t.shape[-1:] == (c,) and t.numel() == rows * c:
+        return t.data_ptr(), 0, c
+    dims, st = t.shape, t.stride()
+    ok = t.dim() >= 1 and dims[-1] == c and t.numel() == rows * c and (st[-1] == 1 or c == 1)
     row, n = c, 1
-    if ok and not t.is_contiguous():
+    if ok:
         for i in range(t.dim() - 2, -1, -1):
-            if shape[i] == 1:
+            if dims[i] == 1:
                 continue
             if n == 1:
                 row = st[i]
             elif st[i] != row * n:
                 ok = False
                 break
-            n *= shape[i]
+            n *= dims[i]
     if not ok:
         raise ValueError("%s: expected %d evenly spaced rows of %d contiguous elements, got shape %s strides %s"
-                         % (name, rows, c, tuple(shape), st))
-    v = getattr(args, name)
-    v.p, v.batch, v.row = t.data_ptr(), 0, row
+                         % (name, rows, c, tuple(dims), st))
+    return t.data_ptr(), 0, row
 
 
-def _set_workspace(args, t, nbytes, device):
+def _space(t, nbytes, device):
+    """(address, bytes) of the workspace."""
     if t is None:
         if nbytes > 0:
             raise ValueError("this call needs a workspace of %d bytes" % nbytes)
-        return
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        return 0, 0
+    if not isinstance(t, _Tensor) or not t.is_cuda or not t.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA (HIP) tensor")
     have = t.numel() * t.element_size()
     if have < nbytes:
         raise ValueError("workspace holds %d bytes, the plan needs %d" % (have, nbytes))
-    if t.device != device:
-        raise ValueError("workspace is on %s, the other tensors on %s" % (t.device, device))
-    args.workspace, args.workspace_bytes = t.data_ptr(), have
-
-
-def _device_of(t, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
-    return t.device
+    if t.get_device() != device:
+        raise ValueError("workspace is on %s, the other tensors on cuda:%d" % (t.device, device))
+    return t.data_ptr(), have
 
 
 def _call(fn, what, plan, args, device, stream):
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            st = fn(plan.handle, ctypes.byref(args), handle)
+        handle = torch.cuda.current_stream(device).cuda_stream
     else:
-        st = fn(plan.handle, ctypes.byref(args), handle)
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = fn(plan.handle, args, handle)
+    else:
+        st = fn(plan.handle, args, handle)
     if st != CC3D_OK:
         raise CC3DError(st, what)
 
@@ -234,41 +265,33 @@ def causal_conv1d_plan(desc):
     return SeqPlan("causal_conv1d", desc, torch.bfloat16 if desc.dtype == CC3D_BF16 else torch.float32)
 
 
-def _conv1d_args(plan, x, w, b, cache_in, lengths):
-    d, dt = _plan_of(plan, "causal_conv1d").desc, plan.dtype
-    dev = _device_of(x, "x")
-    a = Conv1dArgs()
-    seq, cache = (d.n, d.t, d.c), (d.n, d.k - 1, d.c)
-    _set_seq(a, "x", x, seq, dt, dev)
-    _set_dense(a, "w", w, (d.k, d.c), dt, dev)
-    _set_dense(a, "b", b, (d.c,), dt, dev)
-    _set_dense(a, "cache_in", cache_in, cache, dt, dev)
-    _set_dense(a, "lengths", lengths, (d.n,), torch.int32, dev)
-    return a, d, dt, dev, seq, cache
-
-
 def causal_conv1d_forward(plan, x, w, b, y, cache_in=None, cache_out=None, lengths=None, stream=None):
     """y = act(b + sum_k w[k] * [cache_in; x][t + k]); cache_out receives the
     last k - 1 tokens of [cache_in; x].  b may be None."""
-    a, _, dt, dev, seq, cache = _conv1d_args(plan, x, w, b, cache_in, lengths)
-    _set_seq(a, "y", y, seq, dt, dev)
-    _set_dense(a, "cache_out", cache_out, cache, dt, dev)
-    _call(_lib.causal_conv1d_forward, "causal_conv1d_forward", plan, a, dev, stream)
+    sh, ty = _plan_of(plan, "causal_conv1d")
+    dev = _device_of(x, "x")
+    seq, cache = sh["seq"], sh["cache"]
+    args = Conv1dArgs.pack(
+        *_seq(x, "x", seq, ty, dev), *_seq(y, "y", seq, ty, dev), 0, 0, 0, 0, 0, 0, _dense(w, "w", sh["w"], ty, dev),
+        _dense(b, "b", sh["c"], ty, dev), _dense(cache_in, "cache_in", cache, ty, dev),
+        _dense(cache_out, "cache_out", cache, ty, dev), 0, 0, 0, 0, _dense(lengths, "lengths", sh["n"], _I32, dev), 0, 0)
+    _call(_lib.causal_conv1d_forward, "causal_conv1d_forward", plan, args, dev, stream)
 
 
 def causal_conv1d_backward(plan, x, w, b, dy, dx=None, dw=None, db=None, cache_in=None, dcache_out=None,
                            dcache_in=None, lengths=None, workspace=None, stream=None):
     """Gradients of causal_conv1d_forward into dx, dcache_in (the plan's
     dtype) and dw, db (fp32); each may be None."""
-    a, d, dt, dev, seq, cache = _conv1d_args(plan, x, w, b, cache_in, lengths)
-    _set_seq(a, "dy", dy, seq, dt, dev)
-    _set_seq(a, "dx", dx, seq, dt, dev)
-    _set_dense(a, "dcache_out", dcache_out, cache, dt, dev)
-    _set_dense(a, "dcache_in", dcache_in, cache, dt, dev)
-    _set_dense(a, "dw", dw, (d.k, d.c), torch.float32, dev)
-    _set_dense(a, "db", db, (d.c,), torch.float32, dev)
-    _set_workspace(a, workspace, plan.info["backward_workspace_bytes"], dev)
-    _call(_lib.causal_conv1d_backward, "causal_conv1d_backward", plan, a, dev, stream)
+    sh, ty = _plan_of(plan, "causal_conv1d")
+    dev = _device_of(x, "x")
+    seq, cache = sh["seq"], sh["cache"]
+    args = Conv1dArgs.pack(
+        *_seq(x, "x", seq, ty, dev), 0, 0, 0, *_seq(dy, "dy", seq, ty, dev), *_seq(dx, "dx", seq, ty, dev),
+        _dense(w, "w", sh["w"], ty, dev), _dense(b, "b", sh["c"], ty, dev), _dense(cache_in, "cache_in", cache, ty, dev),
+        0, _dense(dcache_out, "dcache_out", cache, ty, dev), _dense(dcache_in, "dcache_in", cache, ty, dev),
+        _dense(dw, "dw", sh["w"], _F32, dev), _dense(db, "db", sh["c"], _F32, dev),
+        _dense(lengths, "lengths", sh["n"], _I32, dev), *_space(workspace, plan.info["backward_workspace_bytes"], dev))
+    _call(_lib.causal_conv1d_backward, "causal_conv1d_backward", plan, args, dev, stream)
 
 
 # --------------------------------------------------------------------------
@@ -285,37 +308,22 @@ def selective_scan_plan(desc):
     return SeqPlan("selective_scan", desc, torch.bfloat16 if desc.dtype == CC3D_BF16 else torch.float32)
 
 
-def _scan_args(plan, u, dt, a, b, c, d, z, dt_bias, h_in, lengths):
-    ds, ty = _plan_of(plan, "selective_scan").desc, plan.dtype
-    dev = _device_of(u, "u")
-    f32 = torch.float32
-    g = ScanArgs()
-    seq, split = (ds.n, ds.t, ds.d), (ds.groups, ds.states)
-    bc = (ds.n, ds.t, ds.groups * ds.states)
-    state = (ds.n, ds.d, ds.states)
-    _set_seq(g, "u", u, seq, ty, dev)
-    _set_seq(g, "dt", dt, seq, ty, dev)
-    _set_seq(g, "b", b, bc, ty, dev, split)
-    _set_seq(g, "c", c, bc, ty, dev, split)
-    _set_seq(g, "z", z, seq, ty, dev)
-    _set_dense(g, "a", a, (ds.d, ds.states), f32, dev)
-    _set_dense(g, "d", d, (ds.d,), f32, dev)
-    _set_dense(g, "dt_bias", dt_bias, (ds.d,), f32, dev)
-    _set_dense(g, "h_in", h_in, state, f32, dev)
-    _set_dense(g, "lengths", lengths, (ds.n,), torch.int32, dev)
-    return g, ds, ty, dev, seq, bc, split, state
-
-
 def selective_scan_forward(plan, u, dt, a, b, c, y, d=None, z=None, dt_bias=None, h_in=None, h_out=None, lengths=None,
                            workspace=None, stream=None):
     """y = (sum_s C h + d u) silu(z) with h = exp(delta a) h + delta u B,
     delta = softplus(dt + dt_bias), from h_in; h_out receives the last state
     (it may be the h_in tensor).  A decode step is a plan with t = 1."""
-    g, ds, ty, dev, seq, _, _, state = _scan_args(plan, u, dt, a, b, c, d, z, dt_bias, h_in, lengths)
-    _set_seq(g, "y", y, seq, ty, dev)
-    _set_dense(g, "h_out", h_out, state, torch.float32, dev)
-    _set_workspace(g, workspace, plan.info["workspace_bytes"], dev)
-    _call(_lib.selective_scan_forward, "selective_scan_forward", plan, g, dev, stream)
+    sh, ty = _plan_of(plan, "selective_scan")
+    dev = _device_of(u, "u")
+    seq, bc, split, state, ch = sh["seq"], sh["bc"], sh["split"], sh["state"], sh["c"]
+    args = ScanArgs.pack(
+        *_seq(u, "u", seq, ty, dev), *_seq(dt, "dt", seq, ty, dev), *_seq(b, "b", bc, ty, dev, split),
+        *_seq(c, "c", bc, ty, dev, split), *_seq(z, "z", seq, ty, dev), *_seq(y, "y", seq, ty, dev),
+        0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0,
+        _dense(a, "a", sh["a"], _F32, dev), _dense(d, "d", ch, _F32, dev), _dense(dt_bias, "dt_bias", ch, _F32, dev),
+        _dense(h_in, "h_in", state, _F32, dev), _dense(h_out, "h_out", state, _F32, dev), 0, 0, 0, 0, 0,
+        _dense(lengths, "lengths", sh["n"], _I32, dev), *_space(workspace, plan.info["workspace_bytes"], dev))
+    _call(_lib.selective_scan_forward, "selective_scan_forward", plan, args, dev, stream)
 
 
 def selective_scan_backward(plan, u, dt, a, b, c, dy, d=None, z=None, dt_bias=None, h_in=None, dh_out=None, du=None,
@@ -324,21 +332,20 @@ def selective_scan_backward(plan, u, dt, a, b, c, dy, d=None, z=None, dt_bias=No
     """Gradients of selective_scan_forward, each into the tensor given for it
     (or none): du, ddt, db, dc, dz of the plan's dtype, da, dd, ddt_bias,
     dh_in fp32.  dh_out: gradient of h_out."""
-    g, ds, ty, dev, seq, bc, split, state = _scan_args(plan, u, dt, a, b, c, d, z, dt_bias, h_in, lengths)
-    f32 = torch.float32
-    _set_seq(g, "dy", dy, seq, ty, dev)
-    _set_seq(g, "du", du, seq, ty, dev)
-    _set_seq(g, "ddt", ddt, seq, ty, dev)
-    _set_seq(g, "dz", dz, seq, ty, dev)
-    _set_seq(g, "db", db, bc, ty, dev, split)
-    _set_seq(g, "dc", dc, bc, ty, dev, split)
-    _set_dense(g, "dh_out", dh_out, state, f32, dev)
-    _set_dense(g, "dh_in", dh_in, state, f32, dev)
-    _set_dense(g, "da", da, (ds.d, ds.states), f32, dev)
-    _set_dense(g, "dd", dd, (ds.d,), f32, dev)
-    _set_dense(g, "ddt_bias", ddt_bias, (ds.d,), f32, dev)
-    _set_workspace(g, workspace, plan.info["backward_workspace_bytes"], dev)
-    _call(_lib.selective_scan_backward, "selective_scan_backward", plan, g, dev, stream)
+    sh, ty = _plan_of(plan, "selective_scan")
+    dev = _device_of(u, "u")
+    seq, bc, split, state, ch = sh["seq"], sh["bc"], sh["split"], sh["state"], sh["c"]
+    args = ScanArgs.pack(
+        *_seq(u, "u", seq, ty, dev), *_seq(dt, "dt", seq, ty, dev), *_seq(b, "b", bc, ty, dev, split),
+        *_seq(c, "c", bc, ty, dev, split), *_seq(z, "z", seq, ty, dev), 0, 0, 0, *_seq(dy, "dy", seq, ty, dev),
+        *_seq(du, "du", seq, ty, dev), *_seq(ddt, "ddt", seq, ty, dev), *_seq(dz, "dz", seq, ty, dev),
+        *_seq(db, "db", bc, ty, dev, split), *_seq(dc, "dc", bc, ty, dev, split),
+        _dense(a, "a", sh["a"], _F32, dev), _dense(d, "d", ch, _F32, dev), _dense(dt_bias, "dt_bias", ch, _F32, dev),
+        _dense(h_in, "h_in", state, _F32, dev), 0, _dense(dh_out, "dh_out", state, _F32, dev),
+        _dense(dh_in, "dh_in", state, _F32, dev), _dense(da, "da", sh["a"], _F32, dev), _dense(dd, "dd", ch, _F32, dev),
+        _dense(ddt_bias, "ddt_bias", ch, _F32, dev), _dense(lengths, "lengths", sh["n"], _I32, dev),
+        *_space(workspace, plan.info["backward_workspace_bytes"], dev))
+    _call(_lib.selective_scan_backward, "selective_scan_backward", plan, args, dev, stream)
 
 
 # --------------------------------------------------------------------------
@@ -358,28 +365,21 @@ def norm_join_plan(desc):
     return SeqPlan("norm_join", desc, torch.bfloat16 if desc.dtype == CC3D_BF16 else torch.float32)
 
 
-def _join_args(plan, y, residual, gate, scale, post_w, post_b, pre_w, pre_b):
-    d, ty = _plan_of(plan, "norm_join").desc, plan.dtype
-    dev = _device_of(y, "y") if y is not None else _device_of(residual, "residual")
-    a = JoinArgs()
-    gates = (d.rows + d.gate_rows - 1) // d.gate_rows
-    _set_rows(a, "y", y, d.rows, d.c, ty, dev)
-    _set_rows(a, "residual", residual, d.rows, d.c, ty, dev)
-    _set_rows(a, "gate", gate, gates, d.c, ty, dev)
-    for name, t in (("scale", scale), ("post_w", post_w), ("post_b", post_b), ("pre_w", pre_w), ("pre_b", pre_b)):
-        _set_dense(a, name, t, (d.c,), ty, dev)
-    return a, d, ty, dev, gates
-
-
 def norm_join_forward(plan, y, residual, x_out=None, h_out=None, gate=None, scale=None, post_w=None, post_b=None,
                       pre_w=None, pre_b=None, stream=None):
     """x_out = residual + scale * gate_act(gate) * (norm(y) * post_w + post_b);
     h_out = act(norm(x_out) * pre_w + pre_b).  y None: x_out is residual (a
     block's first norm); residual None: zeros."""
-    a, d, ty, dev, _ = _join_args(plan, y, residual, gate, scale, post_w, post_b, pre_w, pre_b)
-    _set_rows(a, "x_out", x_out, d.rows, d.c, ty, dev)
-    _set_rows(a, "h_out", h_out, d.rows, d.c, ty, dev)
-    _call(_lib.norm_join_forward, "norm_join_forward", plan, a, dev, stream)
+    sh, ty = _plan_of(plan, "norm_join")
+    dev = _device_of(y, "y") if y is not None else _device_of(residual, "residual")
+    rows, c = sh["rows"], sh["c"]
+    args = JoinArgs.pack(
+        *_rows(y, "y", rows, ty, dev), *_rows(residual, "residual", rows, ty, dev),
+        *_rows(gate, "gate", sh["gates"], ty, dev), *_rows(x_out, "x_out", rows, ty, dev),
+        *_rows(h_out, "h_out", rows, ty, dev), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0,
+        _dense(scale, "scale", c, ty, dev), _dense(post_w, "post_w", c, ty, dev), _dense(post_b, "post_b", c, ty, dev),
+        _dense(pre_w, "pre_w", c, ty, dev), _dense(pre_b, "pre_b", c, ty, dev), 0, 0, 0, 0, 0, 0, 0)
+    _call(_lib.norm_join_forward, "norm_join_forward", plan, args, dev, stream)
 
 
 def norm_join_backward(plan, y, residual, dx_out=None, dh=None, gate=None, scale=None, post_w=None, post_b=None,
@@ -388,14 +388,17 @@ def norm_join_backward(plan, y, residual, dx_out=None, dh=None, gate=None, scale
     """Gradients of norm_join_forward from dx_out and dh (either may be None):
     dy, dresidual, dgate of the plan's dtype, the others fp32; each may be
     None."""
-    a, d, ty, dev, gates = _join_args(plan, y, residual, gate, scale, post_w, post_b, pre_w, pre_b)
-    _set_rows(a, "dx_out", dx_out, d.rows, d.c, ty, dev)
-    _set_rows(a, "dh", dh, d.rows, d.c, ty, dev)
-    _set_rows(a, "dy", dy, d.rows, d.c, ty, dev)
-    _set_rows(a, "dresidual", dresidual, d.rows, d.c, ty, dev)
-    _set_rows(a, "dgate", dgate, gates, d.c, ty, dev)
-    for name, t in (("dscale", dscale), ("dpost_w", dpost_w), ("dpost_b", dpost_b), ("dpre_w", dpre_w),
-                    ("dpre_b", dpre_b)):
-        _set_dense(a, name, t, (d.c,), torch.float32, dev)
-    _set_workspace(a, workspace, plan.info["backward_workspace_bytes"], dev)
-    _call(_lib.norm_join_backward, "norm_join_backward", plan, a, dev, stream)
+    sh, ty = _plan_of(plan, "norm_join")
+    dev = _device_of(y, "y") if y is not None else _device_of(residual, "residual")
+    rows, gates, c = sh["rows"], sh["gates"], sh["c"]
+    args = JoinArgs.pack(
+        *_rows(y, "y", rows, ty, dev), *_rows(residual, "residual", rows, ty, dev), *_rows(gate, "gate", gates, ty, dev),
+        0, 0, 0, 0, 0, 0, *_rows(dx_out, "dx_out", rows, ty, dev), *_rows(dh, "dh", rows, ty, dev),
+        *_rows(dy, "dy", rows, ty, dev), *_rows(dresidual, "dresidual", rows, ty, dev),
+        *_rows(dgate, "dgate", gates, ty, dev),
+        _dense(scale, "scale", c, ty, dev), _dense(post_w, "post_w", c, ty, dev), _dense(post_b, "post_b", c, ty, dev),
+        _dense(pre_w, "pre_w", c, ty, dev), _dense(pre_b, "pre_b", c, ty, dev), _dense(dscale, "dscale", c, _F32, dev),
+        _dense(dpost_w, "dpost_w", c, _F32, dev), _dense(dpost_b, "dpost_b", c, _F32, dev),
+        _dense(dpre_w, "dpre_w", c, _F32, dev), _dense(dpre_b, "dpre_b", c, _F32, dev),
+        *_space(workspace, plan.info["backward_workspace_bytes"], dev))
+    _call(_lib.norm_join_backward, "norm_join_backward", plan, args, dev, stream)
