@@ -24,7 +24,7 @@ struct Conv1dArgs {
   int64_t items; // n * nseg
 };
 
-constexpr int kAhead = 4, kBack = 2;
+constexpr int kAhead = 4;
 
 // A thread's eight channels.  Where C is no multiple of eight the last thread
 // takes the last eight, some of which are the thread's before it too: both
@@ -144,6 +144,8 @@ __global__ __launch_bounds__(256) void conv1d_fwd(Conv1dArgs a) {
 // partial sums; sum_rows adds those in their order.
 template <class T, int K, bool FEW, bool SILU>
 __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
+  // tokens loaded at once, and unrolled (whole turns of the rings)
+  constexpr int kBack = K == 3 ? 3 : K > 4 ? 1 : 2, kGroup = K == 1 ? 2 : K;
   __shared__ float red[256 * 8];
   const int lane = threadIdx.x % lanes, line = threadIdx.x / lanes, lines = 256 / lanes;
   const int tiles = (a.vecs + lanes - 1) / lanes;
@@ -178,19 +180,25 @@ __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
     T* dci = a.dcache_in ? static_cast<T*>(a.dcache_in) + cache_at : nullptr;
 
     const int t0 = sg * a.seg, t1 = min(t0 + a.seg, a.t);
-    Lane<T, FEW> win[K];
+    // Rings of the last K tokens: token t0 + i of the run is in place i % K, so
+    // that a group of K tokens, unrolled, moves nothing.
+    float win[K][8], dp[K][8] = {};
 #pragma unroll
-    for (int i = 0; i < K - 1; ++i) {
-      const int s = t0 - (K - 1) + i;
-      win[i].zero();
-      if (s >= 0) {
-        if (s < len) win[i].load(x + int64_t(s) * a.xr, left);
-      } else if (cin) {
-        win[i].load(cin + int64_t(s + K - 1) * a.c, left);
+    for (int i = 0; i < K; ++i) {
+      const int s = t0 - K + i;  // place i, overwritten when i = 0
+      ld.zero();
+      if (i > 0) {
+        if (s >= 0) {
+          if (s < len) ld.load(x + int64_t(s) * a.xr, left);
+        } else if (cin) {
+          ld.load(cin + int64_t(s + K - 1) * a.c, left);
+        }
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) win[i][j] = ld.get(j);
     }
-    float dp[K][8] = {};  // dp[i]: token t - (K - 1) + i
-    // kBack tokens load while kBack are computed; those past the valid ones are read from the last and not used
+    // kBack tokens load while kBack are computed; those past the valid ones are
+    // read from the last and taken as zero
     const int end = t1 + K - 1, last = max(min(end, len) - 1, 0);
     Lane<T, FEW> next_x[kBack], next_d[kBack];
     auto fetch = [&](int from) {
@@ -202,36 +210,37 @@ __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
       }
     };
     fetch(t0);
-    for (int tb = t0; tb < end; tb += kBack) {
-      Lane<T, FEW> now_x[kBack], now_d[kBack];
+    for (int tb = t0; tb < end; tb += kGroup) {
 #pragma unroll
-      for (int i = 0; i < kBack; ++i) {
-        now_x[i] = next_x[i];
-        now_d[i] = next_d[i];
-      }
-      if (tb + kBack < end) fetch(tb + kBack);
-#pragma unroll
-      for (int i = 0; i < kBack; ++i) {
+      for (int i = 0; i < kGroup; ++i) {
         const int t = tb + i;
         if (t >= end) break;
-        win[K - 1] = now_x[i];
-        if (t >= len) win[K - 1].zero();
+        Lane<T, FEW> now_x = next_x[i % kBack], now_d = next_d[i % kBack];
+        if (i % kBack == kBack - 1 && t + 1 < end) fetch(t + 1);
+        if (t >= len) {
+          now_x.zero();
+          now_d.zero();
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float g = now_d[i].get(j);
+          win[i % K][j] = now_x.get(j);
+          float g = now_d.get(j);
           if (SILU) {
             float s = bias[j];
 #pragma unroll
-            for (int k = 0; k < K; ++k) s = fmaf(wt[k][j], win[k].get(j), s);
+            for (int k = 0; k < K; ++k) s = fmaf(wt[k][j], win[(i + 1 + k) % K][j], s);
             const float sg_ = sigmoid_f32(s);
             g *= sg_ * (1.f + s * (1.f - sg_));
           }
-          g = t < len ? g : 0.f;
-          dp[K - 1][j] = g;
-          const float mine = t < t1 ? g : 0.f;  // the K - 1 tokens after the run are another thread's
-          db[j] += mine;
+          dp[i % K][j] = g;
+        }
+        if (t < t1) {  // the K - 1 tokens after the run are another thread's
 #pragma unroll
-          for (int k = 0; k < K; ++k) dw[k][j] = fmaf(mine, win[k].get(j), dw[k][j]);
+          for (int j = 0; j < 8; ++j) {
+            db[j] += dp[i % K][j];
+#pragma unroll
+            for (int k = 0; k < K; ++k) dw[k][j] = fmaf(dp[i % K][j], win[(i + 1 + k) % K][j], dw[k][j]);
+          }
         }
         const int s = t - (K - 1);
         if (s >= t0 || sg == 0) {
@@ -240,7 +249,7 @@ __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
           for (int j = 0; j < 8; ++j) {
             float acc = 0.f;
 #pragma unroll
-            for (int k = 0; k < K; ++k) acc = fmaf(wt[k][j], dp[K - 1 - k][j], acc);
+            for (int k = 0; k < K; ++k) acc = fmaf(wt[k][j], dp[(i + K - k) % K][j], acc);
             v[j] = acc;
           }
           if (dco && s < len && s >= len - (K - 1)) {
@@ -253,12 +262,6 @@ __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
           } else if (dci) {
             Lane<T, FEW>::store(dci + int64_t(s + K - 1) * a.c, v, left);
           }
-        }
-#pragma unroll
-        for (int q = 0; q < K - 1; ++q) {
-          win[q] = win[q + 1];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) dp[q][j] = dp[q + 1][j];
         }
       }
     }

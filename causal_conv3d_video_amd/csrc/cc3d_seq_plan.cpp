@@ -193,12 +193,17 @@ extern "C" cc3d_status_t causal_conv1d_plan(const cc3d_conv1d_desc_t* d, cc3d_co
   auto* p = make_plan<cc3d_conv1d_plan>(d);
   if (!p) return CC3D_ERR_NO_MEMORY;
   p->seg = int32_t(seg);
-  const int64_t bwd_seg = ceildiv(int64_t(d->n) * d->t, ceildiv(int64_t(1) << 18, vecs));
-  p->bwd_seg = int32_t(std::min<int64_t>(std::min<int64_t>(std::max<int64_t>(bwd_seg, 8), 32), d->t));
-  // backward: partial sums of dw and db, one row for each of at most 512 workgroups along the tokens
-  const int64_t items = int64_t(d->n) * ceildiv(d->t, p->bwd_seg);
-  const int64_t lines = 256 / cc3d::conv1d_lanes(d->c);
-  p->bwd_rows = std::min<int64_t>(ceildiv(items, lines), 512);
+  // Backward: two waves a SIMD (its registers allow no more), so 512 workgroups
+  // are one turn of the card: runs are as long as that turn needs, up to 64
+  // tokens, and a workgroup whose tiles are done takes further runs.  (964
+  // workgroups of 17 tokens took 66 us where 500 of 33 take 54.)
+  const int64_t lines = 256 / cc3d::conv1d_lanes(d->c), tiles = ceildiv(vecs, cc3d::conv1d_lanes(d->c));
+  const int64_t rows = std::max<int64_t>(1, 2 * kUnits / tiles), slots = rows * lines;
+  const int64_t turns = ceildiv(int64_t(d->n) * d->t, slots * 64);
+  const int64_t runs = std::max<int64_t>(1, slots * turns / d->n);
+  p->bwd_seg = int32_t(std::min<int64_t>(std::max<int64_t>(ceildiv(d->t, runs), 8), std::min(d->t, 64)));
+  // partial sums of dw and db: one row for each workgroup along the tokens
+  p->bwd_rows = std::min<int64_t>(ceildiv(int64_t(d->n) * ceildiv(d->t, p->bwd_seg), lines), rows);
   p->info.backward_workspace_bytes = p->bwd_rows * (d->k + 1) * int64_t(d->c) * 4;
   p->info.chunks = int32_t(ceildiv(d->t, p->seg));
   p->info.backward_chunks = int32_t(ceildiv(d->t, p->bwd_seg));
@@ -397,7 +402,8 @@ extern "C" cc3d_status_t norm_join_plan(const cc3d_join_desc_t* d, cc3d_join_pla
   } else if (gates >= limit / 2) {
     p->bwd_parts = std::min(limit, gates);
   } else {
-    const int64_t each = std::min(ceildiv(limit, gates), ceildiv(std::min(d->rows, d->gate_rows), at_once));
+    // (rounded down: one workgroup over the limit would be a second turn of the card)
+    const int64_t each = std::min(limit / gates, ceildiv(d->gate_rows, at_once));
     p->gate_parts = each;
     p->bwd_parts = gates * each;
   }
