@@ -190,13 +190,16 @@ __device__ __forceinline__ void spread_rows(const Feed<T, NS, ROWS>& f, float* b
   }
 }
 
-// What a chunk adds to the state, starting from zero: the forward recurrence
-//   h = exp(delta A) h + delta u B
-// or, REV, the gradient's from the chunk's last token back,
-//   g = exp(delta A) (g + gy C),  gy = dy silu(z),
-// and the chunk's sum of delta, whose exponential is the whole chunk's decay.
-template <class T, int NS, bool REV, bool MULTI>
+// What a chunk adds to the state, starting from zero,
+//   h = exp(delta A) h + delta u B,
+// and its sum of delta, whose exponential is the whole chunk's decay.  BACK: also
+// what it adds to the gradient that leaves it on the left,
+//   G = sum_t exp(A sum_{s <= t} delta_s) C gy,  gy = dy silu(z),
+// taken forward too, with the running product of the same decays: one walk and one
+// exponential a token and state serve both.
+template <class T, int NS, bool BACK, bool MULTI>
 __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void scan_carry(ScanArgs a) {
+  constexpr int kRows = BACK ? 2 : 1;
   // (LDS for the waves there are: it would limit how many workgroups a compute unit holds)
   __shared__ __attribute__((aligned(16))) float box_all[MULTI ? cc3d::kScanMaxStates / NS : 1][StateBox<NS>::kSize];
   const Place at(a);
@@ -205,65 +208,88 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
   const int t0 = ch * a.chunk, te = min(min(t0 + a.chunk, a.t), valid_tokens(a, n));
   const int s0 = at.wave * NS, states = min(a.s - s0, NS);
   const float bias = a.bias ? a.bias[at.chan] : 0.f;
-  float h[NS], a2[NS];
+  Stream<T> dt(a.dt, n, t0, at.chan), u(a.u, n, t0, at.chan);
+  Stream<T> z(BACK ? a.z : ScanRows{}, n, t0, at.chan), dy(BACK ? a.dy : ScanRows{}, n, t0, at.chan);
+  Stream<T> bs(a.b, n, t0, 0), cs(BACK ? a.c : a.b, n, t0, 0);
+  bs.p += at.group * a.s + s0;
+  cs.p += at.group * a.s + s0;
+  Feed<T, NS, kRows> next;
+  T next_dy[4];
+  auto fetch = [&](int left) {
+    feed(next, left, dt, u, z, bs, cs, states, at.lane);
+    if constexpr (BACK) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) next_dy[j] = dy.p[dy.off[j < left ? j : 0]];
+    }
+  };
+  if (t0 < te) fetch(te - t0);
+  float h[NS], a2[NS], g[BACK ? NS : 1], through[BACK ? NS : 1];
   load_states<NS>(a.a + int64_t(at.first) * a.s + s0, a.s, states, at.live, at.lane, box, a2);
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     h[i] = 0.f;
     a2[i] *= kLog2e;
+    if constexpr (BACK) {
+      g[i] = 0.f;
+      through[i] = 1.f;
+    }
   }
   float total = 0.f;
-  const int groups = te > t0 ? (te - t0 + 3) / 4 : 0, step = REV ? -1 : 1;
-  const int begin = REV ? groups - 1 : 0;
-  Stream<T> dt(a.dt, n, t0 + 4 * begin, at.chan), x_in(REV ? a.dy : a.u, n, t0 + 4 * begin, at.chan),
-      z_in(REV ? a.z : ScanRows{}, n, t0 + 4 * begin, at.chan), cf(REV ? a.c : a.b, n, t0 + 4 * begin, 0);
-  cf.p += at.group * a.s + s0;
-  Feed<T, NS, 1> next;
-  if (groups) feed(next, te - t0 - 4 * begin, dt, x_in, z_in, cf, cf, states, at.lane);
-  for (int k = 0; k < groups; ++k) {
-    const int tb = t0 + 4 * (REV ? groups - 1 - k : k);
+  for (int tb = t0; tb < te; tb += 4) {
     wave_fence();
     spread_rows(next, box, tb, te, states, at.lane);
-    float delta[4], x[4];
+    float delta[4], x[4], gy[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       delta[j] = tb + j < te ? delta_of(a, to_f32(next.dt[j]) + bias) : 0.f;
-      x[j] = tb + j < te ? to_f32(next.x[j]) : 0.f;
-      if (!REV) x[j] *= delta[j];
+      x[j] = tb + j < te ? delta[j] * to_f32(next.x[j]) : 0.f;
       total += delta[j];
     }
-    if (REV && z_in.p) {
+    if constexpr (BACK) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float z = tb + j < te ? to_f32(next.z[j]) : 0.f;
-        x[j] *= z * sigmoid_f32(z);
+      for (int j = 0; j < 4; ++j) gy[j] = to_f32(next_dy[j]);
+      if (z.p) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float v = to_f32(next.z[j]);
+          gy[j] *= v * sigmoid_f32(v);
+        }
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) gy[j] = tb + j < te ? gy[j] : 0.f;
     }
     wave_fence();
-    if (k + 1 < groups) {
-      dt.move(step);
-      x_in.move(step);
-      z_in.move(z_in.p ? step : 0);
-      cf.move(step);
-      feed(next, te - tb - 4 * step, dt, x_in, z_in, cf, cf, states, at.lane);
+    if (tb + 4 < te) {
+      dt.move(1);
+      u.move(1);
+      z.move(z.p ? 1 : 0);
+      dy.move(BACK ? 1 : 0);
+      bs.move(1);
+      cs.move(1);
+      fetch(te - tb - 4);
     }
 #pragma unroll
-    for (int jj = 0; jj < 4; ++jj) {
-      const int j = REV ? 3 - jj : jj;
+    for (int j = 0; j < 4; ++j) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const float decay = __builtin_amdgcn_exp2f(delta[j] * a2[i]);
-        if (REV) h[i] = decay * fmaf(x[j], box[j * NS + i], h[i]);
-        else h[i] = fmaf(decay, h[i], x[j] * box[j * NS + i]);
+        h[i] = fmaf(decay, h[i], x[j] * box[j * NS + i]);
+        if constexpr (BACK) {
+          through[i] *= decay;
+          g[i] = fmaf(through[i], gy[j] * box[(4 + j) * NS + i], g[i]);
+        }
       }
     }
   }
   const int channels = a.groups * a.wide;
-  float* out = (REV ? a.gcarry : a.carry) + (at.item * a.s + s0) * channels + at.chan;
+  const int64_t out = (at.item * a.s + s0) * channels + at.chan;
 #pragma unroll
   for (int i = 0; i < NS; ++i)
-    if (i < states) out[int64_t(i) * channels] = h[i];
-  if (!REV && at.wave == 0) a.sums[at.item * channels + at.chan] = total;
+    if (i < states) {
+      a.carry[out + int64_t(i) * channels] = h[i];
+      if constexpr (BACK) a.gcarry[out + int64_t(i) * channels] = g[i];
+    }
+  if (at.wave == 0) a.sums[at.item * channels + at.chan] = total;
 }
 
 // Turns what every chunk adds into the state that enters it, from the
@@ -333,11 +359,11 @@ int run_join(const ScanArgs& a, hipStream_t s) {
   return int(hipGetLastError());
 }
 
-template <class T, int NS, bool REV>
+template <class T, int NS, bool BACK>
 int run_carry(const ScanArgs& a, hipStream_t s) {
   const unsigned blocks = unsigned(int64_t(a.groups) * a.tiles_per_group * a.n * a.chunks);
-  if (a.waves > 1) scan_carry<T, NS, REV, true><<<blocks, 64 * a.waves, 0, s>>>(a);
-  else scan_carry<T, NS, REV, false><<<blocks, 64, 0, s>>>(a);
+  if (a.waves > 1) scan_carry<T, NS, BACK, true><<<blocks, 64 * a.waves, 0, s>>>(a);
+  else scan_carry<T, NS, BACK, false><<<blocks, 64, 0, s>>>(a);
   return int(hipGetLastError());
 }
 

@@ -517,8 +517,7 @@ template <class T, int NS>
 int run_carries(const cc3d_scan_plan& p, ScanArgs a, hipStream_t s) {
   a.waves = cc3d::scan_fwd_waves(p.d);
   a.tiles_per_group = cc3d::scan_tiles_per_group(p.d);
-  int e = run_carry<T, NS, false>(a, s);
-  if (!e) e = run_carry<T, NS, true>(a, s);
+  int e = run_carry<T, NS, true>(a, s);
   if (!e) e = run_join<false>(a, s);
   if (!e) e = run_join<true>(a, s);
   return e;
