@@ -88,10 +88,15 @@ __device__ __forceinline__ float sum_groups(const float (&v)[SG]) {
   else return v[0];
 }
 
-// Two neighbouring channels as they are stored.
+// Two neighbouring channels as they are stored; aligned to one (as 16-byte
+// accesses, 4- and 8-byte ones lose little off their alignment).
+typedef unsigned unsigned_by2 __attribute__((aligned(2)));
+typedef unsigned long long ulong_by4 __attribute__((aligned(4)));
+
 template <class T>
 struct Pair {
   using U = std::conditional_t<sizeof(T) == 4, unsigned long long, unsigned>;
+  using Mem = std::conditional_t<sizeof(T) == 4, ulong_by4, unsigned_by2>;
   U v;
   __device__ __forceinline__ float get(int i) const {
     if constexpr (sizeof(T) == 4) return __uint_as_float(unsigned(v >> (32 * i)));
@@ -99,34 +104,34 @@ struct Pair {
   }
 };
 
-// Element `off` (32 bits) after a base that is the same for the whole wave.
-// `whole`: rows of pairs are aligned to a pair.  Otherwise one by one, the
-// second at `step` (0 when there is no second channel).
-template <class T>
-__device__ __forceinline__ Pair<T> load_pair(const T* base, unsigned off, bool whole, int step) {
-  using U = typename Pair<T>::U;
-  Pair<T> r;
-  if (whole) {
-    r.v = *reinterpret_cast<const U*>(base + off);
+// DUO: there are two channels; otherwise the one stands for both.
+template <class T, bool DUO>
+__device__ __forceinline__ Pair<T> load_pair(const T* p) {
+  using P = Pair<T>;
+  P r;
+  if constexpr (DUO) {
+    r.v = *reinterpret_cast<const typename P::Mem*>(p);
   } else if constexpr (sizeof(T) == 4) {
-    r.v = __float_as_uint(base[off]) | U(__float_as_uint(base[off + step])) << 32;
+    r.v = __float_as_uint(*p) * 0x100000001ull;
   } else {
-    r.v = base[off] | U(base[off + step]) << 16;
+    r.v = *p * 0x10001u;
   }
   return r;
 }
 
+// Stores the channels that are this lane's own.
 template <class T>
-__device__ __forceinline__ void store_pair(T* base, unsigned off, float x, float y, bool whole, bool second) {
-  using U = typename Pair<T>::U;
-  if (whole) {
-    U v;
-    if constexpr (sizeof(T) == 4) v = __float_as_uint(x) | U(__float_as_uint(y)) << 32;
+__device__ __forceinline__ void store_pair(T* p, float x, float y, bool own0, bool own1) {
+  using P = Pair<T>;
+  if (own0 && own1) {
+    typename P::U v;
+    if constexpr (sizeof(T) == 4) v = __float_as_uint(x) | typename P::U(__float_as_uint(y)) << 32;
     else v = pack_bf16(x, y);
-    *reinterpret_cast<U*>(base + off) = v;
-  } else {
-    base[off] = from_f32<T>(x);
-    if (second) base[off + 1] = from_f32<T>(y);
+    *reinterpret_cast<typename P::Mem*>(p) = v;
+  } else if (own0) {
+    p[0] = from_f32<T>(x);
+  } else if (own1) {
+    p[1] = from_f32<T>(y);
   }
 }
 
@@ -148,35 +153,66 @@ struct BwdLds {
   }
 };
 
-template <class T, int SG, int SUB>
-__global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc, int whole) {
+template <class T, int SG, int SUB, bool MULTI, bool DUO>
+__global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
   using L = BwdLds<SG, SUB>;
-  constexpr int LC = 64 / SG, CT = 2 * LC, NB = SUB / SG, kDup = LC / 8;
+  constexpr int LC = 64 / SG, CT = 2 * LC, NB = SUB / SG, kDup = LC / 8, kVal = 8 * SG;
   constexpr int kBcEach = (L::kBc + 63) / 64;
   extern __shared__ __attribute__((aligned(16))) float lds[];
-  const L at(a.chunk, a.waves, wc);
+  const int waves = MULTI ? a.waves : 1;
+  const L at(a.chunk, waves, wc);
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int sw = wave % a.waves, cw = wave / a.waves;
+  const int sw = MULTI ? wave % waves : 0, cw = MULTI ? wave / waves : wave;
   const int q = lane / LC, l = lane % LC;
   const int tiles = a.tiles_per_group * a.groups, tile = blockIdx.x % tiles, worker = blockIdx.x / tiles;
   const int group = tile / a.tiles_per_group;
+  // Channels chan and chan + 1.  In a group of odd width the last lane's first
+  // channel is also the lane's before it, and not its own; lanes past the
+  // group own none.
   const int in_group = ((tile - group * a.tiles_per_group) * wc + cw) * CT + 2 * l;
-  const bool on = in_group < a.wide, on2 = in_group + 1 < a.wide;
-  const int chan = group * a.wide + (on ? in_group : 0), step = on2 ? 1 : 0;
+  const int chan = group * a.wide + (DUO ? min(in_group, a.wide - 2) : 0), other = DUO ? 1 : 0;
+  const bool own[2] = {in_group < a.wide && (!DUO || in_group + 1 < a.wide), DUO && in_group < a.wide};
   const int channels = a.groups * a.wide;
   const int s0 = sw * 4 * SG + q * 4;  // this lane's first state
   f32x4_s* kept = reinterpret_cast<f32x4_s*>(lds + wave * at.per_wave) + lane;
   float* tok = lds + wave * at.per_wave + at.kept;
   float* bc = tok + L::kTok;
+  // where this lane's sums over channels go: kDup tokens a store, one for each
+  // copy; [channel wave][token][state wave][which][4 SG]
+  const int copy = lane & (kDup - 1), value = l / kDup;
+  const int comb_at = (cw * SUB + copy) * waves * kVal + sw * kVal + (value >> 2) * (4 * SG) + q * 4 + (value & 3);
 
   float bias[2], skip[2], a2[2][4], da[2][4] = {}, dd[2] = {}, dbias[2] = {};
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    bias[c] = a.bias ? a.bias[chan + c * step] : 0.f;
-    skip[c] = a.d ? a.d[chan + c * step] : 0.f;
+    bias[c] = a.bias ? a.bias[chan + c * other] : 0.f;
+    skip[c] = a.d ? a.d[chan + c * other] : 0.f;
+    const float* p = a.a + int64_t(chan + c * other) * a.s + s0;
+    if (a.s % 4 == 0 && reinterpret_cast<uintptr_t>(a.a) % 16 == 0) {
+      const f32x4_s v = s0 < a.s ? *reinterpret_cast<const f32x4_s*>(p) : f32x4_s{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      a2[c][i] = s0 + i < a.s ? a.a[int64_t(chan + c * step) * a.s + s0 + i] * kLog2e : 0.f;
+      for (int i = 0; i < 4; ++i) a2[c][i] = v[i] * kLog2e;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a2[c][i] = s0 + i < a.s ? p[i] * kLog2e : 0.f;
+    }
+  }
+  // (a branch costs more here than what it saves: flags select)
+  const bool soft = a.softplus, gated = a.z.p != nullptr;
+  const ScanRows& zrows = gated ? a.z : a.dy;
+  // this lane's places behind a walk's first token: its own tokens' channel
+  // pair in every stream (token q of each SG), and its share of B and C
+  auto own_at = [&](const ScanRows& v) { return unsigned(q) * unsigned(v.row) + unsigned(chan); };
+  const unsigned o_dt = own_at(a.dt), o_u = own_at(a.u), o_z = own_at(zrows), o_dy = own_at(a.dy);
+  const unsigned o_du = own_at(a.du), o_ddt = own_at(a.ddt), o_dz = own_at(a.dz);
+  unsigned o_bc[kBcEach];
+  int t_bc[kBcEach];  // its token of the walk; none of it where there is no such state
+#pragma unroll
+  for (int r = 0; r < kBcEach; ++r) {
+    const int i = lane + 64 * r, which = i / (L::kBc / 2), t = i / (4 * SG) % SUB, s = i % (4 * SG);
+    const bool in = i < L::kBc && sw * 4 * SG + s < a.s;
+    o_bc[r] = in ? unsigned(t) * unsigned(which ? a.c.row : a.b.row) + unsigned(s) : 0;
+    t_bc[r] = in ? t : SUB;
   }
   int turn = 0;
 
@@ -184,69 +220,90 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc, int whole
     const int n = int(item / a.chunks), ch = int(item - int64_t(n) * a.chunks);
     const int t0 = ch * a.chunk, t1 = min(t0 + a.chunk, a.t), te = min(t1, valid_tokens(a, n));
     const int subs = te > t0 ? (te - t0 + SUB - 1) / SUB : 0;
-    // token t0 of the chunk: the same address for the whole wave, with 32-bit offsets behind it
-    auto at_chunk = [&](const ScanRows& v) { return static_cast<T*>(v.p) + int64_t(n) * v.batch + int64_t(t0) * v.row; };
-    const T* bp = at_chunk(a.b) + group * a.s + sw * 4 * SG;
-    const T* cp = at_chunk(a.c) + group * a.s + sw * 4 * SG;
-    const T *dt = at_chunk(a.dt), *u = at_chunk(a.u), *z = a.z.p ? at_chunk(a.z) : nullptr, *dy = at_chunk(a.dy);
-    T* du_o = a.du.p ? at_chunk(a.du) : nullptr;
-    T* ddt_o = a.ddt.p ? at_chunk(a.ddt) : nullptr;
-    T* dz_o = a.dz.p ? at_chunk(a.dz) : nullptr;
-    auto off = [&](const ScanRows& v, int t) { return unsigned(t - t0) * unsigned(v.row) + unsigned(chan); };
-    float* pbc = a.part_bc + (int64_t(tile) * a.n + n) * a.t * a.waves * (8 * SG);
+    // a walk's first token: the same address for the whole wave
+    auto walk = [&](const ScanRows& v, int k) {
+      return static_cast<T*>(v.p) + int64_t(n) * v.batch + int64_t(t0 + k * SUB) * v.row;
+    };
+    float* pbc = a.part_bc + (int64_t(tile) * a.n + n) * a.t * waves * kVal;
 
-    // inputs of the tokens of one walk: this lane group's tokens, and this lane's share of B and C
+    // Inputs of the tokens of one walk: this lane group's tokens, and this
+    // lane's share of B and C.  Tokens past the valid ones are read where they
+    // are (and not used); past the tensor, the walk's first is read instead.
     Pair<T> rdt[NB], ru[NB], rz[NB], rdy[NB];
     T rbc[kBcEach];
-    auto fetch = [&](int tb, bool back) {
+    auto fetch = [&](int k, auto back) {
+      const int there = a.t - t0 - k * SUB;
+      const T *dt = walk(a.dt, k), *u = walk(a.u, k), *z = walk(zrows, k), *dy = walk(a.dy, k);
+      const T *bp = walk(a.b, k) + group * a.s + sw * 4 * SG, *cp = walk(a.c, k) + group * a.s + sw * 4 * SG;
+      auto at_token = [&](const T* p, const ScanRows& v, unsigned o, int b) {
+        return load_pair<T, DUO>(p + int64_t(b * SG) * v.row + o);
+      };
+      if (there >= SUB) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int t = tb + b * SG + q;
-        rdt[b] = ru[b] = rz[b] = rdy[b] = Pair<T>{};
-        if (t < te) {
-          rdt[b] = load_pair(dt, off(a.dt, t), whole, step);
-          ru[b] = load_pair(u, off(a.u, t), whole, step);
-          if (back) {
-            if (z) rz[b] = load_pair(z, off(a.z, t), whole, step);
-            rdy[b] = load_pair(dy, off(a.dy, t), whole, step);
+        for (int b = 0; b < NB; ++b) {
+          rdt[b] = at_token(dt, a.dt, o_dt, b);
+          ru[b] = at_token(u, a.u, o_u, b);
+          if constexpr (back.value) {
+            rz[b] = at_token(z, zrows, o_z, b);
+            rdy[b] = at_token(dy, a.dy, o_dy, b);
           }
         }
-      }
 #pragma unroll
-      for (int r = 0; r < kBcEach; ++r) {
-        const int i = lane + 64 * r, half = L::kBc / 2;
-        const int which = i / half, t = tb + i % half / (4 * SG), s = i % (4 * SG);
-        rbc[r] = T(0);
-        if (i < L::kBc && t < te && sw * 4 * SG + s < a.s && (back || !which))
-          rbc[r] = which ? cp[unsigned(t - t0) * unsigned(a.c.row) + s] : bp[unsigned(t - t0) * unsigned(a.b.row) + s];
+        for (int r = 0; r < kBcEach; ++r) {
+          // (whole rows of 64 lanes are B or C alike, but for a single one)
+          const bool which = kBcEach == 1 ? lane >= L::kBc / 2 : 64 * r >= L::kBc / 2;
+          if (back.value || kBcEach == 1 || !which) rbc[r] = (which ? cp : bp)[o_bc[r]];
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const bool in = b * SG + q < there;
+          auto clamped = [&](const T* p, const ScanRows& v, unsigned o) {
+            return load_pair<T, DUO>(p + (in ? int64_t(b * SG) * v.row + o : int64_t(chan)));
+          };
+          rdt[b] = clamped(dt, a.dt, o_dt);
+          ru[b] = clamped(u, a.u, o_u);
+          if constexpr (back.value) {
+            rz[b] = clamped(z, zrows, o_z);
+            rdy[b] = clamped(dy, a.dy, o_dy);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kBcEach; ++r) {
+          const bool which = kBcEach == 1 ? lane >= L::kBc / 2 : 64 * r >= L::kBc / 2;
+          rbc[r] = (which ? cp : bp)[t_bc[r] < there ? o_bc[r] : 0];
+        }
       }
     };
     // what every lane group needs of them, into LDS
-    auto spread = [&](int tb, bool back) {
+    auto spread = [&](int k, auto back) {
+      const int left = te - t0 - k * SUB;
       wave_fence();
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int j = b * SG + q;
-        const bool in = tb + j < te;
+        const bool in = j < left;
+        float delta[2], x[2], gy[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const bool real = in && (c ? on2 : on);
-          const float delta = real ? delta_of(a, rdt[b].get(c) + bias[c]) : 0.f;
-          tok[j * CT + 2 * l + c] = delta;
-          tok[(SUB + j) * CT + 2 * l + c] = real ? delta * ru[b].get(c) : 0.f;
-          if (back) {
-            float gy = rdy[b].get(c);
-            if (z) {
-              const float zz = rz[b].get(c);
-              gy *= zz * sigmoid_f32(zz);
-            }
-            tok[(2 * SUB + j) * CT + 2 * l + c] = real ? gy : 0.f;
+          const float raw = rdt[b].get(c) + bias[c], plus = softplus_f32(raw);
+          const bool real = in && own[c];
+          delta[c] = real ? (soft ? plus : raw) : 0.f;
+          x[c] = real ? delta[c] * ru[b].get(c) : 0.f;
+          if constexpr (back.value) {
+            const float zz = rz[b].get(c), gate = zz * sigmoid_f32(zz);
+            gy[c] = real ? rdy[b].get(c) * (gated ? gate : 1.f) : 0.f;
           }
         }
+        *reinterpret_cast<float2*>(tok + j * CT + 2 * l) = make_float2(delta[0], delta[1]);
+        *reinterpret_cast<float2*>(tok + (SUB + j) * CT + 2 * l) = make_float2(x[0], x[1]);
+        if constexpr (back.value) *reinterpret_cast<float2*>(tok + (2 * SUB + j) * CT + 2 * l) = make_float2(gy[0], gy[1]);
       }
 #pragma unroll
-      for (int r = 0; r < kBcEach; ++r)
-        if (L::kBc % 64 == 0 || lane + 64 * r < L::kBc) bc[lane + 64 * r] = to_f32(rbc[r]);
+      for (int r = 0; r < kBcEach; ++r) {
+        const float v = t_bc[r] < min(left, SUB) ? to_f32(rbc[r]) : 0.f;
+        if (L::kBc % 64 == 0 || lane + 64 * r < L::kBc) bc[lane + 64 * r] = v;
+      }
       wave_fence();
     };
     auto pair_at = [&](int kind, int j) {
@@ -255,13 +312,17 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc, int whole
     auto states_at = [&](int which, int j) {
       return *reinterpret_cast<const f32x4_s*>(bc + (which * SUB + j) * (4 * SG) + 4 * q);
     };
+    const std::true_type yes{};
+    const std::false_type no{};
 
+    if (subs == 1) fetch(0, yes);
+    else if (subs > 1) fetch(0, no);
     float h[2][4] = {}, g[2][4] = {};
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (!(c ? on2 : on) || s0 + i >= a.s) continue;
+        if (!own[c] || s0 + i >= a.s) continue;
         if (a.chunks > 1) {
           const int64_t k = (item * a.s + s0 + i) * channels + chan + c;
           h[c][i] = a.carry[k];
@@ -274,12 +335,12 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc, int whole
       }
 
     // forward, to the states before every SUB tokens
-    if (subs > 0) fetch(t0, subs == 1);
     for (int k = 0; k < subs - 1; ++k) {
       kept[(2 * k) * 64] = f32x4_s{h[0][0], h[0][1], h[0][2], h[0][3]};
       kept[(2 * k + 1) * 64] = f32x4_s{h[1][0], h[1][1], h[1][2], h[1][3]};
-      spread(t0 + k * SUB, false);
-      fetch(t0 + (k + 1) * SUB, k + 1 == subs - 1);
+      spread(k, no);
+      if (k + 1 == subs - 1) fetch(k + 1, yes);
+      else fetch(k + 1, no);
 #pragma unroll
       for (int j = 0; j < SUB; ++j) {
         const float2 delta = pair_at(0, j), x = pair_at(1, j);
@@ -295,7 +356,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc, int whole
     // and back
     for (int k = subs - 1; k >= 0; --k) {
       const int tb = t0 + k * SUB;
-      spread(tb, true);
+      spread(k, yes);
       Pair<T> mdt[NB], mu[NB], mz[NB], mdy[NB];  // this walk's, while the next one's load
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -304,7 +365,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc, int whole
         mz[b] = rz[b];
         mdy[b] = rdy[b];
       }
-      if (k > 0) fetch(tb - SUB, true);
+      if (k > 0) fetch(k - 1, yes);
       if (k < subs - 1) {
         const f32x4_s x = kept[(2 * k) * 64], y = kept[(2 * k + 1) * 64];
 #pragma unroll
@@ -365,88 +426,87 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc, int whole
         }
       }
 
-      // dB and dC: kDup tokens a store, one for each copy; value = which * 4 SG + q * 4 + state
-      float* comb = lds + at.comb + (turn * a.waves * wc + wave) * L::kComb;
-      const int copy = lane & (kDup - 1), value = l / kDup;  // value: which, state
+      float* comb = lds + at.comb + turn * waves * wc * L::kComb;
 #pragma unroll
       for (int j0 = 0; j0 < SUB; j0 += kDup) {
         float v = bcsum[j0];
 #pragma unroll
         for (int i = 1; i < kDup && j0 + i < SUB; ++i) v = copy == i ? bcsum[j0 + i] : v;
-        if (j0 + copy < SUB) comb[(j0 + copy) * (8 * SG) + (value >> 2) * (4 * SG) + q * 4 + (value & 3)] = v;
+        if (SUB >= kDup || copy < SUB) comb[j0 * waves * kVal + comb_at] = v;
       }
-      float* meet = lds + at.meet + turn * a.waves * wc * L::kMeet;
-      if (a.waves > 1) {
+      float* meet = lds + at.meet + turn * waves * wc * L::kMeet;
+      if constexpr (MULTI) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int i = 0; i < 6; ++i) meet[((wave * NB + b) * 6 + i) * 64 + lane] = sums[b][i];
       }
       __syncthreads();
-      {
-        const float* all = lds + at.comb + turn * a.waves * wc * L::kComb;
-        const int threads = 64 * a.waves * wc;
-        for (int i = threadIdx.x; i < a.waves * L::kComb; i += threads) {
-          const int w = i / L::kComb, r = i - w * L::kComb, j = r / (8 * SG), t = tb + j;
-          float s = all[w * L::kComb + r];
-          for (int o = 1; o < wc; ++o) s += all[(o * a.waves + w) * L::kComb + r];
-          if (t < t1) pbc[(int64_t(t) * a.waves + w) * (8 * SG) + r % (8 * SG)] = s;
-        }
+      const int more = waves * L::kComb;
+      for (int i = threadIdx.x; i < more; i += 64 * waves * wc) {
+        float s = comb[i];
+        if (wc == 4) s += comb[more + i] + comb[2 * more + i] + comb[3 * more + i];
+        else if (wc == 2) s += comb[more + i];
+        if (i < (t1 - tb) * waves * kVal) pbc[int64_t(tb) * waves * kVal + i] = s;
       }
+      T *du_o = walk(a.du, k), *ddt_o = walk(a.ddt, k), *dz_o = walk(a.dz, k);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        if (b % a.waves != sw) continue;
-        if (a.waves > 1) {
+        if constexpr (MULTI) {
+          if (b % waves != sw) continue;
 #pragma unroll
           for (int i = 0; i < 6; ++i) {
             float s = 0.f;
-            for (int w = 0; w < a.waves; ++w) s += meet[(((cw * a.waves + w) * NB + b) * 6 + i) * 64 + lane];
+            for (int w = 0; w < waves; ++w) s += meet[(((cw * waves + w) * NB + b) * 6 + i) * 64 + lane];
             sums[b][i] = s;
           }
         }
-        const int j = b * SG + q, t = tb + j;
-        if (t >= t1 || !on) continue;
-        const bool in = t < te;
+        const int j = b * SG + q;
+        const bool in = j < te - tb;
+        const float2 delta2 = pair_at(0, j), gy2 = pair_at(2, j);
+        const float delta[2] = {delta2.x, delta2.y}, gy[2] = {gy2.x, gy2.y};
         float du[2], ddt[2], dz[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float raw = mdt[b].get(c) + bias[c], uu = mu[b].get(c);
-          const float delta = tok[j * CT + 2 * l + c], gy = tok[(2 * SUB + j) * CT + 2 * l + c];
-          const bool real = in && (c ? on2 : on);
-          ddt[c] = fmaf(sums[b][4 + c], kLn2, uu * sums[b][2 + c]);
-          if (a.softplus && !(raw > 20.f)) ddt[c] *= sigmoid_f32(raw);
-          ddt[c] = real ? ddt[c] : 0.f;
-          du[c] = real ? fmaf(skip[c], gy, delta * sums[b][2 + c]) : 0.f;
-          if (real) dd[c] = fmaf(gy, uu, dd[c]);
+          const float raw = mdt[b].get(c) + bias[c], uu = mu[b].get(c), zz = mz[b].get(c);
+          const bool real = in && own[c];
+          const float slope = sigmoid_f32(raw), sg = sigmoid_f32(zz);
+          const float d = fmaf(sums[b][4 + c], kLn2, uu * sums[b][2 + c]);
+          ddt[c] = real ? d * (soft && !(raw > 20.f) ? slope : 1.f) : 0.f;
+          du[c] = real ? fmaf(skip[c], gy[c], delta[c] * sums[b][2 + c]) : 0.f;
+          dd[c] = real ? fmaf(gy[c], uu, dd[c]) : dd[c];
           dbias[c] += ddt[c];
-          dz[c] = 0.f;
-          if (z && real) {
-            const float zz = mz[b].get(c), sg = sigmoid_f32(zz);
-            dz[c] = mdy[b].get(c) * fmaf(skip[c], uu, sums[b][c]) * (sg * (1.f + zz * (1.f - sg)));
-          }
+          const float y_all = fmaf(skip[c], uu, sums[b][c]);
+          dz[c] = real ? mdy[b].get(c) * y_all * (sg * (1.f + zz * (1.f - sg))) : 0.f;
         }
-        if (du_o) store_pair(du_o, off(a.du, t), du[0], du[1], whole, on2);
-        if (ddt_o) store_pair(ddt_o, off(a.ddt, t), ddt[0], ddt[1], whole, on2);
-        if (dz_o) store_pair(dz_o, off(a.dz, t), dz[0], dz[1], whole, on2);
+        if (j < t1 - tb) {
+          if (a.du.p) store_pair(du_o + int64_t(b * SG) * a.du.row + o_du, du[0], du[1], own[0], own[1]);
+          if (a.ddt.p) store_pair(ddt_o + int64_t(b * SG) * a.ddt.row + o_ddt, ddt[0], ddt[1], own[0], own[1]);
+          if (a.dz.p) store_pair(dz_o + int64_t(b * SG) * a.dz.row + o_dz, dz[0], dz[1], own[0], own[1]);
+        }
       }
       turn ^= 1;
     }
 
     // tokens after the valid ones that no walk held
-    for (int t = t0 + subs * SUB + q; t < t1; t += SG) {
-      if (sw != 0 || !on) continue;
-      if (du_o) store_pair(du_o, off(a.du, t), 0.f, 0.f, whole, on2);
-      if (ddt_o) store_pair(ddt_o, off(a.ddt, t), 0.f, 0.f, whole, on2);
-      if (dz_o) store_pair(dz_o, off(a.dz, t), 0.f, 0.f, whole, on2);
+    if (subs * SUB < t1 - t0) {
+      T *du_o = walk(a.du, subs), *ddt_o = walk(a.ddt, subs), *dz_o = walk(a.dz, subs);
+      for (int j = q; j < t1 - t0 - subs * SUB; j += SG) {
+        if (sw != 0) continue;
+        const unsigned on = unsigned(j - q);
+        if (a.du.p) store_pair(du_o + (o_du + on * unsigned(a.du.row)), 0.f, 0.f, own[0], own[1]);
+        if (a.ddt.p) store_pair(ddt_o + (o_ddt + on * unsigned(a.ddt.row)), 0.f, 0.f, own[0], own[1]);
+        if (a.dz.p) store_pair(dz_o + (o_dz + on * unsigned(a.dz.row)), 0.f, 0.f, own[0], own[1]);
+      }
+      const int64_t first = int64_t(t0 + subs * SUB) * waves * kVal, last = int64_t(t1) * waves * kVal;
+      for (int64_t i = first + threadIdx.x; i < last; i += 64 * waves * wc) pbc[i] = 0.f;
     }
-    const int64_t first = int64_t(t0 + subs * SUB) * a.waves * (8 * SG), last = int64_t(t1) * a.waves * (8 * SG);
-    for (int64_t i = first + threadIdx.x; i < last; i += 64 * a.waves * wc) pbc[i] = 0.f;
     if (ch == 0 && a.dh_in) {
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if ((c ? on2 : on) && s0 + i < a.s) a.dh_in[(int64_t(n) * channels + chan + c) * a.s + s0 + i] = g[c][i];
+          if (own[c] && s0 + i < a.s) a.dh_in[(int64_t(n) * channels + chan + c) * a.s + s0 + i] = g[c][i];
     }
   }
 
@@ -459,13 +519,13 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc, int whole
       w[i] = dbias[c];
     }
     const float sum_d = sum_groups<SG>(s), sum_b = sum_groups<SG>(w);
-    if (!(c ? on2 : on)) continue;
+    if (!own[c]) continue;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (s0 + i < a.s) a.part_a[(int64_t(worker) * channels + chan + c) * a.s + s0 + i] = da[c][i];
     if (q == 0) {
-      a.part_d[(int64_t(worker) * a.waves + sw) * channels + chan + c] = sum_d;
-      a.part_bias[(int64_t(worker) * a.waves + sw) * channels + chan + c] = sum_b;
+      a.part_d[(int64_t(worker) * waves + sw) * channels + chan + c] = sum_d;
+      a.part_bias[(int64_t(worker) * waves + sw) * channels + chan + c] = sum_b;
     }
   }
 }
@@ -489,19 +549,11 @@ __global__ __launch_bounds__(256) void bc_sum(ScanArgs a, ScanRows db, ScanRows 
   static_cast<T*>(out.p)[n * out.batch + t * out.row + gs] = from_f32<T>(sum);
 }
 
-// Every row of pairs starts on a multiple of a pair.
-bool pairs_whole(const ScanArgs& a, int elem) {
-  if (a.wide % 2) return false;
-  for (const ScanRows* v : {&a.u, &a.dt, &a.z, &a.dy, &a.du, &a.ddt, &a.dz})
-    if (v->p && (reinterpret_cast<uintptr_t>(v->p) % (2 * elem) || v->batch % 2 || v->row % 2)) return false;
-  return true;
-}
-
-template <class T, int SG, int SUB>
-int run_main(const ScanArgs& a, const cc3d::ScanBwdShape& v, hipStream_t s) {
+template <class T, int SG, int SUB, bool MULTI, bool DUO>
+int launch_main(const ScanArgs& a, const cc3d::ScanBwdShape& v, hipStream_t s) {
   const int lds = 4 * BwdLds<SG, SUB>(a.chunk, v.waves, v.wc).total;
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&scan_bwd<T, SG, SUB>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&scan_bwd<T, SG, SUB, MULTI, DUO>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) {
       (void)hipGetLastError();  // leave no error for the caller's next runtime call
@@ -509,8 +561,13 @@ int run_main(const ScanArgs& a, const cc3d::ScanBwdShape& v, hipStream_t s) {
     }
   }
   const int64_t tiles = int64_t(a.groups) * a.tiles_per_group;
-  scan_bwd<T, SG, SUB><<<unsigned(tiles * a.workers), 64 * v.waves * v.wc, lds, s>>>(a, v.wc, pairs_whole(a, sizeof(T)));
+  scan_bwd<T, SG, SUB, MULTI, DUO><<<unsigned(tiles * a.workers), 64 * v.waves * v.wc, lds, s>>>(a, v.wc);
   return int(hipGetLastError());
+}
+
+template <class T, int SG, int SUB, bool MULTI>
+int run_main(const ScanArgs& a, const cc3d::ScanBwdShape& v, hipStream_t s) {
+  return a.wide > 1 ? launch_main<T, SG, SUB, MULTI, true>(a, v, s) : launch_main<T, SG, SUB, MULTI, false>(a, v, s);
 }
 
 template <class T, int NS>
@@ -536,9 +593,9 @@ int run_scan_bwd(const cc3d_scan_plan& p, ScanArgs& a, const cc3d_scan_args_t& c
     if (e) return e;
   }
   switch (v.sg) {
-    case 1: e = run_main<T, 1, 4>(a, v, s); break;
-    case 2: e = run_main<T, 2, 8>(a, v, s); break;
-    default: e = run_main<T, 4, 8>(a, v, s);
+    case 1: e = run_main<T, 1, 4, false>(a, v, s); break;
+    case 2: e = run_main<T, 2, 8, false>(a, v, s); break;
+    default: e = v.waves > 1 ? run_main<T, 4, 8, true>(a, v, s) : run_main<T, 4, 8, false>(a, v, s);
   }
   if (!e && (c.db.p || c.dc.p)) {
     const int64_t values = int64_t(a.n) * a.t * 2 * a.groups * a.s;
