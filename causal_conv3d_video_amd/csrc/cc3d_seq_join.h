@@ -196,7 +196,7 @@ inline JoinArgs join_args(const cc3d_join_plan& p, const cc3d_join_args_t& c) {
   a.post = p.d.post;
   a.pre = p.d.pre;
   a.act = p.d.act;
-  a.gate_act = p.d.gate_act;
+  a.gate_act = c.gate.p ? p.d.gate_act : int(CC3D_ACT_NONE);  // without a gate its factor is one
   a.eps = p.d.eps;
   a.inv_c = 1.f / float(p.d.c);
   return a;
