@@ -280,7 +280,7 @@ extern "C" cc3d_status_t selective_scan_plan(const cc3d_scan_desc_t* d, cc3d_sca
   const int64_t bwd_chunks = ceildiv(d->t, bw.chunk);
   const int64_t bwd_tiles = int64_t(d->groups) * bw.tiles_per_group;
   if (int64_t(d->n) * std::max(chunks, bwd_chunks) > kMaxBlocks / tiles ||
-      int64_t(d->n) * d->states > kMaxBlocks / ceildiv(d->d, 64) || int64_t(d->n) * ceildiv(d->d, 16) > kMaxBlocks / 4)
+      int64_t(d->n) * d->states > kMaxBlocks / 2 / ceildiv(d->d, 64) || int64_t(d->n) * ceildiv(d->d, 16) > kMaxBlocks / 4)
     return refuse(CC3D_ERR_UNSUPPORTED);
   auto* p = make_plan<cc3d_scan_plan>(d);
   if (!p) return CC3D_ERR_NO_MEMORY;

@@ -293,26 +293,28 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
 }
 
 // Turns what every chunk adds into the state that enters it, from the
-// sequence's first state on (REV: the gradient that enters it from the right).
+// sequence's first state on, and, in the grid's second half where there is one,
+// the gradient that enters it from the right.
 // A workgroup takes 64 channels of one state; each wave loads 16 chunks at
 // once and joins them, and the waves' joined stretches meet in LDS, so the
 // loads of a long sequence are not one after another.
 constexpr int kJoinChunks = 16, kJoinWaves = 16;
 
-template <bool REV>
-__global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a) {
+__global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a, unsigned half) {
   __shared__ float add_of[kJoinWaves][64], sum_of[kJoinWaves][64];
   const int channels = a.groups * a.wide, tiles = (channels + 63) / 64;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, waves = blockDim.x / 64;
-  // blockIdx.x = (n * S + state) * tiles + tile
-  const int64_t rest = blockIdx.x / tiles;
-  const int tile = int(blockIdx.x - rest * tiles), n = int(rest / a.s), s = int(rest - int64_t(n) * a.s);
+  // block = (n * S + state) * tiles + tile
+  const bool rev = blockIdx.x >= half;
+  const unsigned block = rev ? blockIdx.x - half : blockIdx.x;
+  const int64_t rest = block / tiles;
+  const int tile = int(block - rest * tiles), n = int(rest / a.s), s = int(rest - int64_t(n) * a.s);
   const bool on = tile * 64 + lane < channels;
   const int chan = on ? tile * 64 + lane : channels - 1;
   const float a2 = a.a[int64_t(chan) * a.s + s] * kLog2e;
-  const float* first = REV ? a.dh_out : a.h_in;
+  const float* first = rev ? a.dh_out : a.h_in;
   float enter = first ? first[(int64_t(n) * channels + chan) * a.s + s] : 0.f;
-  float* carry = (REV ? a.gcarry : a.carry) + (int64_t(n) * a.chunks * a.s + s) * channels + chan;
+  float* carry = (rev ? a.gcarry : a.carry) + (int64_t(n) * a.chunks * a.s + s) * channels + chan;
   const float* sums = a.sums + int64_t(n) * a.chunks * channels + chan;
   const int64_t step = int64_t(a.s) * channels;
   for (int base = 0; base < a.chunks; base += kJoinChunks * waves) {
@@ -320,7 +322,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a) {
     float add[kJoinChunks], decay[kJoinChunks], total = 0.f, h = 0.f;
 #pragma unroll
     for (int i = 0; i < kJoinChunks; ++i) {
-      const int k = min(c0 + i, a.chunks - 1), c = REV ? a.chunks - 1 - k : k;
+      const int k = min(c0 + i, a.chunks - 1), c = rev ? a.chunks - 1 - k : k;
       add[i] = carry[c * step];
       decay[i] = sums[int64_t(c) * channels];
     }
@@ -344,18 +346,18 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < kJoinChunks; ++i) {
-      const int k = c0 + i, c = REV ? a.chunks - 1 - k : k;
+      const int k = c0 + i, c = rev ? a.chunks - 1 - k : k;
       if (k < a.chunks && on) carry[c * step] = mine;
       mine = fmaf(decay[i], mine, add[i]);
     }
   }
 }
 
-template <bool REV>
-int run_join(const ScanArgs& a, hipStream_t s) {
+// BACK: both, in one launch.
+inline int run_join(const ScanArgs& a, bool back, hipStream_t s) {
   const int waves = a.chunks >= kJoinChunks * kJoinWaves ? kJoinWaves : (a.chunks + kJoinChunks - 1) / kJoinChunks;
   const unsigned blocks = unsigned(int64_t(a.n) * a.s * ((a.groups * a.wide + 63) / 64));
-  scan_join<REV><<<blocks, 64 * waves, 0, s>>>(a);
+  scan_join<<<back ? 2 * blocks : blocks, 64 * waves, 0, s>>>(a, blocks);
   return int(hipGetLastError());
 }
 

@@ -232,7 +232,7 @@ int run_scan(const cc3d_scan_plan& p, ScanArgs& a, hipStream_t s) {
   if (a.chunks > 1) {
     int e = run_carry<T, NS, false>(a, s);
     if (e) return e;
-    e = run_join<false>(a, s);
+    e = run_join(a, false, s);
     if (e) return e;
   }
   if (a.waves > 1) scan_fwd<T, NS, true><<<blocks, 64 * a.waves, 0, s>>>(a);

@@ -153,6 +153,20 @@ struct BwdLds {
   }
 };
 
+// A view of the kernel's arguments, read again from where they lie: kept in
+// scalar registers the ten views spill into lanes of vector registers, and
+// some 200 of a walk's 2100 vector instructions only moved them.
+struct FreshRows {
+  uintptr_t p;
+  int64_t batch, row;
+};
+__device__ __forceinline__ FreshRows fresh(unsigned offset) {
+  auto base = (const __attribute__((address_space(4))) char*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(base));  // not the same address as before, for all the compiler knows
+  auto q = (const __attribute__((address_space(4))) int64_t*)(base + offset);
+  return {uintptr_t(q[0]), q[1], q[2]};
+}
+
 template <class T, int SG, int SUB, bool MULTI, bool DUO>
 __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
   using L = BwdLds<SG, SUB>;
@@ -199,6 +213,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
   }
   // (a branch costs more here than what it saves: flags select)
   const bool soft = a.softplus, gated = a.z.p != nullptr;
+  const bool has_du = a.du.p != nullptr, has_ddt = a.ddt.p != nullptr, has_dz = a.dz.p != nullptr;
   const ScanRows& zrows = gated ? a.z : a.dy;
   // this lane's places behind a walk's first token: its own tokens' channel
   // pair in every stream (token q of each SG), and its share of B and C
@@ -221,8 +236,13 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
     const int t0 = ch * a.chunk, t1 = min(t0 + a.chunk, a.t), te = min(t1, valid_tokens(a, n));
     const int subs = te > t0 ? (te - t0 + SUB - 1) / SUB : 0;
     // a walk's first token: the same address for the whole wave
-    auto walk = [&](const ScanRows& v, int k) {
-      return static_cast<T*>(v.p) + int64_t(n) * v.batch + int64_t(t0 + k * SUB) * v.row;
+    struct Walk {
+      T* p;
+      int64_t row;
+    };
+    auto walk = [&](unsigned offset, int k) -> Walk {
+      const FreshRows v = fresh(offset);
+      return {reinterpret_cast<T*>(v.p) + int64_t(n) * v.batch + int64_t(t0 + k * SUB) * v.row, v.row};
     };
     float* pbc = a.part_bc + (int64_t(tile) * a.n + n) * a.t * waves * kVal;
 
@@ -233,19 +253,23 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
     T rbc[kBcEach];
     auto fetch = [&](int k, auto back) {
       const int there = a.t - t0 - k * SUB;
-      const T *dt = walk(a.dt, k), *u = walk(a.u, k), *z = walk(zrows, k), *dy = walk(a.dy, k);
-      const T *bp = walk(a.b, k) + group * a.s + sw * 4 * SG, *cp = walk(a.c, k) + group * a.s + sw * 4 * SG;
-      auto at_token = [&](const T* p, const ScanRows& v, unsigned o, int b) {
-        return load_pair<T, DUO>(p + int64_t(b * SG) * v.row + o);
-      };
+      const Walk dt = walk(offsetof(ScanArgs, dt), k), u = walk(offsetof(ScanArgs, u), k);
+      const T* bp = walk(offsetof(ScanArgs, b), k).p + group * a.s + sw * 4 * SG;
+      const T* cp = walk(offsetof(ScanArgs, c), k).p + group * a.s + sw * 4 * SG;
+      Walk z{}, dy{};
+      if constexpr (back.value) {
+        dy = walk(offsetof(ScanArgs, dy), k);
+        z = walk(gated ? offsetof(ScanArgs, z) : offsetof(ScanArgs, dy), k);
+      }
+      auto at_token = [&](const Walk& v, unsigned o, int b) { return load_pair<T, DUO>(v.p + int64_t(b * SG) * v.row + o); };
       if (there >= SUB) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          rdt[b] = at_token(dt, a.dt, o_dt, b);
-          ru[b] = at_token(u, a.u, o_u, b);
+          rdt[b] = at_token(dt, o_dt, b);
+          ru[b] = at_token(u, o_u, b);
           if constexpr (back.value) {
-            rz[b] = at_token(z, zrows, o_z, b);
-            rdy[b] = at_token(dy, a.dy, o_dy, b);
+            rz[b] = at_token(z, o_z, b);
+            rdy[b] = at_token(dy, o_dy, b);
           }
         }
 #pragma unroll
@@ -258,14 +282,14 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const bool in = b * SG + q < there;
-          auto clamped = [&](const T* p, const ScanRows& v, unsigned o) {
-            return load_pair<T, DUO>(p + (in ? int64_t(b * SG) * v.row + o : int64_t(chan)));
+          auto clamped = [&](const Walk& v, unsigned o) {
+            return load_pair<T, DUO>(v.p + (in ? int64_t(b * SG) * v.row + o : int64_t(chan)));
           };
-          rdt[b] = clamped(dt, a.dt, o_dt);
-          ru[b] = clamped(u, a.u, o_u);
+          rdt[b] = clamped(dt, o_dt);
+          ru[b] = clamped(u, o_u);
           if constexpr (back.value) {
-            rz[b] = clamped(z, zrows, o_z);
-            rdy[b] = clamped(dy, a.dy, o_dy);
+            rz[b] = clamped(z, o_z);
+            rdy[b] = clamped(dy, o_dy);
           }
         }
 #pragma unroll
@@ -388,7 +412,37 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
         }
       }
       wave_fence();  // what follows reads LDS again rather than hold eight tokens' values
-      float bcsum[SUB], sums[NB][6];
+      float* comb = lds + at.comb + turn * waves * wc * L::kComb;
+      float* meet = lds + at.meet + turn * waves * wc * L::kMeet;
+      // results of this lane group's token of the b-th SG, from its sums over states
+      auto finish = [&](int b, const float (&sum)[6]) {
+        const Walk du_o = walk(offsetof(ScanArgs, du), k), ddt_o = walk(offsetof(ScanArgs, ddt), k),
+                   dz_o = walk(offsetof(ScanArgs, dz), k);
+        const int j = b * SG + q;
+        const bool in = j < te - tb;
+        const float2 delta2 = pair_at(0, j), gy2 = pair_at(2, j);
+        const float delta[2] = {delta2.x, delta2.y}, gy[2] = {gy2.x, gy2.y};
+        float du[2], ddt[2], dz[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float raw = mdt[b].get(c) + bias[c], uu = mu[b].get(c), zz = mz[b].get(c);
+          const bool real = in && own[c];
+          const float slope = sigmoid_f32(raw), sg = sigmoid_f32(zz);
+          const float d = fmaf(sum[4 + c], kLn2, uu * sum[2 + c]);
+          ddt[c] = real ? d * (soft && !(raw > 20.f) ? slope : 1.f) : 0.f;
+          du[c] = real ? fmaf(skip[c], gy[c], delta[c] * sum[2 + c]) : 0.f;
+          dd[c] = real ? fmaf(gy[c], uu, dd[c]) : dd[c];
+          dbias[c] += ddt[c];
+          const float y_all = fmaf(skip[c], uu, sum[c]);
+          dz[c] = real ? mdy[b].get(c) * y_all * (sg * (1.f + zz * (1.f - sg))) : 0.f;
+        }
+        if (j < t1 - tb) {
+          if (has_du) store_pair(du_o.p + int64_t(b * SG) * du_o.row + o_du, du[0], du[1], own[0], own[1]);
+          if (has_ddt) store_pair(ddt_o.p + int64_t(b * SG) * ddt_o.row + o_ddt, ddt[0], ddt[1], own[0], own[1]);
+          if (has_dz) store_pair(dz_o.p + int64_t(b * SG) * dz_o.row + o_dz, dz[0], dz[1], own[0], own[1]);
+        }
+      };
+      float bcsum[SUB];
 #pragma unroll
       for (int b = NB - 1; b >= 0; --b) {
         float y0[2][SG], gb[2][SG], ca[2][SG];
@@ -417,30 +471,28 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
             }
           }
           bcsum[j] = reduce8<LC>(v, lane);
+          if (j % kDup == 0) {  // kDup tokens a store, one for each copy
+            float w = bcsum[j];
+#pragma unroll
+            for (int i = 1; i < kDup && j + i < SUB; ++i) w = copy == i ? bcsum[j + i] : w;
+            if (SUB >= kDup || copy < SUB) comb[j * waves * kVal + comb_at] = w;
+          }
         }
+        float sum[6];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          sums[b][c] = sum_groups<SG>(y0[c]);
-          sums[b][2 + c] = sum_groups<SG>(gb[c]);
-          sums[b][4 + c] = sum_groups<SG>(ca[c]);
+          sum[c] = sum_groups<SG>(y0[c]);
+          sum[2 + c] = sum_groups<SG>(gb[c]);
+          sum[4 + c] = sum_groups<SG>(ca[c]);
+        }
+        if constexpr (MULTI) {
+#pragma unroll
+          for (int i = 0; i < 6; ++i) meet[((wave * NB + b) * 6 + i) * 64 + lane] = sum[i];
+        } else {
+          finish(b, sum);
         }
       }
 
-      float* comb = lds + at.comb + turn * waves * wc * L::kComb;
-#pragma unroll
-      for (int j0 = 0; j0 < SUB; j0 += kDup) {
-        float v = bcsum[j0];
-#pragma unroll
-        for (int i = 1; i < kDup && j0 + i < SUB; ++i) v = copy == i ? bcsum[j0 + i] : v;
-        if (SUB >= kDup || copy < SUB) comb[j0 * waves * kVal + comb_at] = v;
-      }
-      float* meet = lds + at.meet + turn * waves * wc * L::kMeet;
-      if constexpr (MULTI) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int i = 0; i < 6; ++i) meet[((wave * NB + b) * 6 + i) * 64 + lane] = sums[b][i];
-      }
       __syncthreads();
       const int more = waves * L::kComb;
       for (int i = threadIdx.x; i < more; i += 64 * waves * wc) {
@@ -449,40 +501,17 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
         else if (wc == 2) s += comb[more + i];
         if (i < (t1 - tb) * waves * kVal) pbc[int64_t(tb) * waves * kVal + i] = s;
       }
-      T *du_o = walk(a.du, k), *ddt_o = walk(a.ddt, k), *dz_o = walk(a.dz, k);
+      if constexpr (MULTI) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if constexpr (MULTI) {
+        for (int b = 0; b < NB; ++b) {
           if (b % waves != sw) continue;
+          float total[6];
 #pragma unroll
           for (int i = 0; i < 6; ++i) {
-            float s = 0.f;
-            for (int w = 0; w < waves; ++w) s += meet[(((cw * waves + w) * NB + b) * 6 + i) * 64 + lane];
-            sums[b][i] = s;
+            total[i] = 0.f;
+            for (int w = 0; w < waves; ++w) total[i] += meet[(((cw * waves + w) * NB + b) * 6 + i) * 64 + lane];
           }
-        }
-        const int j = b * SG + q;
-        const bool in = j < te - tb;
-        const float2 delta2 = pair_at(0, j), gy2 = pair_at(2, j);
-        const float delta[2] = {delta2.x, delta2.y}, gy[2] = {gy2.x, gy2.y};
-        float du[2], ddt[2], dz[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float raw = mdt[b].get(c) + bias[c], uu = mu[b].get(c), zz = mz[b].get(c);
-          const bool real = in && own[c];
-          const float slope = sigmoid_f32(raw), sg = sigmoid_f32(zz);
-          const float d = fmaf(sums[b][4 + c], kLn2, uu * sums[b][2 + c]);
-          ddt[c] = real ? d * (soft && !(raw > 20.f) ? slope : 1.f) : 0.f;
-          du[c] = real ? fmaf(skip[c], gy[c], delta[c] * sums[b][2 + c]) : 0.f;
-          dd[c] = real ? fmaf(gy[c], uu, dd[c]) : dd[c];
-          dbias[c] += ddt[c];
-          const float y_all = fmaf(skip[c], uu, sums[b][c]);
-          dz[c] = real ? mdy[b].get(c) * y_all * (sg * (1.f + zz * (1.f - sg))) : 0.f;
-        }
-        if (j < t1 - tb) {
-          if (a.du.p) store_pair(du_o + int64_t(b * SG) * a.du.row + o_du, du[0], du[1], own[0], own[1]);
-          if (a.ddt.p) store_pair(ddt_o + int64_t(b * SG) * a.ddt.row + o_ddt, ddt[0], ddt[1], own[0], own[1]);
-          if (a.dz.p) store_pair(dz_o + int64_t(b * SG) * a.dz.row + o_dz, dz[0], dz[1], own[0], own[1]);
+          finish(b, total);
         }
       }
       turn ^= 1;
@@ -490,13 +519,14 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
 
     // tokens after the valid ones that no walk held
     if (subs * SUB < t1 - t0) {
-      T *du_o = walk(a.du, subs), *ddt_o = walk(a.ddt, subs), *dz_o = walk(a.dz, subs);
+      const Walk du_o = walk(offsetof(ScanArgs, du), subs), ddt_o = walk(offsetof(ScanArgs, ddt), subs),
+                 dz_o = walk(offsetof(ScanArgs, dz), subs);
       for (int j = q; j < t1 - t0 - subs * SUB; j += SG) {
         if (sw != 0) continue;
         const unsigned on = unsigned(j - q);
-        if (a.du.p) store_pair(du_o + (o_du + on * unsigned(a.du.row)), 0.f, 0.f, own[0], own[1]);
-        if (a.ddt.p) store_pair(ddt_o + (o_ddt + on * unsigned(a.ddt.row)), 0.f, 0.f, own[0], own[1]);
-        if (a.dz.p) store_pair(dz_o + (o_dz + on * unsigned(a.dz.row)), 0.f, 0.f, own[0], own[1]);
+        if (has_du) store_pair(du_o.p + (o_du + on * unsigned(du_o.row)), 0.f, 0.f, own[0], own[1]);
+        if (has_ddt) store_pair(ddt_o.p + (o_ddt + on * unsigned(ddt_o.row)), 0.f, 0.f, own[0], own[1]);
+        if (has_dz) store_pair(dz_o.p + (o_dz + on * unsigned(dz_o.row)), 0.f, 0.f, own[0], own[1]);
       }
       const int64_t first = int64_t(t0 + subs * SUB) * waves * kVal, last = int64_t(t1) * waves * kVal;
       for (int64_t i = first + threadIdx.x; i < last; i += 64 * waves * wc) pbc[i] = 0.f;
@@ -575,8 +605,7 @@ int run_carries(const cc3d_scan_plan& p, ScanArgs a, hipStream_t s) {
   a.waves = cc3d::scan_fwd_waves(p.d);
   a.tiles_per_group = cc3d::scan_tiles_per_group(p.d);
   int e = run_carry<T, NS, true>(a, s);
-  if (!e) e = run_join<false>(a, s);
-  if (!e) e = run_join<true>(a, s);
+  if (!e) e = run_join(a, true, s);
   return e;
 }
 
