@@ -119,17 +119,18 @@ __device__ __forceinline__ Pair<T> load_pair(const T* p) {
   return r;
 }
 
-// Stores the channels that are this lane's own.
-template <class T>
+// Stores the channels that are this lane's own: both, the second, or none
+// (DUO); the first or none.
+template <class T, bool DUO>
 __device__ __forceinline__ void store_pair(T* p, float x, float y, bool own0, bool own1) {
   using P = Pair<T>;
-  if (own0 && own1) {
+  if constexpr (!DUO) {
+    if (own0) p[0] = from_f32<T>(x);
+  } else if (own0) {
     typename P::U v;
     if constexpr (sizeof(T) == 4) v = __float_as_uint(x) | typename P::U(__float_as_uint(y)) << 32;
     else v = pack_bf16(x, y);
     *reinterpret_cast<typename P::Mem*>(p) = v;
-  } else if (own0) {
-    p[0] = from_f32<T>(x);
   } else if (own1) {
     p[1] = from_f32<T>(y);
   }
@@ -389,7 +390,6 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
         mz[b] = rz[b];
         mdy[b] = rdy[b];
       }
-      if (k > 0) fetch(k - 1, yes);
       if (k < subs - 1) {
         const f32x4_s x = kept[(2 * k) * 64], y = kept[(2 * k + 1) * 64];
 #pragma unroll
@@ -412,6 +412,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
         }
       }
       wave_fence();  // what follows reads LDS again rather than hold eight tokens' values
+      if (k > 0) fetch(k - 1, yes);
       float* comb = lds + at.comb + turn * waves * wc * L::kComb;
       float* meet = lds + at.meet + turn * waves * wc * L::kMeet;
       // results of this lane group's token of the b-th SG, from its sums over states
@@ -437,9 +438,9 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
           dz[c] = real ? mdy[b].get(c) * y_all * (sg * (1.f + zz * (1.f - sg))) : 0.f;
         }
         if (j < t1 - tb) {
-          if (has_du) store_pair(du_o.p + int64_t(b * SG) * du_o.row + o_du, du[0], du[1], own[0], own[1]);
-          if (has_ddt) store_pair(ddt_o.p + int64_t(b * SG) * ddt_o.row + o_ddt, ddt[0], ddt[1], own[0], own[1]);
-          if (has_dz) store_pair(dz_o.p + int64_t(b * SG) * dz_o.row + o_dz, dz[0], dz[1], own[0], own[1]);
+          if (has_du) store_pair<T, DUO>(du_o.p + int64_t(b * SG) * du_o.row + o_du, du[0], du[1], own[0], own[1]);
+          if (has_ddt) store_pair<T, DUO>(ddt_o.p + int64_t(b * SG) * ddt_o.row + o_ddt, ddt[0], ddt[1], own[0], own[1]);
+          if (has_dz) store_pair<T, DUO>(dz_o.p + int64_t(b * SG) * dz_o.row + o_dz, dz[0], dz[1], own[0], own[1]);
         }
       };
       float bcsum[SUB];
@@ -524,9 +525,9 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
       for (int j = q; j < t1 - t0 - subs * SUB; j += SG) {
         if (sw != 0) continue;
         const unsigned on = unsigned(j - q);
-        if (has_du) store_pair(du_o.p + (o_du + on * unsigned(du_o.row)), 0.f, 0.f, own[0], own[1]);
-        if (has_ddt) store_pair(ddt_o.p + (o_ddt + on * unsigned(ddt_o.row)), 0.f, 0.f, own[0], own[1]);
-        if (has_dz) store_pair(dz_o.p + (o_dz + on * unsigned(dz_o.row)), 0.f, 0.f, own[0], own[1]);
+        if (has_du) store_pair<T, DUO>(du_o.p + (o_du + on * unsigned(du_o.row)), 0.f, 0.f, own[0], own[1]);
+        if (has_ddt) store_pair<T, DUO>(ddt_o.p + (o_ddt + on * unsigned(ddt_o.row)), 0.f, 0.f, own[0], own[1]);
+        if (has_dz) store_pair<T, DUO>(dz_o.p + (o_dz + on * unsigned(dz_o.row)), 0.f, 0.f, own[0], own[1]);
       }
       const int64_t first = int64_t(t0 + subs * SUB) * waves * kVal, last = int64_t(t1) * waves * kVal;
       for (int64_t i = first + threadIdx.x; i < last; i += 64 * waves * wc) pbc[i] = 0.f;
