@@ -131,13 +131,23 @@ __device__ __forceinline__ float normalise(float (&v)[8], int kind, const Cols<T
   return rs;
 }
 
-// The parameters of a lane's channels: ones and zeros where there are none.
+// The parameters of a lane's channels, in fp32 (they serve every row): ones
+// and zeros where there are none.
 template <class T, int KIND>
 struct Params {
-  Raw8<T> scale, w1, b1, w2, b2;
-  __device__ __forceinline__ Params(const JoinArgs& a, const Cols<T, KIND>& cols)
-      : scale(cols.param(a.scale, 1.f)), w1(cols.param(a.w1, 1.f)), b1(cols.param(a.b1, 0.f)),
-        w2(cols.param(a.w2, 1.f)), b2(cols.param(a.b2, 0.f)) {}
+  float scale[8], w1[8], b1[8], w2[8], b2[8];
+  __device__ __forceinline__ Params(const JoinArgs& a, const Cols<T, KIND>& cols) {
+    auto get = [&](const void* p, float none, float (&v)[8]) {
+      const Raw8<T> r = cols.param(p, none);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = get8(r, j);
+    };
+    get(a.scale, 1.f, scale);
+    get(a.w1, 1.f, w1);
+    get(a.b1, 0.f, b1);
+    get(a.w2, 1.f, w2);
+    get(a.b2, 0.f, b2);
+  }
 };
 
 __device__ __forceinline__ float gate_of(float g, bool silu) { return silu ? g * sigmoid_f32(g) : g; }

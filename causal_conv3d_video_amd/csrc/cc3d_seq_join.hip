@@ -58,8 +58,8 @@ __global__ __launch_bounds__(RowSum<LPR>::kThreads) void join_fwd(JoinArgs a) {
       normalise(v, a.post, cols, a, sum);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float n1 = fmaf(v[j], get8(p.w1, j), get8(p.b1, j));
-        x[j] = fmaf(get8(p.scale, j) * gate_of(get8(rg, j), gate_silu), n1, x[j]);
+        const float n1 = fmaf(v[j], p.w1[j], p.b1[j]);
+        x[j] = fmaf(p.scale[j] * gate_of(get8(rg, j), gate_silu), n1, x[j]);
       }
     }
     if (xo.p) {
@@ -69,7 +69,7 @@ __global__ __launch_bounds__(RowSum<LPR>::kThreads) void join_fwd(JoinArgs a) {
     if (ho.p) {
       normalise(x, a.pre, cols, a, sum);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], get8(p.w2, j), get8(p.b2, j));
+      for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], p.w2[j], p.b2[j]);
       if (act_silu) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] *= sigmoid_f32(x[j]);

@@ -97,22 +97,34 @@ __global__ __launch_bounds__(RowSum<LPR>::kThreads, LPR > 512 ? 4 : 2) void join
         x[j] = get8(rr, j);
         dx[j] = get8(rdx, j);
       }
+      // the gate's factor and slope, once for both of their places
+      float ga[8], slope[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ga[j] = get8(rg, j);
+      if (gate_silu) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float g = ga[j], sg = sigmoid_f32(g);
+          ga[j] = g * sg;
+          slope[j] = sg * (1.f + g * (1.f - sg));
+        }
+      }
       const float rs1 = a.y ? normalise(xn1, a.post, cols, a, sum) : 1.f;
       if (a.dh) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float n1 = fmaf(xn1[j], get8(p.w1, j), get8(p.b1, j));
-          if (a.y) x[j] = fmaf(get8(p.scale, j) * gate_of(get8(rg, j), gate_silu), n1, x[j]);
+          const float n1 = fmaf(xn1[j], p.w1[j], p.b1[j]);
+          if (a.y) x[j] = fmaf(p.scale[j] * ga[j], n1, x[j]);
         }
         const float rs2 = normalise(x, a.pre, cols, a, sum);
         float d[8], m = 0.f, md = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float g = get8(rdh, j);
-          if (act_silu) g *= silu_slope(fmaf(x[j], get8(p.w2, j), get8(p.b2, j)));
+          if (act_silu) g *= silu_slope(fmaf(x[j], p.w2[j], p.b2[j]));
           acc[3][j] = fmaf(g, x[j], acc[3][j]);
           acc[4][j] += g;
-          d[j] = g * get8(p.w2, j);
+          d[j] = g * p.w2[j];
           const float own = cols.on(j) ? d[j] : 0.f;
           m = fmaf(own, x[j], m);
           md += own;
@@ -131,16 +143,16 @@ __global__ __launch_bounds__(RowSum<LPR>::kThreads, LPR > 512 ? 4 : 2) void join
       float dn[8], dg[8], m = 0.f, md = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float g = get8(rg, j), ga = gate_of(g, gate_silu), s = get8(p.scale, j);
-        const float along = dx[j] * fmaf(xn1[j], get8(p.w1, j), get8(p.b1, j));
-        acc[0][j] = fmaf(along, ga, acc[0][j]);
+        const float s = p.scale[j];
+        const float along = dx[j] * fmaf(xn1[j], p.w1[j], p.b1[j]);
+        acc[0][j] = fmaf(along, ga[j], acc[0][j]);
         dg[j] = along * s;
         acc[5][j] += dg[j];  // (left alone without a shared gate)
-        if (gate_silu) dg[j] *= silu_slope(g);
-        dn[j] = dx[j] * s * ga;
+        if (gate_silu) dg[j] *= slope[j];
+        dn[j] = dx[j] * s * ga[j];
         acc[1][j] = fmaf(dn[j], xn1[j], acc[1][j]);
         acc[2][j] += dn[j];
-        dn[j] *= get8(p.w1, j);
+        dn[j] *= p.w1[j];
         const float own = cols.on(j) ? dn[j] : 0.f;
         m = fmaf(own, xn1[j], m);
         md += own;
