@@ -1,5 +1,4 @@
-// Short cached causal convolution of each channel, forward and backward, and
-// the fixed-order sum over rows of partial sums.
+// Short cached causal convolution of each channel, forward and backward.
 //
 //   Z = [cache; x];  p[t] = b + sum_k w[k] * Z[t + k];  y[t] = act(p[t])
 //
@@ -7,7 +6,11 @@
 // and one written: bound by memory.  A thread owns eight consecutive channels
 // (16-byte loads and stores of bf16, neighbouring threads on neighbouring
 // channels) and walks a run of tokens with the last K - 1 of them in
-// registers, so x is read once but for K - 1 tokens a run.
+// registers, so x is read once but for K - 1 tokens a run; the next tokens load
+// while some are computed.  Measured: 6240 ragged sequences of up to 17 tokens
+// of 384 fp32 channels, K = 3, in 72 us (vector units busy 16% of the kernel);
+// a full read and write of its tensors at a large copy's 4.74 TB/s would take
+// 77.  One token of a few streams costs the launch, 4 us.
 #include "cc3d_seq_device.h"
 
 namespace {
@@ -141,7 +144,11 @@ __global__ __launch_bounds__(256) void conv1d_fwd(Conv1dArgs a) {
 // t - K + 1; a run ends K - 1 tokens after its last.  dw and db are sums over
 // all tokens: a thread keeps them in registers over every run that it takes,
 // the workgroup's rows add theirs in LDS, and each workgroup writes one row of
-// partial sums; sum_rows adds those in their order.
+// partial sums; sum_rows adds those in their order.  Three elements move for
+// the forward pass' two, against some 265 vector instructions for eight bf16
+// channels of a token at K = 4, runs' overlaps included: 2 x 8193 tokens of 2048
+// channels in 54 us and 5 for the sums, vector units busy 51% of the kernel; the
+// bytes alone would take 42 at a large copy's rate.
 template <class T, int K, bool FEW, bool SILU>
 __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
   // tokens loaded at once, and unrolled (whole turns of the rings)

