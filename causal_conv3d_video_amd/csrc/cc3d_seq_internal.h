@@ -18,6 +18,7 @@ struct cc3d_scan_plan {
   cc3d_seq_info_t info{};
   int32_t chunk = 0;      // forward: tokens per chunk (a multiple of 4; T rounded up when not split)
   int32_t bwd_workers = 0;  // backward: workgroups per channel tile (each takes every bwd_workers-th chunk)
+  bool bwd_fits = false;  // backward: no launch has too many threads
 };
 
 struct cc3d_join_plan {
@@ -28,6 +29,10 @@ struct cc3d_join_plan {
 };
 
 namespace cc3d {
+
+// The runtime takes launches of fewer than 2^32 threads.
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
+inline bool fits(int64_t workgroups, int threads) { return workgroups <= kMaxThreads / threads; }
 
 // Lanes that hold one row of the block join (8 channels each), a power of two.
 inline int join_lanes(int c) {
@@ -58,6 +63,12 @@ inline int scan_tiles_per_group(const cc3d_scan_desc_t& d) {
 // States a wave holds, and waves that share one tile of channels.
 inline int scan_fwd_ns(const cc3d_scan_desc_t& d) { return d.states <= 4 ? 4 : d.states <= 8 ? 8 : 16; }
 inline int scan_fwd_waves(const cc3d_scan_desc_t& d) { return (d.states + scan_fwd_ns(d) - 1) / scan_fwd_ns(d); }
+// Lanes that hold a channel's states in a call of one token, four each.
+inline int scan_step_lanes(int states) {
+  int l = 1;
+  while (l * 4 < states) l *= 2;
+  return l;
+}
 
 // The backward pass' layout.  A lane holds two neighbouring channels with
 // four states each; `sg` groups of lanes of a wave hold different states, so a
@@ -102,7 +113,8 @@ struct SumJob {
   float* dst;
   int64_t rows, cols, stride;
 };
-constexpr int kSumJobs = 5;
+constexpr int kSumJobs = 5, kSumThreads = 1024;
+inline int64_t sum_workgroups(int64_t cols) { return (cols + 63) / 64; }
 int launch_sums(const SumJob* jobs, int n, void* stream);
 
 }  // namespace cc3d

@@ -39,8 +39,7 @@ int64_t elem_of(int32_t dtype) { return dtype == CC3D_BF16 ? 2 : 4; }
 // (MI355X) and its SIMDs; the kernels run on any count.
 constexpr int64_t kUnits = 256;
 constexpr int64_t kSimds = 1024;
-// Workgroups of one launch, and the addresses a view may span.
-constexpr int64_t kMaxBlocks = (int64_t(1) << 31) - 1;
+// The addresses a view may span.
 constexpr int64_t kMaxSpan = int64_t(1) << 46;
 // Elements between two tokens of the scan: offsets inside a chunk of 64
 // tokens are 32 bits.
@@ -164,6 +163,18 @@ class Check {
   uintptr_t same_[2] = {0, 0};
 };
 
+// Whether the sums of a backward call's parameter gradients fit one launch.
+struct Summed {
+  const float* dst;
+  int64_t cols;
+};
+bool sums_fit(std::initializer_list<Summed> jobs) {
+  int64_t workgroups = 0;
+  for (const Summed& j : jobs)
+    if (j.dst) workgroups += cc3d::sum_workgroups(j.cols);
+  return cc3d::fits(workgroups, cc3d::kSumThreads);
+}
+
 template <class Plan, class Desc>
 Plan* make_plan(const Desc* d) {
   Plan* p = new (std::nothrow) Plan;
@@ -189,7 +200,7 @@ extern "C" cc3d_status_t causal_conv1d_plan(const cc3d_conv1d_desc_t* d, cc3d_co
   int64_t seg = std::max<int64_t>(ceildiv(int64_t(d->n) * d->t, ceildiv(int64_t(1) << 18, vecs)), 1);
   seg = std::min<int64_t>(std::max<int64_t>(seg, 8), 64);
   seg = std::min<int64_t>(seg, d->t);
-  if (int64_t(d->n) * ceildiv(d->t, seg) > kMaxBlocks / ceildiv(vecs, 256)) return refuse(CC3D_ERR_UNSUPPORTED);
+  if (int64_t(d->n) * ceildiv(d->t, seg) > (cc3d::kMaxThreads - 255) / vecs) return refuse(CC3D_ERR_UNSUPPORTED);
   auto* p = make_plan<cc3d_conv1d_plan>(d);
   if (!p) return CC3D_ERR_NO_MEMORY;
   p->seg = int32_t(seg);
@@ -253,6 +264,7 @@ extern "C" cc3d_status_t causal_conv1d_backward(cc3d_conv1d_plan_t p, const cc3d
   c.dense(a->lengths, int64_t(d.n) * 4, 4, false, false);
   c.workspace(a->workspace, a->workspace_bytes, p->info.backward_workspace_bytes);
   if (!c.ok()) return refuse(CC3D_ERR_INVALID_ARG);
+  if (!sums_fit({{a->dw, int64_t(d.k) * d.c}, {a->db, d.c}})) return refuse(CC3D_ERR_UNSUPPORTED);
   return launched(cc3d::launch_conv1d_backward(*p, *a, stream));
 }
 
@@ -267,11 +279,17 @@ extern "C" cc3d_status_t selective_scan_plan(const cc3d_scan_desc_t* d, cc3d_sca
       (d->softplus != 0 && d->softplus != 1) || !known_dtype(d->dtype))
     return refuse(CC3D_ERR_INVALID_ARG);
   if (d->states > cc3d::kScanMaxStates || d->t > kMaxTokens) return refuse(CC3D_ERR_UNSUPPORTED);
-  const int64_t tiles = int64_t(d->groups) * cc3d::scan_tiles_per_group(*d);
+  // (an output of more elements than a view may span would be refused by every call)
+  if (int64_t(d->n) * d->t > kMaxSpan / d->d) return refuse(CC3D_ERR_UNSUPPORTED);
+  const int64_t tiles = int64_t(d->groups) * cc3d::scan_tiles_per_group(*d), nc = int64_t(d->n);
+  const int threads = 64 * cc3d::scan_fwd_waves(*d);
+  if (d->t == 1 ? !cc3d::fits(nc * ceildiv(int64_t(d->d) * cc3d::scan_step_lanes(d->states), 256), 256)
+                : !cc3d::fits(nc * tiles, threads))
+    return refuse(CC3D_ERR_UNSUPPORTED);
   // Forward: split the time axis when the channels alone leave SIMDs idle, into
   // four waves a SIMD: 8192 tokens of 2048 channels in 125 us, two a SIMD 142 (a
   // join 1 us slower among them).
-  const int64_t base = int64_t(d->n) * tiles * cc3d::scan_fwd_waves(*d);
+  const int64_t base = nc * tiles * cc3d::scan_fwd_waves(*d);
   int64_t chunk = ceildiv(d->t, 4) * 4;
   if (base < kSimds && d->t > 64) {
     const int64_t pieces = std::min<int64_t>(ceildiv(4 * kSimds, base), ceildiv(d->t, 32));
@@ -281,19 +299,19 @@ extern "C" cc3d_status_t selective_scan_plan(const cc3d_scan_desc_t* d, cc3d_sca
   const cc3d::ScanBwdShape bw = cc3d::scan_bwd_shape(*d);
   const int64_t bwd_chunks = ceildiv(d->t, bw.chunk);
   const int64_t bwd_tiles = int64_t(d->groups) * bw.tiles_per_group;
-  if (int64_t(d->n) * std::max(chunks, bwd_chunks) > kMaxBlocks / tiles ||
-      int64_t(d->n) * d->states > kMaxBlocks / 2 / ceildiv(d->d, 64) || int64_t(d->n) * ceildiv(d->d, 16) > kMaxBlocks / 4)
-    return refuse(CC3D_ERR_UNSUPPORTED);
   auto* p = make_plan<cc3d_scan_plan>(d);
   if (!p) return CC3D_ERR_NO_MEMORY;
   p->chunk = int32_t(chunk);
   p->info.chunks = int32_t(chunks);
   p->info.backward_chunks = int32_t(bwd_chunks);
   // carries [n][chunk][S][C] and the chunks' sums of delta [n][chunk][C]
-  const int64_t state = int64_t(d->states) * d->d, nc = int64_t(d->n);
+  const int64_t state = int64_t(d->states) * d->d;
   if (chunks > 1) p->info.workspace_bytes = nc * chunks * (state + d->d) * 4;
   // backward: two waves a SIMD, each workgroup taking every bwd_workers-th chunk
   p->bwd_workers = int32_t(std::min<int64_t>(nc * bwd_chunks, ceildiv(2 * kSimds, bwd_tiles * bw.waves * bw.wc)));
+  // (groups * states stays below 2^30 with it: what follows them counts in 32 bits)
+  p->bwd_fits = cc3d::fits(bwd_tiles * p->bwd_workers, 64 * bw.waves * bw.wc) &&
+                (bwd_chunks == 1 || cc3d::fits(nc * tiles * bwd_chunks, threads));
   // partial sums: dA [worker][C][S], dD and ddt_bias [worker * waves][C], dB and dC [tile][n][t][waves][2][4 sg]
   int64_t ws = 0;
   if (bwd_chunks > 1) ws += nc * bwd_chunks * (2 * state + d->d);
@@ -370,7 +388,9 @@ extern "C" cc3d_status_t selective_scan_backward(cc3d_scan_plan_t p, const cc3d_
   c.require(!a->ddt_bias || a->dt_bias);
   c.workspace(a->workspace, a->workspace_bytes, p->info.backward_workspace_bytes);
   if (!c.ok()) return refuse(CC3D_ERR_INVALID_ARG);
-  if (far_rows(d, {&a->u, &a->dt, &a->b, &a->c, &a->z, &a->dy, &a->du, &a->ddt, &a->dz})) return refuse(CC3D_ERR_UNSUPPORTED);
+  if (!p->bwd_fits || far_rows(d, {&a->u, &a->dt, &a->b, &a->c, &a->z, &a->dy, &a->du, &a->ddt, &a->dz}) ||
+      !sums_fit({{a->da, int64_t(d.d) * d.states}, {a->dd, d.d}, {a->ddt_bias, d.d}}))
+    return refuse(CC3D_ERR_UNSUPPORTED);
   return launched(cc3d::launch_scan_backward(*p, *a, stream));
 }
 

@@ -4,6 +4,8 @@
 #pragma once
 #include "cc3d_seq_device.h"
 
+#include <algorithm>
+
 namespace {
 
 struct ScanRows {
@@ -299,58 +301,63 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
 // A workgroup takes 64 channels of one state; each wave loads 16 chunks at
 // once and joins them, and the waves' joined stretches meet in LDS, so the
 // loads of a long sequence are not one after another.  8.8 us for 128
-// chunks of 2048 channels and 16 states.
+// chunks of 2048 channels and 16 states.  A grid of up to kJoinGrid workgroups
+// takes all of them in turns: `all` of up to 1024 threads each may be more
+// threads than a launch holds.
 constexpr int kJoinChunks = 16, kJoinWaves = 16;
+constexpr unsigned kJoinGrid = 1u << 16;
 
-__global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a, unsigned half) {
+__global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a, unsigned half, unsigned all) {
   __shared__ float add_of[kJoinWaves][64], sum_of[kJoinWaves][64];
   const int channels = a.groups * a.wide, tiles = (channels + 63) / 64;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, waves = blockDim.x / 64;
-  // block = (n * S + state) * tiles + tile
-  const bool rev = blockIdx.x >= half;
-  const unsigned block = rev ? blockIdx.x - half : blockIdx.x;
-  const int64_t rest = block / tiles;
-  const int tile = int(block - rest * tiles), n = int(rest / a.s), s = int(rest - int64_t(n) * a.s);
-  const bool on = tile * 64 + lane < channels;
-  const int chan = on ? tile * 64 + lane : channels - 1;
-  const float a2 = a.a[int64_t(chan) * a.s + s] * kLog2e;
-  const float* first = rev ? a.dh_out : a.h_in;
-  float enter = first ? first[(int64_t(n) * channels + chan) * a.s + s] : 0.f;
-  float* carry = (rev ? a.gcarry : a.carry) + (int64_t(n) * a.chunks * a.s + s) * channels + chan;
-  const float* sums = a.sums + int64_t(n) * a.chunks * channels + chan;
-  const int64_t step = int64_t(a.s) * channels;
-  for (int base = 0; base < a.chunks; base += kJoinChunks * waves) {
-    const int c0 = base + wave * kJoinChunks;
-    float add[kJoinChunks], decay[kJoinChunks], total = 0.f, h = 0.f;
+  for (unsigned at = blockIdx.x; at < all; at += gridDim.x) {
+    // block = (n * S + state) * tiles + tile
+    const bool rev = at >= half;
+    const unsigned block = rev ? at - half : at;
+    const int64_t rest = block / tiles;
+    const int tile = int(block - rest * tiles), n = int(rest / a.s), s = int(rest - int64_t(n) * a.s);
+    const bool on = tile * 64 + lane < channels;
+    const int chan = on ? tile * 64 + lane : channels - 1;
+    const float a2 = a.a[int64_t(chan) * a.s + s] * kLog2e;
+    const float* first = rev ? a.dh_out : a.h_in;
+    float enter = first ? first[(int64_t(n) * channels + chan) * a.s + s] : 0.f;
+    float* carry = (rev ? a.gcarry : a.carry) + (int64_t(n) * a.chunks * a.s + s) * channels + chan;
+    const float* sums = a.sums + int64_t(n) * a.chunks * channels + chan;
+    const int64_t step = int64_t(a.s) * channels;
+    for (int base = 0; base < a.chunks; base += kJoinChunks * waves) {
+      const int c0 = base + wave * kJoinChunks;
+      float add[kJoinChunks], decay[kJoinChunks], total = 0.f, h = 0.f;
 #pragma unroll
-    for (int i = 0; i < kJoinChunks; ++i) {
-      const int k = min(c0 + i, a.chunks - 1), c = rev ? a.chunks - 1 - k : k;
-      add[i] = carry[c * step];
-      decay[i] = sums[int64_t(c) * channels];
-    }
+      for (int i = 0; i < kJoinChunks; ++i) {
+        const int k = min(c0 + i, a.chunks - 1), c = rev ? a.chunks - 1 - k : k;
+        add[i] = carry[c * step];
+        decay[i] = sums[int64_t(c) * channels];
+      }
 #pragma unroll
-    for (int i = 0; i < kJoinChunks; ++i) {
-      const bool in = c0 + i < a.chunks;
-      add[i] = in ? add[i] : 0.f;
-      decay[i] = in ? decay[i] : 0.f;
-      total += decay[i];
-      decay[i] = __builtin_amdgcn_exp2f(decay[i] * a2);
-      h = fmaf(decay[i], h, add[i]);
-    }
-    __syncthreads();
-    add_of[wave][lane] = h;
-    sum_of[wave][lane] = total;
-    __syncthreads();
-    float mine = enter;
-    for (int w = 0; w < waves; ++w) {
-      if (w == wave) mine = enter;
-      enter = fmaf(__builtin_amdgcn_exp2f(sum_of[w][lane] * a2), enter, add_of[w][lane]);
-    }
+      for (int i = 0; i < kJoinChunks; ++i) {
+        const bool in = c0 + i < a.chunks;
+        add[i] = in ? add[i] : 0.f;
+        decay[i] = in ? decay[i] : 0.f;
+        total += decay[i];
+        decay[i] = __builtin_amdgcn_exp2f(decay[i] * a2);
+        h = fmaf(decay[i], h, add[i]);
+      }
+      __syncthreads();
+      add_of[wave][lane] = h;
+      sum_of[wave][lane] = total;
+      __syncthreads();
+      float mine = enter;
+      for (int w = 0; w < waves; ++w) {
+        if (w == wave) mine = enter;
+        enter = fmaf(__builtin_amdgcn_exp2f(sum_of[w][lane] * a2), enter, add_of[w][lane]);
+      }
 #pragma unroll
-    for (int i = 0; i < kJoinChunks; ++i) {
-      const int k = c0 + i, c = rev ? a.chunks - 1 - k : k;
-      if (k < a.chunks && on) carry[c * step] = mine;
-      mine = fmaf(decay[i], mine, add[i]);
+      for (int i = 0; i < kJoinChunks; ++i) {
+        const int k = c0 + i, c = rev ? a.chunks - 1 - k : k;
+        if (k < a.chunks && on) carry[c * step] = mine;
+        mine = fmaf(decay[i], mine, add[i]);
+      }
     }
   }
 }
@@ -358,8 +365,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a, unsigne
 // BACK: both, in one launch.
 inline int run_join(const ScanArgs& a, bool back, hipStream_t s) {
   const int waves = a.chunks >= kJoinChunks * kJoinWaves ? kJoinWaves : (a.chunks + kJoinChunks - 1) / kJoinChunks;
-  const unsigned blocks = unsigned(int64_t(a.n) * a.s * ((a.groups * a.wide + 63) / 64));
-  scan_join<<<back ? 2 * blocks : blocks, 64 * waves, 0, s>>>(a, blocks);
+  // (below 2^30: the plan holds n * tiles * S / 16 * 64 threads below 2^32)
+  const unsigned half = unsigned(int64_t(a.n) * a.s * ((a.groups * a.wide + 63) / 64)), all = back ? 2 * half : half;
+  scan_join<<<std::min(all, kJoinGrid), 64 * waves, 0, s>>>(a, half, all);
   return int(hipGetLastError());
 }
 

@@ -570,22 +570,27 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
 }
 
 // dB and dC: the sum over the group's tiles of the partial sums [tile][n][t][waves][2][each].
+// A grid of up to kBcGrid workgroups takes all values in turns: a long call has
+// more of them than a launch has threads.
+constexpr int64_t kBcGrid = 1 << 16;
+
 template <class T>
 __global__ __launch_bounds__(256) void bc_sum(ScanArgs a, ScanRows db, ScanRows dc, int each) {
-  const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
   const int64_t per = int64_t(2) * a.groups * a.s;  // values a token
-  const int64_t tok = id / per;
-  if (tok >= int64_t(a.n) * a.t) return;
-  const int v = int(id - tok * per), which = v / (a.groups * a.s), gs = v - which * a.groups * a.s;
-  const int group = gs / a.s, s = gs - group * a.s;
-  const ScanRows& out = which ? dc : db;
-  if (!out.p) return;
+  const int64_t values = int64_t(a.n) * a.t * per, step = int64_t(gridDim.x) * 256;
   const int64_t token = int64_t(a.waves) * 2 * each, tile = int64_t(a.n) * a.t * token;
-  const float* p = a.part_bc + group * a.tiles_per_group * tile + tok * token + (s / each * 2 + which) * each + s % each;
-  float sum = 0.f;
-  for (int i = 0; i < a.tiles_per_group; ++i) sum += p[i * tile];
-  const int64_t n = tok / a.t, t = tok - n * a.t;
-  static_cast<T*>(out.p)[n * out.batch + t * out.row + gs] = from_f32<T>(sum);
+  for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < values; id += step) {
+    const int64_t tok = id / per;
+    const int v = int(id - tok * per), which = v / (a.groups * a.s), gs = v - which * a.groups * a.s;
+    const int group = gs / a.s, s = gs - group * a.s;
+    const ScanRows& out = which ? dc : db;
+    if (!out.p) continue;
+    const float* p = a.part_bc + int64_t(group) * a.tiles_per_group * tile + tok * token + (s / each * 2 + which) * each + s % each;
+    float sum = 0.f;
+    for (int i = 0; i < a.tiles_per_group; ++i) sum += p[i * tile];
+    const int64_t n = tok / a.t, t = tok - n * a.t;
+    static_cast<T*>(out.p)[n * out.batch + t * out.row + gs] = from_f32<T>(sum);
+  }
 }
 
 template <class T, int SG, int SUB, bool MULTI, bool DUO>
@@ -637,7 +642,7 @@ int run_scan_bwd(const cc3d_scan_plan& p, ScanArgs& a, const cc3d_scan_args_t& c
   }
   if (!e && (c.db.p || c.dc.p)) {
     const int64_t values = int64_t(a.n) * a.t * 2 * a.groups * a.s;
-    bc_sum<T><<<unsigned((values + 255) / 256), 256, 0, s>>>(a, view_of(c.db), view_of(c.dc), 4 * v.sg);
+    bc_sum<T><<<unsigned(std::min((values + 255) / 256, kBcGrid)), 256, 0, s>>>(a, view_of(c.db), view_of(c.dc), 4 * v.sg);
     e = int(hipGetLastError());
   }
   return e;

@@ -13,7 +13,7 @@ struct SumArgs {
 // 64 columns a workgroup; each of its 16 waves adds every 16th row, 16 loads
 // at a time (a row after another would be a chain of memory latencies), and
 // the waves' sums are added in their order.  1020 rows of 2575 columns: 6.6 us.
-__global__ __launch_bounds__(1024) void sum_rows(SumArgs a) {
+__global__ __launch_bounds__(cc3d::kSumThreads) void sum_rows(SumArgs a) {
   __shared__ float red[16][64];
   const int lane = threadIdx.x % 64, line = threadIdx.x / 64;
   int k = 0;
@@ -52,10 +52,10 @@ int launch_sums(const SumJob* jobs, int n, void* stream) {
     if (!jobs[i].dst) continue;
     a.job[a.n] = jobs[i];
     a.first[a.n++] = blocks;
-    blocks += unsigned((jobs[i].cols + 63) / 64);
+    blocks += unsigned(sum_workgroups(jobs[i].cols));
   }
   if (!blocks) return 0;
-  sum_rows<<<blocks, 1024, 0, static_cast<hipStream_t>(stream)>>>(a);
+  sum_rows<<<blocks, kSumThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
   return int(hipGetLastError());
 }
 

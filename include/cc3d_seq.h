@@ -35,7 +35,13 @@
  *                         stride, an output whose strides overlap itself, an
  *                         output overlapping another buffer (but for the
  *                         exceptions named below), a workspace too small
- *   CC3D_ERR_UNSUPPORTED  outside the stated limits
+ *   CC3D_ERR_UNSUPPORTED  outside the stated limits; or a launch of 2^32
+ *                         threads or more (a thread takes eight channels of
+ *                         up to 64 tokens of the convolution, one channel and
+ *                         up to 16 states of a chunk of the scan): the plan is
+ *                         refused where the forward call is too large, the
+ *                         backward call where only it, or the parameters'
+ *                         gradients that it is asked for, are
  *   CC3D_ERR_DEVICE       the runtime rejected a launch
  * The counters of causal_conv3d_counters count these calls and refusals too.
  */

@@ -1,0 +1,199 @@
+"""Values at the edges of the sequence operators' arithmetic on the GPU:
+the softplus over its whole range, recurrences that grow, states that decay at
+once, and infinities beside the tokens after a sequence's valid ones."""
+import ctypes
+
+import pytest
+import torch
+
+import causal_conv3d_video_amd as cc3d
+import seq_oracle as so
+import test_seq_gpu as base
+
+pytestmark = pytest.mark.gpu
+BF, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+DEV = base.DEV
+INF = float("inf")
+
+
+def _scan_bounds(i, lengths, softplus):
+    """(reference, magnitudes) of y and h_out, and of the gradients."""
+    o = [base.d64(i[k]) for k in ("u", "dt", "a", "b", "c", "d", "z", "dt_bias", "h_in")] + [lengths, softplus]
+    g = [base.d64(i[k]) for k in ("u", "dt", "a", "b", "c", "dy", "d", "z", "dt_bias", "h_in", "dh_out")] + [lengths,
+                                                                                                            softplus]
+    return (so.scan(*o)[:2], so.scan(*o, mag=True)[:2]), (so.scan_grad(*g), so.scan_grad(*g, mag=True))
+
+
+def _scan(i, n, t, c, s, g, dtype, softplus, lengths=None, names=()):
+    """y, h_out and the named gradients of one call each way."""
+    plan = cc3d.selective_scan_plan(cc3d.make_scan_desc(n, t, c, s, groups=g, softplus=softplus, dtype=dtype))
+    j = {k: base.dev(v) for k, v in i.items()}
+    lt = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    opt = dict(d=j["d"], z=j["z"], dt_bias=j["dt_bias"], h_in=j["h_in"], lengths=lt)
+    ins = [j[k] for k in ("u", "dt", "a", "b", "c")]
+    y, h = base.nan(n, t, c, dtype=dtype), base.nan(n, c, s)
+    cc3d.selective_scan_forward(plan, *ins, y, h_out=h, workspace=base.space(plan), **opt)
+    like = dict(du="u", ddt="dt", da="a", db="b", dc="c", dd="d", dz="z", ddt_bias="dt_bias")
+    got = {k: base.nan(*(j[like[k]].shape if k in like else (n, c, s)),
+                       dtype=dtype if k in ("du", "ddt", "db", "dc", "dz") else F32) for k in names}
+    if names:
+        cc3d.selective_scan_backward(plan, *ins, j["dy"], dh_out=j["dh_out"], workspace=base.space(plan, True), **opt, **got)
+    return y, h, got
+
+
+# ---------------------------------------------------------------- softplus
+
+def test_softplus_is_good_to_a_few_roundings_over_its_range(cuda_device):
+    """With u = B = C = 1 and no state, y is delta itself, and so is du with
+    dy = 1: through the single-token kernel, the kernel of many tokens and the
+    backward one.  In units of 2**-24 of the value: the exponential's argument
+    is rounded twice, 1.25 |v| of a negative v and at most 1.25 of a positive
+    one; the exponential 2; 1 + e, whose loss is added back through a
+    reciprocal and a product, 4; the logarithm 2, its factor 2, their sum 1;
+    below 12 with the positive argument's share, 14 with the loss of its own
+    next order."""
+    v = torch.cat([torch.linspace(-30, 21, 60000, dtype=F32)]
+                  + [x + torch.linspace(-1e-3, 1e-3, 512, dtype=F32) for x in (-20., -16., -8., -4., -2., 0., 20.)])
+    c = v.numel()
+    want = so.softplus(v.double())
+    bound = (14 + 1.25 * torch.clamp(-v.double(), min=0)) * so.EPS32 * want
+    one = torch.ones(c, 1, device=DEV)
+    seen = {}
+    for t in (1, 3):
+        plan = cc3d.selective_scan_plan(cc3d.make_scan_desc(1, t, c, 1, dtype=F32))
+        dt = v.to(DEV).expand(1, t, c).contiguous()
+        u, bc = torch.ones(1, t, c, device=DEV), torch.ones(1, t, 1, device=DEV)
+        # (a state that is forgotten at once: every token's y is its own delta)
+        y, du = base.nan(1, t, c), base.nan(1, t, c)
+        cc3d.selective_scan_forward(plan, u, dt, -1e30 * one, bc, bc, y, workspace=base.space(plan))
+        cc3d.selective_scan_backward(plan, u, dt, -1e30 * one, bc, bc, u, du=du, workspace=base.space(plan, True))
+        seen.update({("y", t): y, ("du", t): du})
+    for what, got in seen.items():
+        for q in range(got.shape[1]):
+            over = (got[0, q].cpu().double() - want).abs() - bound
+            k = int(over.argmax())
+            assert float(over[k]) <= 0, (what, q, float(v[k]), float(over[k] / (so.EPS32 * want[k])))
+
+
+# ------------------------------------------------------- growing recurrences
+
+@pytest.mark.parametrize("t,s,ragged", [(700, 16, False), (700, 4, True), (330, 40, True)])
+def test_growing_recurrences_stay_finite_where_the_formula_does(cuda_device, t, s, ragged):
+    """Every token's decay is e**3, so a chunk of 32 tokens multiplies by more
+    than fp32 holds; inputs are zero but in the last 20 tokens and gradients
+    but in the first 20, so nothing in the formula comes near that."""
+    n, c, g = 3, 70, 2
+    i = base.scan_inputs(n, t, c, s, g, F32, False, "dz", 500 + t + s)
+    i["dt"] = torch.full((n, t, c), -1.0)
+    i["a"] = torch.full((c, s), -3.0)
+    ln = [t, t - 6, 150] if ragged else None
+    for q in range(n):
+        end = t if ln is None else ln[q]
+        i["u"][q, :end - 20] = 0
+        i["dy"][q, 20:] = 0
+    names = ("du", "ddt", "da", "db", "dc", "dd", "dz", "dh_in")
+    y, h, got = _scan(i, n, t, c, s, g, F32, False, ln, names)
+    ((ry, rh), (my, mh)), (ref, mag) = _scan_bounds(i, ln, False)
+    depth = 4 * t + 2 * s + 640  # as in test_seq_gpu: exponents here are 3, their roundings far below 64
+    so.assert_close(y, ry, my, depth, "y")
+    so.assert_close(h, rh, mh, depth, "h_out")
+    for k, v in got.items():
+        so.assert_close(v, ref[k], mag[k], 2 * depth + n * t + c, k)
+
+
+def test_a_chunk_may_grow_by_more_than_fp32_holds(cuda_device):
+    """States of 1e-30 times e**144 over the first chunk, and gradients the same over the last."""
+    n, t, c, s = 2, 200, 64, 16
+    i = base.scan_inputs(n, t, c, s, 1, F32, False, "h", 510)
+    i["a"] = torch.full((c, s), -6.0)
+    for first, k in ((0, "h_in"), (t - 24, "dh_out")):
+        i["dt"] = torch.zeros(n, t, c)
+        i["dt"][:, first:first + 24] = -1.0
+        j = dict(i, u=torch.zeros(n, t, c), dy=torch.zeros(n, t, c), h_in=None, dh_out=None)
+        j[k] = i[k] * 1e-30
+        y, h, got = _scan(j, n, t, c, s, 1, F32, False, None, ("dh_in",))
+        ((ry, rh), (my, mh)), (ref, mag) = _scan_bounds(j, None, False)
+        # an exponent of 144, formed of at most three rounded products
+        depth = 4 * t + 2 * s + 640 + 4 * 144
+        so.assert_close(y, ry, my, depth, "y")
+        so.assert_close(h, rh, mh, depth, "h_out")
+        so.assert_close(got["dh_in"], ref["dh_in"], mag["dh_in"], depth, "dh_in")
+
+
+# ------------------------------------------------ states forgotten at once
+
+@pytest.mark.parametrize("t,s", [(1, 16), (5, 16), (6, 4), (131, 16), (200, 40)])
+def test_states_forgotten_at_once(cuda_device, t, s):
+    """A = -inf: exp(delta A) is zero for every step, and a sequence's state
+    does not change after its last token."""
+    n, c = 4, 36
+    i = base.scan_inputs(n, t, c, s, 2, F32, True, "dzbh", 520 + t)
+    i["a"][:, 0] = -INF
+    i["a"][5, s // 2] = -INF
+    ln = [t, 0, 1, max(1, t - 2)]
+    names = ("du", "da", "db", "dc", "dd", "dz", "dh_in")  # ddt's formula is inf * 0 there
+    y, h, got = _scan(i, n, t, c, s, 2, F32, True, ln, names)
+    ((ry, rh), (my, mh)), (ref, mag) = _scan_bounds(i, ln, True)
+    depth = 4 * t + 2 * s + 640
+    so.assert_close(y, ry, my, depth, "y")
+    so.assert_close(h, rh, mh, depth, "h_out")
+    for k, v in got.items():
+        so.assert_close(v, ref[k], mag[k], 2 * depth + n * t + c, k)
+
+
+# ------------------------------- zeros after the valid tokens, whatever precedes
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("s", [4, 8, 16, 64])
+def test_scan_results_after_an_infinite_token_are_zero(cuda_device, s, dtype):
+    n, t, c, g = 3, 75, 40, 2
+    i = base.scan_inputs(n, t, c, s, g, dtype, True, "dzbh", 530 + s)
+    ln = [5, 70, 13]
+    for q, end in enumerate(ln):
+        i["u"][q, end - 1, 3] = INF
+    names = ("du", "ddt", "db", "dc", "dz")
+    y, _, got = _scan(i, n, t, c, s, g, dtype, True, ln, names)
+    for k, v in dict(got, y=y).items():
+        for q, end in enumerate(ln):
+            assert bool((v[q, end:] == 0).all()), (k, q)
+
+
+@pytest.mark.parametrize("dtype,c,k", [(BF, 24, 4), (F32, 24, 4), (BF, 5, 3), (F32, 9, 8), (BF, 16, 2)])
+def test_conv1d_gradients_after_an_infinite_token_are_zero(cuda_device, dtype, c, k):
+    g = torch.Generator().manual_seed(540 + c)
+    n, t = 4, 40
+    x, w, dy = base.rn(g, n, t, c, dtype=dtype), base.rn(g, k, c, dtype=dtype), base.rn(g, n, t, c, dtype=dtype)
+    ln = [5, 33, 8, 39]
+    for q, end in enumerate(ln):
+        x[q, end - 1, 2] = INF
+    plan = cc3d.causal_conv1d_plan(cc3d.make_conv1d_desc(n, t, c, k, act="silu", dtype=dtype))
+    dx = base.nan(n, t, c, dtype=dtype)
+    cc3d.causal_conv1d_backward(plan, base.dev(x), base.dev(w), None, base.dev(dy), dx=dx, workspace=base.space(plan, True),
+                                lengths=torch.tensor(ln, dtype=torch.int32, device=DEV))
+    for q, end in enumerate(ln):
+        assert bool((dx[q, end:] == 0).all()), q
+        assert bool(torch.isfinite(dx[q, :end - k].float()).all()), q
+
+
+# --------------------------------------------------------- another call's error
+
+def test_an_error_of_another_call_is_not_taken_for_one_of_the_launch(cuda_device):
+    """The runtime keeps the last error of a thread until it is asked for it."""
+    hip = ctypes.CDLL("libamdhip64.so.7")
+    launch, o, _ = base._everything(57)
+    launch()
+    torch.cuda.synchronize()
+    first = {k: v.clone() for k, v in o.items()}
+    for v in o.values():
+        v.fill_(base.NAN)
+    assert hip.hipGetLastError() == 0
+    bad = hip.hipSetDevice(1 << 20)
+    assert bad != 0
+    try:
+        launch()
+        assert hip.hipGetLastError() == bad  # and it is still there for whom it concerns
+    finally:
+        hip.hipGetLastError()
+    torch.cuda.synchronize()
+    for k, v in o.items():
+        assert torch.equal(v, first[k]), k
