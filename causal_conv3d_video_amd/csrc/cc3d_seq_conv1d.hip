@@ -339,7 +339,7 @@ Conv1dArgs base_args(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& c, int
   a.n = p.d.n;
   a.t = p.d.t;
   a.c = p.d.c;
-  a.vecs = (a.c + 7) / 8;
+  a.vecs = int((int64_t(a.c) + 7) / 8);
   a.seg = seg;
   a.nseg = (a.t + seg - 1) / seg;
   a.items = int64_t(a.n) * a.nseg;

@@ -58,7 +58,7 @@ constexpr int kScanFwdStates = 16;
 constexpr int kScanMaxStates = 64;
 
 inline int scan_tiles_per_group(const cc3d_scan_desc_t& d) {
-  return (d.d / d.groups + kScanLanes - 1) / kScanLanes;
+  return (d.d / d.groups - 1) / kScanLanes + 1;
 }
 // States a wave holds, and waves that share one tile of channels.
 inline int scan_fwd_ns(const cc3d_scan_desc_t& d) { return d.states <= 4 ? 4 : d.states <= 8 ? 8 : 16; }
@@ -89,7 +89,7 @@ inline ScanBwdShape scan_bwd_shape(const cc3d_scan_desc_t& d) {
   const int wide = d.d / d.groups, each = 128 / v.sg;
   v.wc = 1;
   while (v.wc * 2 * v.waves <= 4 && v.wc * each < wide) v.wc *= 2;
-  v.tiles_per_group = (wide + each * v.wc - 1) / (each * v.wc);
+  v.tiles_per_group = (wide - 1) / (each * v.wc) + 1;
   // 64 tokens keep seven states a lane's element between them, 32 those of four-token walks
   const int most = v.sg == 1 ? 32 : 64;
   v.chunk = d.t >= most ? most : (d.t + v.sub - 1) / v.sub * v.sub;

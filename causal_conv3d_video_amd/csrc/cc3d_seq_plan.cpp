@@ -44,6 +44,9 @@ constexpr int64_t kMaxSpan = int64_t(1) << 46;
 // Elements between two tokens of the scan: offsets inside a chunk of 64
 // tokens are 32 bits.
 constexpr int64_t kMaxRow = (int64_t(1) << 25) - 1;
+// Channels of the scan: the last lane of a channel tile, up to 512 wide, counts
+// in 32 bits too.
+constexpr int32_t kMaxScanChannels = INT32_MAX - 511;
 // Tokens of one call: token counters are 32 bits and run a chunk past the end.
 constexpr int32_t kMaxTokens = 1 << 30;
 
@@ -278,7 +281,7 @@ extern "C" cc3d_status_t selective_scan_plan(const cc3d_scan_desc_t* d, cc3d_sca
   if (!d || d->n < 1 || d->t < 1 || d->d < 1 || d->states < 1 || d->groups < 1 || d->d % d->groups ||
       (d->softplus != 0 && d->softplus != 1) || !known_dtype(d->dtype))
     return refuse(CC3D_ERR_INVALID_ARG);
-  if (d->states > cc3d::kScanMaxStates || d->t > kMaxTokens) return refuse(CC3D_ERR_UNSUPPORTED);
+  if (d->states > cc3d::kScanMaxStates || d->t > kMaxTokens || d->d > kMaxScanChannels) return refuse(CC3D_ERR_UNSUPPORTED);
   // (an output of more elements than a view may span would be refused by every call)
   if (int64_t(d->n) * d->t > kMaxSpan / d->d) return refuse(CC3D_ERR_UNSUPPORTED);
   const int64_t tiles = int64_t(d->groups) * cc3d::scan_tiles_per_group(*d), nc = int64_t(d->n);
@@ -315,7 +318,7 @@ extern "C" cc3d_status_t selective_scan_plan(const cc3d_scan_desc_t* d, cc3d_sca
   // partial sums: dA [worker][C][S], dD and ddt_bias [worker * waves][C], dB and dC [tile][n][t][waves][2][4 sg]
   int64_t ws = 0;
   if (bwd_chunks > 1) ws += nc * bwd_chunks * (2 * state + d->d);
-  ws += int64_t(p->bwd_workers) * (state + 2 * bw.waves * d->d);
+  ws += int64_t(p->bwd_workers) * (state + 2 * bw.waves * int64_t(d->d));
   ws += bwd_tiles * nc * d->t * bw.waves * 8 * bw.sg;
   p->info.backward_workspace_bytes = ws * 4;
   *out = p;

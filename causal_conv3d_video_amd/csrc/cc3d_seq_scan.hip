@@ -144,7 +144,9 @@ __global__ __launch_bounds__(256) void scan_step(ScanArgs a, unsigned per_sequen
   float h[4] = {}, sum = 0.f, uu = 0.f;
   const bool valid = valid_tokens(a, int(n)) > 0;
   if (left > 0) {
-    const T *b = rows<T>(a.b, int(n)) + group * a.s + s0, *c = rows<T>(a.c, int(n)) + group * a.s + s0;
+    // (a row of B or C may hold more than 2^31 elements here; with more tokens the plan's limits keep it below)
+    const int64_t bc_at = int64_t(group) * a.s + s0;
+    const T *b = rows<T>(a.b, int(n)) + bc_at, *c = rows<T>(a.c, int(n)) + bc_at;
     const float* aa = a.a + int64_t(chan) * a.s + s0;
     float a4[4] = {}, b4[4] = {}, c4[4] = {};
     if constexpr (VEC) {

@@ -92,7 +92,7 @@ typedef struct cc3d_seq_info {
  * dw and db are fp32, summed over all sequences.
  * ------------------------------------------------------------------------ */
 typedef struct cc3d_conv1d_desc {
-  int32_t n, t, c;   /* sequences, tokens, channels; >= 1 */
+  int32_t n, t, c;   /* sequences, tokens (up to 2^30), channels; >= 1 */
   int32_t k;         /* taps, 1..8 */
   int32_t act;       /* cc3d_act_t */
   int32_t dtype;     /* cc3d_dtype_t of every tensor but dw and db */
@@ -148,7 +148,8 @@ cc3d_status_t causal_conv1d_backward(cc3d_conv1d_plan_t plan, const cc3d_conv1d_
  * The states are computed again from h_in; nothing is kept by the forward
  * call.  Any gradient may be left out (NULL).  With A >= 0 the recurrence
  * grows and may overflow, as the formula does.  Views whose tokens are 2^25
- * elements or more apart are refused as unsupported (but with T = 1).
+ * elements or more apart are refused as unsupported (but with T = 1), and so
+ * are more than 2^31 - 512 channels and 2^30 tokens.
  * ------------------------------------------------------------------------ */
 typedef struct cc3d_scan_desc {
   int32_t n, t, d;    /* sequences, tokens, channels; >= 1 */

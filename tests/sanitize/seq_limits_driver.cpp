@@ -2,6 +2,7 @@
 // the sequence operators' plans and argument checks under the sanitizers, with
 // the launches replaced by ones that only count.
 #include <cstdio>
+#include <initializer_list>
 
 #include "cc3d_seq_internal.h"
 
@@ -110,6 +111,14 @@ int main() {
   expect(scan(INT32_MAX, 1 << 30, INT32_MAX, 64, 1) == CC3D_ERR_UNSUPPORTED, "2^92 elements");
   expect(scan(INT32_MAX, 1, INT32_MAX, 64, INT32_MAX) == CC3D_ERR_UNSUPPORTED, "2^62 elements");
   expect(conv(INT32_MAX, 1 << 30, INT32_MAX, 8) == CC3D_ERR_UNSUPPORTED, "2^92 elements");
+  // counts next to 2^31
+  for (int c : {INT32_MAX, INT32_MAX - 6, INT32_MAX - 7})
+    expect(conv(1, 1, c, 1, &f, &b) == CC3D_OK && f == CC3D_OK && b == CC3D_OK, "convolution of 2^31 - 1 channels");
+  for (int c : {INT32_MAX, INT32_MAX - 63, INT32_MAX - 510})
+    expect(scan(1, 1, c, 1, 1) == CC3D_ERR_UNSUPPORTED, "scan of 2^31 - 1 channels");
+  expect(scan(1, 1, INT32_MAX - 511, 1, 1, &f) == CC3D_OK && f == CC3D_OK, "scan of 2^31 - 512 channels");
+  expect(scan(1, 1, 1 << 26, 64, 1 << 26, &f, &b) == CC3D_OK && f == CC3D_OK && b == CC3D_ERR_UNSUPPORTED, "2^32 elements of B");
+  expect(scan(1, 2, 1 << 26, 64, 1 << 26) == CC3D_ERR_UNSUPPORTED, "the same of two tokens");
   std::printf("%ld checks, %ld failed checks, %ld launches\n", checks, failed, launches);
   return failed != 0;
 }

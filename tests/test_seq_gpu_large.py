@@ -45,3 +45,44 @@ def test_grids_go_on_in_turns(cuda_device, n, t, c, s, g):
         for q in range(0, n, 64):
             part = got[k][q:q + 64]
             assert torch.equal(part, v.expand_as(part)), (k, q)
+
+
+def test_a_row_of_b_and_c_past_32_bits(cuda_device):
+    """One token of 2**25 + 64 groups of 64 states: the last groups' B and C lie past 2**31 elements."""
+    c, s, part = (1 << 25) + 64, 64, 128
+    g = torch.Generator(device=DEV).manual_seed(610)
+
+    def rn(*shape, dtype=BF, scale=1.0):
+        return torch.randn(*shape, generator=g, device=DEV, dtype=dtype).mul_(scale)
+
+    u, dt, b, cc = rn(1, 1, c), rn(1, 1, c), rn(1, 1, c, s), rn(1, 1, c, s)
+    a = rn(c, s, dtype=F32).abs_().neg_()
+    h_in = rn(1, c, s, dtype=F32)
+
+    def call(lo, hi):
+        n = hi - lo
+        plan = cc3d.selective_scan_plan(cc3d.make_scan_desc(1, 1, n, s, groups=n))
+        y = base.nan(1, 1, n, dtype=BF)
+        cc3d.selective_scan_forward(plan, u[:, :, lo:hi], dt[:, :, lo:hi], a[lo:hi], b[:, :, lo:hi], cc[:, :, lo:hi], y,
+                                    h_in=h_in[:, lo:hi].contiguous())
+        return y
+
+    whole = call(0, c)
+    for lo in (0, (1 << 25) - part // 2, c - part):
+        y = call(lo, lo + part)
+        assert bool(torch.isfinite(y.float()).all()) and torch.equal(whole[:, :, lo:lo + part], y), lo
+
+
+def test_conv1d_of_all_channels_32_bits_count(cuda_device):
+    """C = 2**31 - 1, one tap and no activation: y = w x and dx = w dy, rounded once."""
+    c = (1 << 31) - 1
+    g = torch.Generator(device=DEV).manual_seed(620)
+    x, w = (torch.randn(c, generator=g, device=DEV, dtype=BF) for _ in range(2))
+    plan = cc3d.causal_conv1d_plan(cc3d.make_conv1d_desc(1, 1, c, 1))
+    y = torch.full_like(x, float("nan"))
+    cc3d.causal_conv1d_forward(plan, x.view(1, 1, c), w.view(1, c), None, y.view(1, 1, c))
+    assert torch.equal(y, x * w)
+    y.fill_(float("nan"))
+    space = torch.empty(plan.info["backward_workspace_bytes"], dtype=torch.uint8, device=DEV)
+    cc3d.causal_conv1d_backward(plan, x.view(1, 1, c), w.view(1, c), None, x.view(1, 1, c), dx=y.view(1, 1, c), workspace=space)
+    assert torch.equal(y, x * w)
