@@ -204,11 +204,12 @@ __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) win[i][j] = ld.get(j);
     }
-    // kBack tokens load while kBack are computed; those past the valid ones are
-    // read from the last and taken as zero
-    const int end = t1 + K - 1, last = max(min(end, len) - 1, 0);
+    // kBack tokens load while kBack are computed; for those past the valid ones
+    // the last is read, or none where all are, and they are taken as zero
+    const int end = t1 + K - 1, last = min(end, len) - 1;
     Lane<T, FEW> next_x[kBack], next_d[kBack];
     auto fetch = [&](int from) {
+      if (from > last) return;
 #pragma unroll
       for (int i = 0; i < kBack; ++i) {
         const int64_t t = min(from + i, last);

@@ -152,9 +152,13 @@ __global__ __launch_bounds__(256) void scan_step(ScanArgs a, unsigned per_sequen
     if constexpr (VEC) {
       using U = std::conditional_t<sizeof(T) == 4, f32x4_s, unsigned long long>;
       const f32x4_s va = *reinterpret_cast<const f32x4_s*>(aa);
-      const U vb = *reinterpret_cast<const U*>(b), vc = *reinterpret_cast<const U*>(c);
       f32x4_s vh{0.f, 0.f, 0.f, 0.f};
       if (a.h_in) vh = *reinterpret_cast<const f32x4_s*>(a.h_in + state_at);
+      U vb{}, vc{};
+      if (valid) {
+        vb = *reinterpret_cast<const U*>(b);
+        vc = *reinterpret_cast<const U*>(c);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         h[i] = vh[i];
@@ -173,8 +177,8 @@ __global__ __launch_bounds__(256) void scan_step(ScanArgs a, unsigned per_sequen
         if (i < left) {
           if (a.h_in) h[i] = a.h_in[state_at + i];
           a4[i] = aa[i];
-          b4[i] = to_f32(b[i]);
-          c4[i] = to_f32(c[i]);
+          b4[i] = valid ? to_f32(b[i]) : 0.f;
+          c4[i] = valid ? to_f32(c[i]) : 0.f;
         }
     }
     if (valid) {

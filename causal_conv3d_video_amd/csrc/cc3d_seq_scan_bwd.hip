@@ -256,12 +256,12 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
     float* pbc = a.part_bc + (int64_t(tile) * a.n + n) * a.t * waves * kVal;
 
     // Inputs of the tokens of one walk: this lane group's tokens, and this
-    // lane's share of B and C.  Tokens past the valid ones are read where they
-    // are (and not used); past the tensor, the walk's first is read instead.
+    // lane's share of B and C.  For tokens past the valid ones the walk's first
+    // is read (and not used).
     Pair<T> rdt[NB], ru[NB], rz[NB], rdy[NB];
     T rbc[kBcEach];
     auto fetch = [&](int k, auto back) {
-      const int there = a.t - t0 - k * SUB;
+      const int there = te - t0 - k * SUB;  // at least one
       const Walk dt = walk(offsetof(ScanArgs, dt), k), u = walk(offsetof(ScanArgs, u), k);
       const T* bp = walk(offsetof(ScanArgs, b), k).p + group * a.s + sw * 4 * SG;
       const T* cp = walk(offsetof(ScanArgs, c), k).p + group * a.s + sw * 4 * SG;
