@@ -117,14 +117,15 @@ __device__ __forceinline__ float sigmoid_f32(float v) {
 }
 
 // log(1 + exp(v)), v itself above 20 (where exp(-v) is below half a unit in
-// the last place of v).  log2 of a number near 1 loses the small one, so
-// below -4, where e = exp(v) < 0.02, the series e - e^2/2 + e^3/3 - e^4/4
-// (its next term is below 2^-25 of the first).
+// the last place of v).  What w = 1 + e loses of e = exp(v), e - (w - 1)
+// (no rounding for e <= 1), is added back: log(1 + e) = log(w) + lost / w, the
+// next order below 2^-25 of the result.  Against 64 bits over a million
+// values: 4 units of 2^-24 above 0, 6.4 at -4 (55.7 without), and below that
+// the rounding of the exponential's argument, |v| or so.
 __device__ __forceinline__ float softplus_f32(float v) {
-  const float e = __builtin_amdgcn_exp2f(v * kLog2e);
-  const float series = e * (1.f + e * (-0.5f + e * (0.33333333f - 0.25f * e)));
-  const float full = kLn2 * __builtin_amdgcn_logf(1.f + e);
-  return v > 20.f ? v : v < -4.f ? series : full;
+  const float e = __builtin_amdgcn_exp2f(v * kLog2e), w = 1.f + e;
+  const float log1p = fmaf(e - (w - 1.f), __builtin_amdgcn_rcpf(w), kLn2 * __builtin_amdgcn_logf(w));
+  return v > 20.f ? v : log1p;
 }
 
 // v from lane ^ X of the wave, X = 1, 2, 4 or 8 (reached by mirroring half a
