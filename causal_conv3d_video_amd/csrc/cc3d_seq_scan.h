@@ -5,6 +5,7 @@
 #include "cc3d_seq_device.h"
 
 #include <algorithm>
+#include <cfloat>
 
 namespace {
 
@@ -199,7 +200,9 @@ __device__ __forceinline__ void spread_rows(const Feed<T, NS, ROWS>& f, float* b
 //   G = sum_t exp(A sum_{s <= t} delta_s) C gy,  gy = dy silu(z),
 // taken forward too, with the running product of the same decays: one walk and one
 // exponential a token and state serve both.  2 x 2049 tokens of 2048 channels, 16
-// states: 63 us, where a walk each way took 43 + 37.
+// states: 63 us, where a walk each way took 43 + 37.  Where decays grow (delta A
+// > 0) that product may overflow beside a gradient that is zero; such a wave
+// walks back over its chunk as the formula does, one token after another.
 template <class T, int NS, bool BACK, bool MULTI>
 __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void scan_carry(ScanArgs a) {
   constexpr int kRows = BACK ? 2 : 1;
@@ -284,6 +287,28 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
       }
     }
   }
+  if constexpr (BACK) {
+    bool over = false;  // once infinite, or not a number, it stays so
+#pragma unroll
+    for (int i = 0; i < NS; ++i) over |= !(through[i] <= FLT_MAX);
+    if (__any(over)) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) g[i] = 0.f;
+      for (int t = te - 1; t >= t0; --t) {
+        auto token = [&](const ScanRows& v) { return rows<T>(v, n) + int64_t(t) * v.row; };
+        const float delta = delta_of(a, to_f32(token(a.dt)[at.chan]) + bias);
+        const T* c = token(a.c) + at.group * a.s + s0;
+        float gy = to_f32(token(a.dy)[at.chan]);
+        if (a.z.p) {
+          const float v = to_f32(token(a.z)[at.chan]);
+          gy *= v * sigmoid_f32(v);
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+          if (i < states) g[i] = __builtin_amdgcn_exp2f(delta * a2[i]) * fmaf(gy, to_f32(c[i]), g[i]);
+      }
+    }
+  }
   const int channels = a.groups * a.wide;
   const int64_t out = (at.item * a.s + s0) * channels + at.chan;
 #pragma unroll
@@ -298,12 +323,28 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
 // Turns what every chunk adds into the state that enters it, from the
 // sequence's first state on, and, in the grid's second half where there is one,
 // the gradient that enters it from the right.
+// A chunk's decay is kept as an exponent of two, as it may overflow where its
+// product with the state does not.
 // A workgroup takes 64 channels of one state; each wave loads 16 chunks at
 // once and joins them, and the waves' joined stretches meet in LDS, so the
 // loads of a long sequence are not one after another.  8.8 us for 128
 // chunks of 2048 channels and 16 states.  A grid of up to kJoinGrid workgroups
 // takes all of them in turns: `all` of up to 1024 threads each may be more
 // threads than a launch holds.
+struct Decay {
+  float part;  // in (0.5, 1]
+  int whole;
+  __device__ __forceinline__ Decay() {}
+  // (past +-2000 it is zero or infinite anyway; a NaN is in the chunk's sum as well)
+  __device__ __forceinline__ explicit Decay(float x) {
+    x = __builtin_amdgcn_fmed3f(x, -2000.f, 2000.f);
+    const float w = ceilf(x);
+    part = __builtin_amdgcn_exp2f(x - w);
+    whole = int(w);
+  }
+  __device__ __forceinline__ float of(float h) const { return __builtin_ldexpf(h * part, whole); }
+};
+
 constexpr int kJoinChunks = 16, kJoinWaves = 16;
 constexpr unsigned kJoinGrid = 1u << 16;
 
@@ -327,21 +368,22 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a, unsigne
     const int64_t step = int64_t(a.s) * channels;
     for (int base = 0; base < a.chunks; base += kJoinChunks * waves) {
       const int c0 = base + wave * kJoinChunks;
-      float add[kJoinChunks], decay[kJoinChunks], total = 0.f, h = 0.f;
+      float add[kJoinChunks], sum[kJoinChunks], total = 0.f, h = 0.f;
+      Decay decay[kJoinChunks];
 #pragma unroll
       for (int i = 0; i < kJoinChunks; ++i) {
         const int k = min(c0 + i, a.chunks - 1), c = rev ? a.chunks - 1 - k : k;
         add[i] = carry[c * step];
-        decay[i] = sums[int64_t(c) * channels];
+        sum[i] = sums[int64_t(c) * channels];
       }
 #pragma unroll
       for (int i = 0; i < kJoinChunks; ++i) {
         const bool in = c0 + i < a.chunks;
         add[i] = in ? add[i] : 0.f;
-        decay[i] = in ? decay[i] : 0.f;
-        total += decay[i];
-        decay[i] = __builtin_amdgcn_exp2f(decay[i] * a2);
-        h = fmaf(decay[i], h, add[i]);
+        sum[i] = in ? sum[i] : 0.f;
+        total += sum[i];
+        decay[i] = Decay(sum[i] * a2);
+        h = decay[i].of(h) + add[i];
       }
       __syncthreads();
       add_of[wave][lane] = h;
@@ -350,13 +392,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a, unsigne
       float mine = enter;
       for (int w = 0; w < waves; ++w) {
         if (w == wave) mine = enter;
-        enter = fmaf(__builtin_amdgcn_exp2f(sum_of[w][lane] * a2), enter, add_of[w][lane]);
+        enter = Decay(sum_of[w][lane] * a2).of(enter) + add_of[w][lane];
       }
 #pragma unroll
       for (int i = 0; i < kJoinChunks; ++i) {
         const int k = c0 + i, c = rev ? a.chunks - 1 - k : k;
         if (k < a.chunks && on) carry[c * step] = mine;
-        mine = fmaf(decay[i], mine, add[i]);
+        mine = decay[i].of(mine) + add[i];
       }
     }
   }

@@ -146,8 +146,10 @@ cc3d_status_t causal_conv1d_backward(cc3d_conv1d_plan_t plan, const cc3d_conv1d_
  *   dB = sum over the group's channels of g * delta * u;  dC of gy * h
  *   dz = dy * (sum_s C * h + D * u) * silu'(z);  dh_in = exp(delta[0] * A) * g[0]
  * The states are computed again from h_in; nothing is kept by the forward
- * call.  Any gradient may be left out (NULL).  With A >= 0 the recurrence
- * grows and may overflow, as the formula does.  Views whose tokens are 2^25
+ * call.  Any gradient may be left out (NULL).  Where decays grow (delta A > 0)
+ * states and gradients may overflow, as the formula's do; what a piece of the
+ * time axis adds is found from zero, so large parts that cancel across pieces
+ * may overflow too.  Views whose tokens are 2^25
  * elements or more apart are refused as unsupported (but with T = 1), and so
  * are more than 2^31 - 512 channels and 2^30 tokens.
  * ------------------------------------------------------------------------ */

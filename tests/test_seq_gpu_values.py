@@ -11,6 +11,31 @@ F32 = torch.float32
 DEV = base.DEV
 
 
+def _scan_bounds(i, lengths, softplus):
+    """(reference, magnitudes) of y and h_out, and of the gradients."""
+    o = [base.d64(i[k]) for k in ("u", "dt", "a", "b", "c", "d", "z", "dt_bias", "h_in")] + [lengths, softplus]
+    g = [base.d64(i[k]) for k in ("u", "dt", "a", "b", "c", "dy", "d", "z", "dt_bias", "h_in", "dh_out")] + [lengths,
+                                                                                                            softplus]
+    return (so.scan(*o)[:2], so.scan(*o, mag=True)[:2]), (so.scan_grad(*g), so.scan_grad(*g, mag=True))
+
+
+def _scan(i, n, t, c, s, g, dtype, softplus, lengths=None, names=()):
+    """y, h_out and the named gradients of one call each way."""
+    plan = cc3d.selective_scan_plan(cc3d.make_scan_desc(n, t, c, s, groups=g, softplus=softplus, dtype=dtype))
+    j = {k: base.dev(v) for k, v in i.items()}
+    lt = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    opt = dict(d=j["d"], z=j["z"], dt_bias=j["dt_bias"], h_in=j["h_in"], lengths=lt)
+    ins = [j[k] for k in ("u", "dt", "a", "b", "c")]
+    y, h = base.nan(n, t, c, dtype=dtype), base.nan(n, c, s)
+    cc3d.selective_scan_forward(plan, *ins, y, h_out=h, workspace=base.space(plan), **opt)
+    like = dict(du="u", ddt="dt", da="a", db="b", dc="c", dd="d", dz="z", ddt_bias="dt_bias")
+    got = {k: base.nan(*(j[like[k]].shape if k in like else (n, c, s)),
+                       dtype=dtype if k in ("du", "ddt", "db", "dc", "dz") else F32) for k in names}
+    if names:
+        cc3d.selective_scan_backward(plan, *ins, j["dy"], dh_out=j["dh_out"], workspace=base.space(plan, True), **opt, **got)
+    return y, h, got
+
+
 # ---------------------------------------------------------------- softplus
 
 def test_softplus_is_good_to_a_few_roundings_over_its_range(cuda_device):
@@ -43,3 +68,48 @@ def test_softplus_is_good_to_a_few_roundings_over_its_range(cuda_device):
             over = (got[0, q].cpu().double() - want).abs() - bound
             k = int(over.argmax())
             assert float(over[k]) <= 0, (what, q, float(v[k]), float(over[k] / (so.EPS32 * want[k])))
+
+
+# ------------------------------------------------------- growing recurrences
+
+@pytest.mark.parametrize("t,s,ragged", [(700, 16, False), (700, 4, True), (330, 40, True)])
+def test_growing_recurrences_stay_finite_where_the_formula_does(cuda_device, t, s, ragged):
+    """Every token's decay is e**3, so a chunk of 32 tokens multiplies by more
+    than fp32 holds; inputs are zero but in the last 20 tokens and gradients
+    but in the first 20, so nothing in the formula comes near that."""
+    n, c, g = 3, 70, 2
+    i = base.scan_inputs(n, t, c, s, g, F32, False, "dz", 500 + t + s)
+    i["dt"] = torch.full((n, t, c), -1.0)
+    i["a"] = torch.full((c, s), -3.0)
+    ln = [t, t - 6, 150] if ragged else None
+    for q in range(n):
+        end = t if ln is None else ln[q]
+        i["u"][q, :end - 20] = 0
+        i["dy"][q, 20:] = 0
+    names = ("du", "ddt", "da", "db", "dc", "dd", "dz", "dh_in")
+    y, h, got = _scan(i, n, t, c, s, g, F32, False, ln, names)
+    ((ry, rh), (my, mh)), (ref, mag) = _scan_bounds(i, ln, False)
+    depth = 4 * t + 2 * s + 640  # as in test_seq_gpu: exponents here are 3, their roundings far below 64
+    so.assert_close(y, ry, my, depth, "y")
+    so.assert_close(h, rh, mh, depth, "h_out")
+    for k, v in got.items():
+        so.assert_close(v, ref[k], mag[k], 2 * depth + n * t + c, k)
+
+
+def test_a_chunk_may_grow_by_more_than_fp32_holds(cuda_device):
+    """States of 1e-30 times e**144 over the first chunk, and gradients the same over the last."""
+    n, t, c, s = 2, 200, 64, 16
+    i = base.scan_inputs(n, t, c, s, 1, F32, False, "h", 510)
+    i["a"] = torch.full((c, s), -6.0)
+    for first, k in ((0, "h_in"), (t - 24, "dh_out")):
+        i["dt"] = torch.zeros(n, t, c)
+        i["dt"][:, first:first + 24] = -1.0
+        j = dict(i, u=torch.zeros(n, t, c), dy=torch.zeros(n, t, c), h_in=None, dh_out=None)
+        j[k] = i[k] * 1e-30
+        y, h, got = _scan(j, n, t, c, s, 1, F32, False, None, ("dh_in",))
+        ((ry, rh), (my, mh)), (ref, mag) = _scan_bounds(j, None, False)
+        # an exponent of 144, formed of at most three rounded products
+        depth = 4 * t + 2 * s + 640 + 4 * 144
+        so.assert_close(y, ry, my, depth, "y")
+        so.assert_close(h, rh, mh, depth, "h_out")
+        so.assert_close(got["dh_in"], ref["dh_in"], mag["dh_in"], depth, "dh_in")
