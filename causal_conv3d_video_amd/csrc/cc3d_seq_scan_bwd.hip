@@ -503,12 +503,13 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
       }
 
       __syncthreads();
-      const int more = waves * L::kComb;
+      // (a token past the valid ones has zeros here, unless a state or gradient is infinite)
+      const int more = waves * L::kComb, held = (te - tb) * waves * kVal;
       for (int i = threadIdx.x; i < more; i += 64 * waves * wc) {
         float s = comb[i];
         if (wc == 4) s += comb[more + i] + comb[2 * more + i] + comb[3 * more + i];
         else if (wc == 2) s += comb[more + i];
-        if (i < (t1 - tb) * waves * kVal) pbc[int64_t(tb) * waves * kVal + i] = s;
+        if (i < (t1 - tb) * waves * kVal) pbc[int64_t(tb) * waves * kVal + i] = i < held ? s : 0.f;
       }
       if constexpr (MULTI) {
 #pragma unroll

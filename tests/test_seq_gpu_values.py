@@ -7,8 +7,9 @@ import seq_oracle as so
 import test_seq_gpu as base
 
 pytestmark = pytest.mark.gpu
-F32 = torch.float32
+BF, F32 = torch.bfloat16, torch.float32
 DEV = base.DEV
+INF = float("inf")
 
 
 def _scan_bounds(i, lengths, softplus):
@@ -113,3 +114,20 @@ def test_a_chunk_may_grow_by_more_than_fp32_holds(cuda_device):
         so.assert_close(y, ry, my, depth, "y")
         so.assert_close(h, rh, mh, depth, "h_out")
         so.assert_close(got["dh_in"], ref["dh_in"], mag["dh_in"], depth, "dh_in")
+
+
+# ------------------------------- zeros after the valid tokens, whatever precedes
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("s", [4, 8, 16, 64])
+def test_scan_results_after_an_infinite_token_are_zero(cuda_device, s, dtype):
+    n, t, c, g = 3, 75, 40, 2
+    i = base.scan_inputs(n, t, c, s, g, dtype, True, "dzbh", 530 + s)
+    ln = [5, 70, 13]
+    for q, end in enumerate(ln):
+        i["u"][q, end - 1, 3] = INF
+    names = ("du", "ddt", "db", "dc", "dz")
+    y, _, got = _scan(i, n, t, c, s, g, dtype, True, ln, names)
+    for k, v in dict(got, y=y).items():
+        for q, end in enumerate(ln):
+            assert bool((v[q, end:] == 0).all()), (k, q)
