@@ -223,12 +223,10 @@ __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
       for (int i = 0; i < kGroup; ++i) {
         const int t = tb + i;
         if (t >= end) break;
-        Lane<T, FEW> now_x = next_x[i % kBack], now_d = next_d[i % kBack];
+        Lane<T, FEW> now_x = next_x[i % kBack];
+        const Lane<T, FEW> now_d = next_d[i % kBack];
         if (i % kBack == kBack - 1 && t + 1 < end) fetch(t + 1);
-        if (t >= len) {
-          now_x.zero();
-          now_d.zero();
-        }
+        if (t >= len) now_x.zero();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           win[i % K][j] = now_x.get(j);
@@ -240,7 +238,7 @@ __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
             const float sg_ = sigmoid_f32(s);
             g *= sg_ * (1.f + s * (1.f - sg_));
           }
-          dp[i % K][j] = g;
+          dp[i % K][j] = t < len ? g : 0.f;  // (also beside an infinite argument)
         }
         if (t < t1) {  // the K - 1 tokens after the run are another thread's
 #pragma unroll

@@ -131,3 +131,20 @@ def test_scan_results_after_an_infinite_token_are_zero(cuda_device, s, dtype):
     for k, v in dict(got, y=y).items():
         for q, end in enumerate(ln):
             assert bool((v[q, end:] == 0).all()), (k, q)
+
+
+@pytest.mark.parametrize("dtype,c,k", [(BF, 24, 4), (F32, 24, 4), (BF, 5, 3), (F32, 9, 8), (BF, 16, 2)])
+def test_conv1d_gradients_after_an_infinite_token_are_zero(cuda_device, dtype, c, k):
+    g = torch.Generator().manual_seed(540 + c)
+    n, t = 4, 40
+    x, w, dy = base.rn(g, n, t, c, dtype=dtype), base.rn(g, k, c, dtype=dtype), base.rn(g, n, t, c, dtype=dtype)
+    ln = [5, 33, 8, 39]
+    for q, end in enumerate(ln):
+        x[q, end - 1, 2] = INF
+    plan = cc3d.causal_conv1d_plan(cc3d.make_conv1d_desc(n, t, c, k, act="silu", dtype=dtype))
+    dx = base.nan(n, t, c, dtype=dtype)
+    cc3d.causal_conv1d_backward(plan, base.dev(x), base.dev(w), None, base.dev(dy), dx=dx, workspace=base.space(plan, True),
+                                lengths=torch.tensor(ln, dtype=torch.int32, device=DEV))
+    for q, end in enumerate(ln):
+        assert bool((dx[q, end:] == 0).all()), q
+        assert bool(torch.isfinite(dx[q, :max(0, end - k)].float()).all()), q
