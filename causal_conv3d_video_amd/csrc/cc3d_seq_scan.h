@@ -72,6 +72,14 @@ __device__ __forceinline__ float delta_of(const ScanArgs& a, float raw) {
   return a.softplus ? softplus_f32(raw) : raw;
 }
 
+// A as the exponent of two of a step of one.  A state that is forgotten at once,
+// A = -inf, has the lowest finite one instead: past a sequence's last token
+// steps are zero, and zero times it has to leave the state as it is.
+__device__ __forceinline__ float rate_of(float a) {
+  const float r = a * kLog2e;
+  return r < -FLT_MAX ? -FLT_MAX : r;
+}
+
 // Orders a wave's own LDS writes before its lanes' reads of each other's.
 __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -234,7 +242,7 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     h[i] = 0.f;
-    a2[i] *= kLog2e;
+    a2[i] = rate_of(a2[i]);
     if constexpr (BACK) {
       g[i] = 0.f;
       through[i] = 1.f;
@@ -360,7 +368,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a, unsigne
     const int tile = int(block - rest * tiles), n = int(rest / a.s), s = int(rest - int64_t(n) * a.s);
     const bool on = tile * 64 + lane < channels;
     const int chan = on ? tile * 64 + lane : channels - 1;
-    const float a2 = a.a[int64_t(chan) * a.s + s] * kLog2e;
+    const float a2 = rate_of(a.a[int64_t(chan) * a.s + s]);
     const float* first = rev ? a.dh_out : a.h_in;
     float enter = first ? first[(int64_t(n) * channels + chan) * a.s + s] : 0.f;
     float* carry = (rev ? a.gcarry : a.carry) + (int64_t(n) * a.chunks * a.s + s) * channels + chan;

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
   float h[NS] = {}, a2[NS];
   load_states<NS>(a.a + int64_t(at.first) * a.s + s0, a.s, states, at.live, at.lane, box, a2);
 #pragma unroll
-  for (int i = 0; i < NS; ++i) a2[i] *= kLog2e;
+  for (int i = 0; i < NS; ++i) a2[i] = rate_of(a2[i]);
   if (a.chunks > 1) {
 #pragma unroll
     for (int i = 0; i < NS; ++i)

@@ -214,10 +214,10 @@ __global__ __launch_bounds__(256, 2) void scan_bwd(ScanArgs a, int wc) {
     if (a.s % 4 == 0 && reinterpret_cast<uintptr_t>(a.a) % 16 == 0) {
       const f32x4_s v = s0 < a.s ? *reinterpret_cast<const f32x4_s*>(p) : f32x4_s{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a2[c][i] = v[i] * kLog2e;
+      for (int i = 0; i < 4; ++i) a2[c][i] = rate_of(v[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a2[c][i] = s0 + i < a.s ? p[i] * kLog2e : 0.f;
+      for (int i = 0; i < 4; ++i) a2[c][i] = s0 + i < a.s ? rate_of(p[i]) : 0.f;
     }
   }
   // (a branch costs more here than what it saves: flags select)

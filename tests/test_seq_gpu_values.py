@@ -148,3 +148,24 @@ def test_conv1d_gradients_after_an_infinite_token_are_zero(cuda_device, dtype, c
     for q, end in enumerate(ln):
         assert bool((dx[q, end:] == 0).all()), q
         assert bool(torch.isfinite(dx[q, :max(0, end - k)].float()).all()), q
+
+
+# ------------------------------------------------ states forgotten at once
+
+@pytest.mark.parametrize("t,s", [(1, 16), (5, 16), (6, 4), (131, 16), (200, 40)])
+def test_states_forgotten_at_once(cuda_device, t, s):
+    """A = -inf: exp(delta A) is zero for every step, and a sequence's state
+    does not change after its last token."""
+    n, c = 4, 36
+    i = base.scan_inputs(n, t, c, s, 2, F32, True, "dzbh", 520 + t)
+    i["a"][:, 0] = -INF
+    i["a"][5, s // 2] = -INF
+    ln = [t, 0, 1, max(1, t - 2)]
+    names = ("du", "da", "db", "dc", "dd", "dz", "dh_in")  # ddt's formula is inf * 0 there
+    y, h, got = _scan(i, n, t, c, s, 2, F32, True, ln, names)
+    ((ry, rh), (my, mh)), (ref, mag) = _scan_bounds(i, ln, True)
+    depth = 4 * t + 2 * s + 640
+    so.assert_close(y, ry, my, depth, "y")
+    so.assert_close(h, rh, mh, depth, "h_out")
+    for k, v in got.items():
+        so.assert_close(v, ref[k], mag[k], 2 * depth + n * t + c, k)
