@@ -293,23 +293,19 @@ __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {
 }
 
 template <class T, int K, bool SILU, bool FEW>
-void run_conv1d(const Conv1dArgs& a, bool backward, hipStream_t s) {
-  if (backward) {
-    const int lanes = cc3d::conv1d_lanes(a.c);
-    conv1d_bwd<T, K, FEW, SILU><<<unsigned(a.rows * ((a.vecs + lanes - 1) / lanes)), 256, 0, s>>>(a, lanes);
-  } else {
-    conv1d_fwd<T, K, FEW, SILU><<<unsigned((a.items * a.vecs + 255) / 256), 256, 0, s>>>(a);
-  }
+int run_conv1d(const Conv1dArgs& a, bool backward, hipStream_t s) {
+  if (!backward) return launch(conv1d_fwd<T, K, FEW, SILU>, (a.items * a.vecs + 255) / 256, 256, 0, s, a);
+  const int lanes = cc3d::conv1d_lanes(a.c);
+  return launch(conv1d_bwd<T, K, FEW, SILU>, a.rows * ((a.vecs + lanes - 1) / lanes), 256, 0, s, a, lanes);
 }
 
 template <class T, int K, bool SILU>
-void pick_few(const Conv1dArgs& a, bool backward, hipStream_t s) {
-  if (a.c < 8) run_conv1d<T, K, SILU, true>(a, backward, s);
-  else run_conv1d<T, K, SILU, false>(a, backward, s);
+int pick_few(const Conv1dArgs& a, bool backward, hipStream_t s) {
+  return a.c < 8 ? run_conv1d<T, K, SILU, true>(a, backward, s) : run_conv1d<T, K, SILU, false>(a, backward, s);
 }
 
 template <class T, bool SILU>
-void pick_taps(int k, const Conv1dArgs& a, bool backward, hipStream_t s) {
+int pick_taps(int k, const Conv1dArgs& a, bool backward, hipStream_t s) {
   switch (k) {
     case 1: return pick_few<T, 1, SILU>(a, backward, s);
     case 2: return pick_few<T, 2, SILU>(a, backward, s);
@@ -322,15 +318,10 @@ void pick_taps(int k, const Conv1dArgs& a, bool backward, hipStream_t s) {
   }
 }
 
-void pick_type(const cc3d_conv1d_desc_t& d, const Conv1dArgs& a, bool backward, hipStream_t s) {
+int pick_type(const cc3d_conv1d_desc_t& d, const Conv1dArgs& a, bool backward, hipStream_t s) {
   const bool silu = d.act == CC3D_ACT_SILU;
-  if (d.dtype == CC3D_BF16) {
-    if (silu) pick_taps<bf16_s, true>(d.k, a, backward, s);
-    else pick_taps<bf16_s, false>(d.k, a, backward, s);
-  } else {
-    if (silu) pick_taps<float, true>(d.k, a, backward, s);
-    else pick_taps<float, false>(d.k, a, backward, s);
-  }
+  if (d.dtype == CC3D_BF16) return silu ? pick_taps<bf16_s, true>(d.k, a, backward, s) : pick_taps<bf16_s, false>(d.k, a, backward, s);
+  return silu ? pick_taps<float, true>(d.k, a, backward, s) : pick_taps<float, false>(d.k, a, backward, s);
 }
 
 Conv1dArgs base_args(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& c, int seg) {
@@ -362,8 +353,7 @@ int launch_conv1d_forward(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& c
   a.yb = c.y.batch;
   a.yr = c.y.row;
   a.cache_out = c.cache_out;
-  pick_type(p.d, a, false, static_cast<hipStream_t>(stream));
-  return int(hipGetLastError());
+  return pick_type(p.d, a, false, static_cast<hipStream_t>(stream));
 }
 
 int launch_conv1d_backward(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& c, void* stream) {
@@ -378,8 +368,7 @@ int launch_conv1d_backward(const cc3d_conv1d_plan& p, const cc3d_conv1d_args_t& 
   a.dcache_out = c.dcache_out;
   a.part = static_cast<float*>(c.workspace);
   a.rows = p.bwd_rows;
-  pick_type(p.d, a, true, static_cast<hipStream_t>(stream));
-  const int e = int(hipGetLastError());
+  const int e = pick_type(p.d, a, true, static_cast<hipStream_t>(stream));
   if (e) return e;
   const int64_t stride = int64_t(p.d.k + 1) * p.d.c, taps = int64_t(p.d.k) * p.d.c;
   const SumJob jobs[] = {{a.part, c.dw, a.rows, taps, stride}, {a.part + taps, c.db, a.rows, p.d.c, stride}};

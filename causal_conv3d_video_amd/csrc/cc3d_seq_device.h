@@ -9,6 +9,22 @@
 
 namespace {
 
+// One launch; 0, or the runtime's code for this launch.  (The runtime's last
+// error may be another call's: it is neither asked for nor cleared when the
+// launch is taken.)
+template <class T>
+struct SameType {
+  using type = T;
+};
+template <class... P>
+int launch(void (*kernel)(P...), int64_t workgroups, int threads, int lds, hipStream_t s, typename SameType<P>::type... args) {
+  void* at[] = {&args...};
+  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(unsigned(workgroups)),
+                                       dim3(unsigned(threads)), at, size_t(lds), s);
+  if (e != hipSuccess) (void)hipGetLastError();  // leave no error for the caller's next runtime call
+  return int(e);
+}
+
 typedef unsigned u32x4_s __attribute__((ext_vector_type(4)));
 typedef float f32x4_s __attribute__((ext_vector_type(4)));
 

@@ -169,7 +169,7 @@ struct RowStream {
 
 // Calls run<T, LPR, KIND> for a plan's rows.
 template <template <class, int, int> class Run, class T, class... A>
-void pick_join(int c, A&&... args) {
+int pick_join(int c, A&&... args) {
   if (c < 8) return Run<T, 8, kFew>::run(args...);
   const bool even = c % 8 == 0;
   switch (cc3d::join_lanes(c)) {

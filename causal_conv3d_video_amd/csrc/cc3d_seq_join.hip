@@ -86,11 +86,11 @@ __global__ __launch_bounds__(RowSum<LPR>::kThreads) void join_fwd(JoinArgs a) {
 
 template <class T, int LPR, int KIND>
 struct Forward {
-  static void run(const JoinArgs& a, hipStream_t s) {
+  static int run(const JoinArgs& a, hipStream_t s) {
     constexpr int kThreads = RowSum<LPR>::kThreads, kAtOnce = kThreads / LPR;
     // four waves a SIMD, the most its registers allow
-    const unsigned blocks = unsigned(std::min<int64_t>((a.rows + kAtOnce - 1) / kAtOnce, 8192 * 64 / kThreads));
-    join_fwd<T, LPR, KIND><<<blocks, kThreads, 0, s>>>(a);
+    return launch(join_fwd<T, LPR, KIND>, std::min<int64_t>((a.rows + kAtOnce - 1) / kAtOnce, 8192 * 64 / kThreads), kThreads, 0,
+                  s, a);
   }
 };
 
@@ -105,9 +105,7 @@ int launch_join_forward(const cc3d_join_plan& p, const cc3d_join_args_t& c, void
   a.xr = c.x_out.row;
   a.hr = c.h_out.row;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (p.d.dtype == CC3D_BF16) pick_join<Forward, bf16_s>(a.c, a, s);
-  else pick_join<Forward, float>(a.c, a, s);
-  return int(hipGetLastError());
+  return p.d.dtype == CC3D_BF16 ? pick_join<Forward, bf16_s>(a.c, a, s) : pick_join<Forward, float>(a.c, a, s);
 }
 
 }  // namespace cc3d

@@ -233,8 +233,8 @@ __global__ __launch_bounds__(256) void gate_sum(JoinArgs a) {
 
 template <class T, int LPR, int KIND>
 struct Backward {
-  static void run(const JoinArgs& a, int64_t parts, hipStream_t s) {
-    join_bwd<T, LPR, KIND><<<unsigned(parts), RowSum<LPR>::kThreads, 0, s>>>(a);
+  static int run(const JoinArgs& a, int64_t parts, hipStream_t s) {
+    return launch(join_bwd<T, LPR, KIND>, parts, RowSum<LPR>::kThreads, 0, s, a);
   }
 };
 
@@ -256,14 +256,10 @@ int launch_join_backward(const cc3d_join_plan& p, const cc3d_join_args_t& c, voi
   a.dgr = c.dgate.row;
   a.part = static_cast<float*>(c.workspace);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (p.d.dtype == CC3D_BF16) pick_join<Backward, bf16_s>(a.c, a, p.bwd_parts, s);
-  else pick_join<Backward, float>(a.c, a, p.bwd_parts, s);
-  int e = int(hipGetLastError());
+  int e = p.d.dtype == CC3D_BF16 ? pick_join<Backward, bf16_s>(a.c, a, p.bwd_parts, s)
+                                 : pick_join<Backward, float>(a.c, a, p.bwd_parts, s);
   if (!e && a.gate_parts && a.shared_gate && a.dgate) {
-    const unsigned blocks = unsigned(a.gates * ((a.c + 63) / 64));
-    if (p.d.dtype == CC3D_BF16) gate_sum<bf16_s><<<blocks, 256, 0, s>>>(a);
-    else gate_sum<float><<<blocks, 256, 0, s>>>(a);
-    e = int(hipGetLastError());
+    e = launch(p.d.dtype == CC3D_BF16 ? gate_sum<bf16_s> : gate_sum<float>, a.gates * ((a.c + 63) / 64), 256, 0, s, a);
   }
   if (e) return e;
   const int64_t stride = int64_t(a.gate_parts ? 6 : 5) * a.c;

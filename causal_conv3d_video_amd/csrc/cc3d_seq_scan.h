@@ -417,16 +417,13 @@ inline int run_join(const ScanArgs& a, bool back, hipStream_t s) {
   const int waves = a.chunks >= kJoinChunks * kJoinWaves ? kJoinWaves : (a.chunks + kJoinChunks - 1) / kJoinChunks;
   // (below 2^30: the plan holds n * tiles * S / 16 * 64 threads below 2^32)
   const unsigned half = unsigned(int64_t(a.n) * a.s * ((a.groups * a.wide + 63) / 64)), all = back ? 2 * half : half;
-  scan_join<<<std::min(all, kJoinGrid), 64 * waves, 0, s>>>(a, half, all);
-  return int(hipGetLastError());
+  return launch(scan_join, std::min(all, kJoinGrid), 64 * waves, 0, s, a, half, all);
 }
 
 template <class T, int NS, bool BACK>
 int run_carry(const ScanArgs& a, hipStream_t s) {
-  const unsigned blocks = unsigned(int64_t(a.groups) * a.tiles_per_group * a.n * a.chunks);
-  if (a.waves > 1) scan_carry<T, NS, BACK, true><<<blocks, 64 * a.waves, 0, s>>>(a);
-  else scan_carry<T, NS, BACK, false><<<blocks, 64, 0, s>>>(a);
-  return int(hipGetLastError());
+  const int64_t blocks = int64_t(a.groups) * a.tiles_per_group * a.n * a.chunks;
+  return launch(a.waves > 1 ? scan_carry<T, NS, BACK, true> : scan_carry<T, NS, BACK, false>, blocks, 64 * a.waves, 0, s, a);
 }
 
 inline ScanRows view_of(const cc3d_rows_t& v) { return {v.p, v.batch, v.row}; }

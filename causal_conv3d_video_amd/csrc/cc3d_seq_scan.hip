@@ -220,15 +220,12 @@ __global__ __launch_bounds__(256) void scan_step(ScanArgs a, unsigned per_sequen
 template <class T, int LP>
 int run_step(const ScanArgs& a, hipStream_t s) {
   const unsigned per_sequence = unsigned((int64_t(a.groups) * a.wide * LP + 255) / 256);
-  const unsigned blocks = per_sequence * unsigned(a.n);
   bool vec = a.s % 4 == 0;
   for (const void* p : {static_cast<const void*>(a.a), static_cast<const void*>(a.h_in), static_cast<const void*>(a.h_out)})
     vec = vec && reinterpret_cast<uintptr_t>(p) % 16 == 0;
   for (const ScanRows* v : {&a.b, &a.c})
     vec = vec && reinterpret_cast<uintptr_t>(v->p) % (4 * sizeof(T)) == 0 && (a.n == 1 || v->batch % 4 == 0);
-  if (vec) scan_step<T, LP, true><<<blocks, 256, 0, s>>>(a, per_sequence);
-  else scan_step<T, LP, false><<<blocks, 256, 0, s>>>(a, per_sequence);
-  return int(hipGetLastError());
+  return launch(vec ? scan_step<T, LP, true> : scan_step<T, LP, false>, int64_t(per_sequence) * a.n, 256, 0, s, a, per_sequence);
 }
 
 template <class T>
@@ -244,16 +241,13 @@ template <class T, int NS>
 int run_scan(const cc3d_scan_plan& p, ScanArgs& a, hipStream_t s) {
   a.waves = cc3d::scan_fwd_waves(p.d);
   const int64_t tiles = int64_t(a.groups) * a.tiles_per_group;
-  const unsigned blocks = unsigned(tiles * a.n * a.chunks);
   if (a.chunks > 1) {
     int e = run_carry<T, NS, false>(a, s);
     if (e) return e;
     e = run_join(a, false, s);
     if (e) return e;
   }
-  if (a.waves > 1) scan_fwd<T, NS, true><<<blocks, 64 * a.waves, 0, s>>>(a);
-  else scan_fwd<T, NS, false><<<blocks, 64, 0, s>>>(a);
-  return int(hipGetLastError());
+  return launch(a.waves > 1 ? scan_fwd<T, NS, true> : scan_fwd<T, NS, false>, tiles * a.n * a.chunks, 64 * a.waves, 0, s, a);
 }
 
 template <class T>

@@ -606,8 +606,7 @@ int launch_main(const ScanArgs& a, const cc3d::ScanBwdShape& v, hipStream_t s) {
     }
   }
   const int64_t tiles = int64_t(a.groups) * a.tiles_per_group;
-  scan_bwd<T, SG, SUB, MULTI, DUO><<<unsigned(tiles * a.workers), 64 * v.waves * v.wc, lds, s>>>(a, v.wc);
-  return int(hipGetLastError());
+  return launch(scan_bwd<T, SG, SUB, MULTI, DUO>, tiles * a.workers, 64 * v.waves * v.wc, lds, s, a, v.wc);
 }
 
 template <class T, int SG, int SUB, bool MULTI>
@@ -643,8 +642,7 @@ int run_scan_bwd(const cc3d_scan_plan& p, ScanArgs& a, const cc3d_scan_args_t& c
   }
   if (!e && (c.db.p || c.dc.p)) {
     const int64_t values = int64_t(a.n) * a.t * 2 * a.groups * a.s;
-    bc_sum<T><<<unsigned(std::min((values + 255) / 256, kBcGrid)), 256, 0, s>>>(a, view_of(c.db), view_of(c.dc), 4 * v.sg);
-    e = int(hipGetLastError());
+    e = launch(bc_sum<T>, std::min((values + 255) / 256, kBcGrid), 256, 0, s, a, view_of(c.db), view_of(c.dc), 4 * v.sg);
   }
   return e;
 }

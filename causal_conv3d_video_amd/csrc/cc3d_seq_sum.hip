@@ -55,8 +55,7 @@ int launch_sums(const SumJob* jobs, int n, void* stream) {
     blocks += unsigned(sum_workgroups(jobs[i].cols));
   }
   if (!blocks) return 0;
-  sum_rows<<<blocks, kSumThreads, 0, static_cast<hipStream_t>(stream)>>>(a);
-  return int(hipGetLastError());
+  return launch(sum_rows, blocks, kSumThreads, 0, static_cast<hipStream_t>(stream), a);
 }
 
 }  // namespace cc3d
