@@ -52,7 +52,7 @@ inline int conv1d_lanes(int c) {
   return l;
 }
 
-// Channels per wave of the scan, and states per wave of its forward pass.
+// Channels per wave of the scan, and the most states per wave of its forward pass.
 constexpr int kScanLanes = 64;
 constexpr int kScanFwdStates = 16;
 constexpr int kScanMaxStates = 64;
@@ -61,7 +61,7 @@ inline int scan_tiles_per_group(const cc3d_scan_desc_t& d) {
   return (d.d / d.groups - 1) / kScanLanes + 1;
 }
 // States a wave holds, and waves that share one tile of channels.
-inline int scan_fwd_ns(const cc3d_scan_desc_t& d) { return d.states <= 4 ? 4 : d.states <= 8 ? 8 : 16; }
+inline int scan_fwd_ns(const cc3d_scan_desc_t& d) { return d.states <= 4 ? 4 : d.states <= 8 ? 8 : kScanFwdStates; }
 inline int scan_fwd_waves(const cc3d_scan_desc_t& d) { return (d.states + scan_fwd_ns(d) - 1) / scan_fwd_ns(d); }
 // Lanes that hold a channel's states in a call of one token, four each.
 inline int scan_step_lanes(int states) {

@@ -35,7 +35,6 @@ struct ScanArgs {
 struct Place {
   int lane, wave, tile, group, chan;
   int first, live;  // the wave's first channel and how many it has
-  bool on;
   int64_t item;
   __device__ __forceinline__ Place(const ScanArgs& a) {
     lane = threadIdx.x % 64;
@@ -47,7 +46,6 @@ struct Place {
     const int in_group = (tile - group * a.tiles_per_group) * 64 + lane;
     // lanes past the group's last channel compute that one too: what they
     // store is the same value to the same place
-    on = in_group < a.wide;
     chan = group * a.wide + min(in_group, a.wide - 1);
     first = group * a.wide + in_group - lane;
     live = min(a.wide - (in_group - lane), 64);
@@ -423,7 +421,9 @@ inline int run_join(const ScanArgs& a, bool back, hipStream_t s) {
 template <class T, int NS, bool BACK>
 int run_carry(const ScanArgs& a, hipStream_t s) {
   const int64_t blocks = int64_t(a.groups) * a.tiles_per_group * a.n * a.chunks;
-  return launch(a.waves > 1 ? scan_carry<T, NS, BACK, true> : scan_carry<T, NS, BACK, false>, blocks, 64 * a.waves, 0, s, a);
+  if constexpr (NS == cc3d::kScanFwdStates)  // (fewer a wave: all of them in one)
+    if (a.waves > 1) return launch(scan_carry<T, NS, BACK, true>, blocks, 64 * a.waves, 0, s, a);
+  return launch(scan_carry<T, NS, BACK, false>, blocks, 64, 0, s, a);
 }
 
 inline ScanRows view_of(const cc3d_rows_t& v) { return {v.p, v.batch, v.row}; }

@@ -247,7 +247,10 @@ int run_scan(const cc3d_scan_plan& p, ScanArgs& a, hipStream_t s) {
     e = run_join(a, false, s);
     if (e) return e;
   }
-  return launch(a.waves > 1 ? scan_fwd<T, NS, true> : scan_fwd<T, NS, false>, tiles * a.n * a.chunks, 64 * a.waves, 0, s, a);
+  const int64_t blocks = tiles * a.n * a.chunks;
+  if constexpr (NS == cc3d::kScanFwdStates)  // (fewer a wave: all of them in one)
+    if (a.waves > 1) return launch(scan_fwd<T, NS, true>, blocks, 64 * a.waves, 0, s, a);
+  return launch(scan_fwd<T, NS, false>, blocks, 64, 0, s, a);
 }
 
 template <class T>
