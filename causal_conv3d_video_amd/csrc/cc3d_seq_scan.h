@@ -329,28 +329,15 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
 // Turns what every chunk adds into the state that enters it, from the
 // sequence's first state on, and, in the grid's second half where there is one,
 // the gradient that enters it from the right.
-// A chunk's decay is kept as an exponent of two, as it may overflow where its
-// product with the state does not.
+// A chunk's decay is kept as its square root and multiplied twice, as it may
+// overflow where its product with the state does not: a root is held to 2^127,
+// whose square takes every normal number past the largest.
 // A workgroup takes 64 channels of one state; each wave loads 16 chunks at
 // once and joins them, and the waves' joined stretches meet in LDS, so the
 // loads of a long sequence are not one after another.  8.8 us for 128
 // chunks of 2048 channels and 16 states.  A grid of up to kJoinGrid workgroups
 // takes all of them in turns: `all` of up to 1024 threads each may be more
 // threads than a launch holds.
-struct Decay {
-  float part;  // in (0.5, 1]
-  int whole;
-  __device__ __forceinline__ Decay() {}
-  // (past +-2000 it is zero or infinite anyway; a NaN is in the chunk's sum as well)
-  __device__ __forceinline__ explicit Decay(float x) {
-    x = __builtin_amdgcn_fmed3f(x, -2000.f, 2000.f);
-    const float w = ceilf(x);
-    part = __builtin_amdgcn_exp2f(x - w);
-    whole = int(w);
-  }
-  __device__ __forceinline__ float of(float h) const { return __builtin_ldexpf(h * part, whole); }
-};
-
 constexpr int kJoinChunks = 16, kJoinWaves = 16;
 constexpr unsigned kJoinGrid = 1u << 16;
 
@@ -366,7 +353,10 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a, unsigne
     const int tile = int(block - rest * tiles), n = int(rest / a.s), s = int(rest - int64_t(n) * a.s);
     const bool on = tile * 64 + lane < channels;
     const int chan = on ? tile * 64 + lane : channels - 1;
-    const float a2 = rate_of(a.a[int64_t(chan) * a.s + s]);
+    const float half_a2 = 0.5f * rate_of(a.a[int64_t(chan) * a.s + s]);
+    // (a NaN of the sum is in what the chunk adds as well)
+    auto root_of = [&](float sum) { return __builtin_amdgcn_exp2f(fminf(sum * half_a2, 127.f)); };
+    auto join = [](float root, float h, float add) { return fmaf(root * h, root, add); };
     const float* first = rev ? a.dh_out : a.h_in;
     float enter = first ? first[(int64_t(n) * channels + chan) * a.s + s] : 0.f;
     float* carry = (rev ? a.gcarry : a.carry) + (int64_t(n) * a.chunks * a.s + s) * channels + chan;
@@ -374,22 +364,21 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a, unsigne
     const int64_t step = int64_t(a.s) * channels;
     for (int base = 0; base < a.chunks; base += kJoinChunks * waves) {
       const int c0 = base + wave * kJoinChunks;
-      float add[kJoinChunks], sum[kJoinChunks], total = 0.f, h = 0.f;
-      Decay decay[kJoinChunks];
+      float add[kJoinChunks], root[kJoinChunks], total = 0.f, h = 0.f;
 #pragma unroll
       for (int i = 0; i < kJoinChunks; ++i) {
         const int k = min(c0 + i, a.chunks - 1), c = rev ? a.chunks - 1 - k : k;
         add[i] = carry[c * step];
-        sum[i] = sums[int64_t(c) * channels];
+        root[i] = sums[int64_t(c) * channels];
       }
 #pragma unroll
       for (int i = 0; i < kJoinChunks; ++i) {
         const bool in = c0 + i < a.chunks;
         add[i] = in ? add[i] : 0.f;
-        sum[i] = in ? sum[i] : 0.f;
-        total += sum[i];
-        decay[i] = Decay(sum[i] * a2);
-        h = decay[i].of(h) + add[i];
+        root[i] = in ? root[i] : 0.f;
+        total += root[i];
+        root[i] = root_of(root[i]);
+        h = join(root[i], h, add[i]);
       }
       __syncthreads();
       add_of[wave][lane] = h;
@@ -398,13 +387,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a, unsigne
       float mine = enter;
       for (int w = 0; w < waves; ++w) {
         if (w == wave) mine = enter;
-        enter = Decay(sum_of[w][lane] * a2).of(enter) + add_of[w][lane];
+        enter = join(root_of(sum_of[w][lane]), enter, add_of[w][lane]);
       }
 #pragma unroll
       for (int i = 0; i < kJoinChunks; ++i) {
         const int k = c0 + i, c = rev ? a.chunks - 1 - k : k;
         if (k < a.chunks && on) carry[c * step] = mine;
-        mine = decay[i].of(mine) + add[i];
+        mine = join(root[i], mine, add[i]);
       }
     }
   }

@@ -586,7 +586,7 @@ __global__ __launch_bounds__(256) void bc_sum(ScanArgs a, ScanRows db, ScanRows 
     const int group = gs / a.s, s = gs - group * a.s;
     const ScanRows& out = which ? dc : db;
     if (!out.p) continue;
-    const float* p = a.part_bc + int64_t(group) * a.tiles_per_group * tile + tok * token + (s / each * 2 + which) * each + s % each;
+    const float* p = a.part_bc + group * a.tiles_per_group * tile + tok * token + (s / each * 2 + which) * each + s % each;
     float sum = 0.f;
     for (int i = 0; i < a.tiles_per_group; ++i) sum += p[i * tile];
     const int64_t n = tok / a.t, t = tok - n * a.t;
