@@ -28,6 +28,8 @@ int launch(void (*kernel)(P...), int64_t workgroups, int threads, int lds, hipSt
 typedef unsigned u32x4_s __attribute__((ext_vector_type(4)));
 typedef float f32x4_s __attribute__((ext_vector_type(4)));
 
+// The hardware's exponential is of two: exp(v) rounds v * kLog2e besides, which is
+// |v| units of 2^-24 of the result or so.
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 

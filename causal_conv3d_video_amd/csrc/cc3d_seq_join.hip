@@ -88,7 +88,8 @@ template <class T, int LPR, int KIND>
 struct Forward {
   static int run(const JoinArgs& a, hipStream_t s) {
     constexpr int kThreads = RowSum<LPR>::kThreads, kAtOnce = kThreads / LPR;
-    // four waves a SIMD, the most its registers allow
+    // two turns of the four waves a SIMD that its registers allow: one turn is 2 to 3%
+    // slower (921600 rows of 192 bf16 channels 302 us for 296, 400000 of 96 64.8 for 63.0)
     return launch(join_fwd<T, LPR, KIND>, std::min<int64_t>((a.rows + kAtOnce - 1) / kAtOnce, 8192 * 64 / kThreads), kThreads, 0,
                   s, a);
   }

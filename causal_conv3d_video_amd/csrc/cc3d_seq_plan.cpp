@@ -198,7 +198,7 @@ extern "C" cc3d_status_t causal_conv1d_plan(const cc3d_conv1d_desc_t* d, cc3d_co
     return refuse(CC3D_ERR_INVALID_ARG);
   if (d->k > 8 || d->t > kMaxTokens) return refuse(CC3D_ERR_UNSUPPORTED);
   // Tokens per thread: long runs read less of the window twice, short ones
-  // fill the card; 2^18 threads are eight waves on every SIMD and then some.
+  // fill the card; 2^18 threads are four waves on every SIMD.
   const int64_t vecs = ceildiv(d->c, 8);
   int64_t seg = std::max<int64_t>(ceildiv(int64_t(d->n) * d->t, ceildiv(int64_t(1) << 18, vecs)), 1);
   seg = std::min<int64_t>(std::max<int64_t>(seg, 8), 64);
@@ -207,8 +207,9 @@ extern "C" cc3d_status_t causal_conv1d_plan(const cc3d_conv1d_desc_t* d, cc3d_co
   auto* p = make_plan<cc3d_conv1d_plan>(d);
   if (!p) return CC3D_ERR_NO_MEMORY;
   p->seg = int32_t(seg);
-  // Backward: two waves a SIMD (its registers allow no more), so 512 workgroups
-  // are one turn of the card: runs are as long as that turn needs, up to 64
+  // Backward: two waves a SIMD (what registers allow at three to five taps; one
+  // from six on, five in fp32, which makes it two turns), so 512 workgroups are
+  // one turn of the card: runs are as long as that turn needs, up to 64
   // tokens, and a workgroup whose tiles are done takes further runs.  (964
   // workgroups of 17 tokens took 66 us where 500 of 33 take 54.)
   const int64_t lines = 256 / cc3d::conv1d_lanes(d->c), tiles = ceildiv(vecs, cc3d::conv1d_lanes(d->c));
@@ -291,7 +292,10 @@ extern "C" cc3d_status_t selective_scan_plan(const cc3d_scan_desc_t* d, cc3d_sca
     return refuse(CC3D_ERR_UNSUPPORTED);
   // Forward: split the time axis when the channels alone leave SIMDs idle, into
   // four waves a SIMD: 8192 tokens of 2048 channels in 125 us, two a SIMD 142 (a
-  // join 1 us slower among them).
+  // join 1 us slower among them).  From one wave a SIMD on the second walk over the
+  // tokens costs more than what it fills: 64 sequences of 1024 such tokens (two
+  // waves a SIMD) 590 us whole and 881 split; right at the border, 32 of 2048, still
+  // 919 whole and 868 split.
   const int64_t base = nc * tiles * cc3d::scan_fwd_waves(*d);
   int64_t chunk = ceildiv(d->t, 4) * 4;
   if (base < kSimds && d->t > 64) {
@@ -311,6 +315,8 @@ extern "C" cc3d_status_t selective_scan_plan(const cc3d_scan_desc_t* d, cc3d_sca
   const int64_t state = int64_t(d->states) * d->d;
   if (chunks > 1) p->info.workspace_bytes = nc * chunks * (state + d->d) * 4;
   // backward: two waves a SIMD, each workgroup taking every bwd_workers-th chunk
+  // (with 9 to 16 states; the LDS of other counts' workgroups of four waves lets a
+  // compute unit hold one, and half of the workers are a second turn)
   p->bwd_workers = int32_t(std::min<int64_t>(nc * bwd_chunks, ceildiv(2 * kSimds, bwd_tiles * bw.waves * bw.wc)));
   // (groups * states stays below 2^30 with it: what follows them counts in 32 bits)
   p->bwd_fits = cc3d::fits(bwd_tiles * p->bwd_workers, 64 * bw.waves * bw.wc) &&
@@ -417,7 +423,10 @@ extern "C" cc3d_status_t norm_join_plan(const cc3d_join_desc_t* d, cc3d_join_pla
   // Backward: at most two waves a SIMD, each workgroup with a row of partial sums
   // of the five parameter gradients.  Where a gate row serves several rows a
   // workgroup takes whole gate rows, or, where there are few of them, a part of one,
-  // whose partial sums of the gate's gradient follow.
+  // whose partial sums of the gate's gradient follow.  Whole rows from half of the
+  // workgroups on: 100 rows of 768 bf16 channels a gate row in 87 us either way at
+  // 256 gate rows, 112 at 300, 162 at 500; 192 fp32 channels at 260 in 38.5 us, and
+  // 40.7 where only twice as many gate rows are taken whole.
   const int lanes = cc3d::join_lanes(d->c), threads = cc3d::join_threads(lanes);
   const int64_t at_once = threads / lanes;
   const int64_t limit = 2 * kSimds * 64 / threads;

@@ -20,8 +20,9 @@
  * gradients are written as zero, and the carried state is that after the
  * last valid token (the incoming one where there is none).
  *
- * Arithmetic is fp32 whatever the storage type; states are fp32; results are
- * rounded once, to nearest even.  Every sum has a fixed order: repeated calls
+ * Arithmetic is fp32 whatever the storage type (an exponential of v to about
+ * |v| units of 2^-24); states are fp32; results are rounded once, to nearest
+ * even.  Every sum has a fixed order: repeated calls
  * give the same bits.
  *
  * Plans are host metadata (no device call), immutable, usable from any
