@@ -208,7 +208,9 @@ __device__ __forceinline__ void spread_rows(const Feed<T, NS, ROWS>& f, float* b
 // exponential a token and state serve both.  2 x 2049 tokens of 2048 channels, 16
 // states: 63 us, where a walk each way took 43 + 37.  Where decays grow (delta A
 // > 0) that product may overflow beside a gradient that is zero; such a wave
-// walks back over its chunk as the formula does, one token after another.
+// walks back over its chunk as the formula does, one token and state after
+// another (all states at once in registers the compiler kept some for it through
+// the whole walk, which then waited for its loads: 4 us more).
 template <class T, int NS, bool BACK, bool MULTI>
 __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void scan_carry(ScanArgs a) {
   constexpr int kRows = BACK ? 2 : 1;
@@ -293,28 +295,6 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
       }
     }
   }
-  if constexpr (BACK) {
-    bool over = false;  // once infinite, or not a number, it stays so
-#pragma unroll
-    for (int i = 0; i < NS; ++i) over |= !(through[i] <= FLT_MAX);
-    if (__any(over)) {
-#pragma unroll
-      for (int i = 0; i < NS; ++i) g[i] = 0.f;
-      for (int t = te - 1; t >= t0; --t) {
-        auto token = [&](const ScanRows& v) { return rows<T>(v, n) + int64_t(t) * v.row; };
-        const float delta = delta_of(a, to_f32(token(a.dt)[at.chan]) + bias);
-        const T* c = token(a.c) + at.group * a.s + s0;
-        float gy = to_f32(token(a.dy)[at.chan]);
-        if (a.z.p) {
-          const float v = to_f32(token(a.z)[at.chan]);
-          gy *= v * sigmoid_f32(v);
-        }
-#pragma unroll
-        for (int i = 0; i < NS; ++i)
-          if (i < states) g[i] = __builtin_amdgcn_exp2f(delta * a2[i]) * fmaf(gy, to_f32(c[i]), g[i]);
-      }
-    }
-  }
   const int channels = a.groups * a.wide;
   const int64_t out = (at.item * a.s + s0) * channels + at.chan;
 #pragma unroll
@@ -324,6 +304,30 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
       if constexpr (BACK) a.gcarry[out + int64_t(i) * channels] = g[i];
     }
   if (at.wave == 0) a.sums[at.item * channels + at.chan] = total;
+  if constexpr (BACK) {
+    bool over = false;  // once infinite, or not a number, it stays so
+#pragma unroll
+    for (int i = 0; i < NS; ++i) over |= !(through[i] <= FLT_MAX);
+    if (__any(over)) {
+#pragma nounroll
+      for (int i = 0; i < states; ++i) {
+        const float rate = rate_of(a.a[int64_t(at.chan) * a.s + s0 + i]);
+        float back = 0.f;
+#pragma nounroll
+        for (int t = te - 1; t >= t0; --t) {
+          auto token = [&](const ScanRows& v) { return rows<T>(v, n) + int64_t(t) * v.row; };
+          const float delta = delta_of(a, to_f32(token(a.dt)[at.chan]) + bias);
+          float gy = to_f32(token(a.dy)[at.chan]);
+          if (a.z.p) {
+            const float v = to_f32(token(a.z)[at.chan]);
+            gy *= v * sigmoid_f32(v);
+          }
+          back = __builtin_amdgcn_exp2f(delta * rate) * fmaf(gy, to_f32(token(a.c)[at.group * a.s + s0 + i]), back);
+        }
+        a.gcarry[out + int64_t(i) * channels] = back;
+      }
+    }
+  }
 }
 
 // Turns what every chunk adds into the state that enters it, from the
