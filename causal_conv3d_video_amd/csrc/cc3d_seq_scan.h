@@ -207,7 +207,7 @@ __device__ __forceinline__ void spread_rows(const Feed<T, NS, ROWS>& f, float* b
 // taken forward too, with the running product of the same decays: one walk and one
 // exponential a token and state serve both.  2 x 2049 tokens of 2048 channels, 16
 // states: 63 us, where a walk each way took 43 + 37.  Where decays grow (delta A
-// > 0) that product may overflow beside a gradient that is zero; such a wave
+// > 0) that product may overflow beside a gradient that is zero; such a lane
 // walks back over its chunk as the formula does, one token and state after
 // another (all states at once in registers the compiler kept some for it through
 // the whole walk, which then waited for its loads: 4 us more).
@@ -305,12 +305,13 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
     }
   if (at.wave == 0) a.sums[at.item * channels + at.chan] = total;
   if constexpr (BACK) {
-    bool over = false;  // once infinite, or not a number, it stays so
+    unsigned over = 0;  // once infinite, or not a number, a product stays so
 #pragma unroll
-    for (int i = 0; i < NS; ++i) over |= !(through[i] <= FLT_MAX);
-    if (__any(over)) {
+    for (int i = 0; i < NS; ++i) over |= through[i] <= FLT_MAX ? 0 : 1u << i;
+    if (over) {
 #pragma nounroll
       for (int i = 0; i < states; ++i) {
+        if (!(over >> i & 1)) continue;
         const float rate = rate_of(a.a[int64_t(at.chan) * a.s + s0 + i]);
         float back = 0.f;
 #pragma nounroll
@@ -358,8 +359,10 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join(ScanArgs a, unsigne
     const bool on = tile * 64 + lane < channels;
     const int chan = on ? tile * 64 + lane : channels - 1;
     const float half_a2 = 0.5f * rate_of(a.a[int64_t(chan) * a.s + s]);
-    // (a NaN of the sum is in what the chunk adds as well)
-    auto root_of = [&](float sum) { return __builtin_amdgcn_exp2f(fminf(sum * half_a2, 127.f)); };
+    auto root_of = [&](float sum) {
+      const float x = sum * half_a2;
+      return __builtin_amdgcn_exp2f(x > 127.f ? 127.f : x);  // (NaN stays NaN)
+    };
     auto join = [](float root, float h, float add) { return fmaf(root * h, root, add); };
     const float* first = rev ? a.dh_out : a.h_in;
     float enter = first ? first[(int64_t(n) * channels + chan) * a.s + s] : 0.f;

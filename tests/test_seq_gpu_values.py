@@ -169,3 +169,43 @@ def test_states_forgotten_at_once(cuda_device, t, s):
     so.assert_close(h, rh, mh, depth, "h_out")
     for k, v in got.items():
         so.assert_close(v, ref[k], mag[k], 2 * depth + n * t + c, k)
+
+
+# ------------------------------------------------------- masks by the step
+
+@pytest.mark.parametrize("t,s", [(1, 16), (7, 4), (150, 16), (150, 64)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_steps_masked_by_infinity_or_the_lowest_value_leave_the_state(cuda_device, t, s, dtype):
+    """softplus(-inf) = 0: such a token changes no state and has no gradient of its step; so with the type's lowest value."""
+    n, c = 3, 40
+    i = base.scan_inputs(n, t, c, s, 2, dtype, True, "dzbh", 560 + t)
+    names = ("du", "ddt", "da", "db", "dc", "dd", "dz", "ddt_bias", "dh_in")
+    for low in (-INF, float(torch.finfo(dtype).min)):
+        i["dt"][:, t // 3:] = low
+        i["dt"][1] = low
+        y, h, got = _scan(i, n, t, c, s, 2, dtype, True, None, names)
+        ref_in = dict(i, dt=i["dt"].clamp(min=-1e30))  # the same steps of zero, without the oracle's inf - inf
+        ((ry, rh), (my, mh)), (ref, mag) = _scan_bounds(ref_in, None, True)
+        depth = 4 * t + 2 * s + 640
+        so.assert_close(y, ry, my, depth, "y")
+        so.assert_close(h, rh, mh, depth, "h_out")
+        assert torch.equal(h[1].cpu(), i["h_in"][1])
+        for k, v in got.items():
+            so.assert_close(v, ref[k], mag[k], 2 * depth + n * t + c, k)
+
+
+def test_not_a_number_in_a_reaches_its_channel_only(cuda_device):
+    n, t, c, s = 2, 150, 40, 16
+    i = base.scan_inputs(n, t, c, s, 2, F32, True, "dzbh", 570)
+    names = ("du", "ddt", "dz", "dh_in")
+    clean = _scan(i, n, t, c, s, 2, F32, True, None, names)
+    i["a"][7, 3] = base.NAN
+    got = _scan(i, n, t, c, s, 2, F32, True, None, names)
+    keep = torch.arange(c) != 7
+    for k in names:
+        axis = 1 if k == "dh_in" else 2
+        assert torch.equal(got[2][k].cpu().index_select(axis, keep.nonzero()[:, 0]),
+                           clean[2][k].cpu().index_select(axis, keep.nonzero()[:, 0])), k
+    assert torch.equal(got[0].cpu()[..., keep], clean[0].cpu()[..., keep])
+    assert bool(torch.isnan(got[0][..., 7]).all()) and bool(torch.isnan(got[1][:, 7, 3]).all())
+    assert bool(torch.isnan(got[2]["dh_in"][:, 7, 3]).all())
