@@ -339,7 +339,7 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
 // whose square takes every normal number past the largest.
 // A workgroup takes 64 channels of one state; each wave loads 16 chunks at
 // once and joins them, and the waves' joined stretches meet in LDS, so the
-// loads of a long sequence are not one after another.  8.8 us for 128
+// loads of a long sequence are not one after another.  9.5 us for 128
 // chunks of 2048 channels and 16 states.  A grid of up to kJoinGrid workgroups
 // takes all of them in turns: `all` of up to 1024 threads each may be more
 // threads than a launch holds.

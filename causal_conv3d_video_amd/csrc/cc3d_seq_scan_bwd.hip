@@ -22,9 +22,9 @@
 // their dB and dC in LDS, and each workgroup writes one row of partial sums a
 // token, added in the tiles' order by a last small kernel.
 //
-// Measured, bf16, 2 x 2049 tokens of 2048 channels, 16 states: 246 us (in a
-// kernel trace, whose durations add up to more: scan_carry 63, scan_join 10, this
-// kernel 180, bc_sum and sum_rows 5 each).
+// Measured, bf16, 2 x 2049 tokens of 2048 channels, 16 states: 247 us (in a
+// kernel trace, whose durations add up to more: scan_carry 63, scan_join 11, this
+// kernel 180, bc_sum and sum_rows 6 each).
 // 31 vector instructions a channel, token and state bound it: vector units busy
 // 69% at the two waves a SIMD that its 256 registers allow (some still spill).
 // The bytes alone would take 25 us at a large copy's rate.  One channel and eight

@@ -152,7 +152,7 @@ cc3d_status_t causal_conv1d_backward(cc3d_conv1d_plan_t plan, const cc3d_conv1d_
  * time axis adds is found from zero, so large parts that cancel across pieces
  * may overflow too.  Views whose tokens are 2^25
  * elements or more apart are refused as unsupported (but with T = 1), and so
- * are more than 2^31 - 512 channels and 2^30 tokens.
+ * are more than 2^31 - 512 channels, 2^30 tokens and 2^46 elements of u.
  * ------------------------------------------------------------------------ */
 typedef struct cc3d_scan_desc {
   int32_t n, t, d;    /* sequences, tokens, channels; >= 1 */
