@@ -116,10 +116,10 @@ __global__ __launch_bounds__(RowSum<LPR>::kThreads, LPR > 512 ? 4 : 2) void join
       }
       const float rs1 = a.y ? normalise(xn1, a.post, cols, a, sum) : 1.f;
       if (a.dh) {
+        // (a row that is not there stays zero: an infinite gate times it would reach every channel)
+        if (a.y && (kAtOnce == 1 || there)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float n1 = fmaf(xn1[j], p.w1[j], p.b1[j]);
-          if (a.y) x[j] = fmaf(p.scale[j] * ga[j], n1, x[j]);
+          for (int j = 0; j < 8; ++j) x[j] = fmaf(p.scale[j] * ga[j], fmaf(xn1[j], p.w1[j], p.b1[j]), x[j]);
         }
         const float rs2 = normalise(x, a.pre, cols, a, sum);
         float d[8], m = 0.f, md = 0.f;

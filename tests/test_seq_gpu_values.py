@@ -209,3 +209,23 @@ def test_not_a_number_in_a_reaches_its_channel_only(cuda_device):
     assert torch.equal(got[0].cpu()[..., keep], clean[0].cpu()[..., keep])
     assert bool(torch.isnan(got[0][..., 7]).all()) and bool(torch.isnan(got[1][:, 7, 3]).all())
     assert bool(torch.isnan(got[2]["dh_in"][:, 7, 3]).all())
+
+
+# -------------------------------------------- rows that a workgroup does not have
+
+@pytest.mark.parametrize("r,c,gate_rows", [(33, 24, 33), (17, 8, 17), (40003, 24, 1), (700, 515, 7)])
+def test_an_infinite_gate_reaches_its_own_channel_of_the_sums_only(cuda_device, r, c, gate_rows):
+    """An infinite gate makes its rows' norm zero and, at its channel, no number:
+    dpre_w of the other channels and dpre_b are sums of numbers, whatever a
+    workgroup does with the lines of lanes that have no row in its last step."""
+    g = torch.Generator().manual_seed(580 + c)
+    y, res, dh = base.rn(g, r, c), base.rn(g, r, c), base.rn(g, r, c)
+    gate = base.rn(g, -(-r // gate_rows), c)
+    gate[-1, 3] = INF
+    plan = cc3d.norm_join_plan(cc3d.make_join_desc(r, c, post="rms", pre="rms", gate_rows=gate_rows, dtype=F32))
+    dw, db = base.nan(c), base.nan(c)
+    one = torch.ones(c, device=DEV)
+    cc3d.norm_join_backward(plan, base.dev(y), base.dev(res), dh=base.dev(dh), gate=base.dev(gate), pre_w=one, pre_b=one * 0,
+                            dpre_w=dw, dpre_b=db, workspace=base.space(plan, True))
+    keep = torch.arange(c) != 3
+    assert bool(torch.isfinite(dw.cpu()[keep]).all()) and bool(torch.isfinite(db.cpu()).all())
