@@ -147,7 +147,7 @@ __global__ __launch_bounds__(256) void conv1d_fwd(Conv1dArgs a) {
 // partial sums; sum_rows adds those in their order.  Three elements move for
 // the forward pass' two, against some 267 vector instructions for eight bf16
 // channels of a token at K = 4, runs' overlaps included: 2 x 8193 tokens of 2048
-// channels in 54 us and 5 for the sums, vector units busy 51% of the kernel; the
+// channels in 54 us and 5 for the sums, vector units busy 52% of the kernel; the
 // bytes alone would take 42 at a large copy's rate.
 template <class T, int K, bool FEW, bool SILU>
 __global__ __launch_bounds__(256) void conv1d_bwd(Conv1dArgs a, int lanes) {

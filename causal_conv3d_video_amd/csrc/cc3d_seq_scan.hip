@@ -14,9 +14,9 @@
 // finds what each chunk adds to the state and its decay, exp(A sum delta), a
 // small one joins them, and the main pass starts each chunk from its state.
 //
-// Measured, bf16, 16 states: 8192 tokens of 2048 channels in 128 us (in a kernel
-// trace, whose durations add up to more than the pass: 56 for the chunks' sums, 9
-// for the join, 75 for the main pass).  The vector units are busy 82% of the main
+// Measured, bf16, 16 states: 8192 tokens of 2048 channels in 126 us (in a kernel
+// trace, whose durations add up to more than the pass: 54 for the chunks' sums, 9
+// for the join, 73 for the main pass).  The vector units are busy 83% of the main
 // pass, with 123 instructions a channel and token; the bytes alone would take 28
 // at a large copy's 4.74 TB/s.  1560 ragged sequences of up to 17 tokens of 768
 // channels take one pass, 83 us, vector units busy 65%; the nominal bytes, 67.
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(MULTI ? 64 * (cc3d::kScanMaxStates / NS) : 64) void
 // stretch of memory across LP lanes, and its sum over states LP lanes wide.
 // VEC: states and rows of B and C are aligned to four.
 // 256 streams of 768 channels, 16 states: 7.7 us, 3.5 TB/s of states and inputs,
-// vector units busy 16%.  As one more token of scan_fwd the call took 35 us, with
+// vector units busy 17%.  As one more token of scan_fwd the call took 35 us, with
 // this kernel 10 (of which the host is a part).
 template <class T, int LP, bool VEC>
 __global__ __launch_bounds__(256) void scan_step(ScanArgs a, unsigned per_sequence) {

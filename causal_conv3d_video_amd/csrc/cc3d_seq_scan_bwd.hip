@@ -24,7 +24,7 @@
 //
 // Measured, bf16, 2 x 2049 tokens of 2048 channels, 16 states: 247 us (in a
 // kernel trace, whose durations add up to more: scan_carry 63, scan_join 11, this
-// kernel 180, bc_sum and sum_rows 6 each).
+// kernel 178, bc_sum and sum_rows 6 each).
 // 31 vector instructions a channel, token and state bound it: vector units busy
 // 69% at the two waves a SIMD that its 256 registers allow (some still spill).
 // The bytes alone would take 25 us at a large copy's rate.  One channel and eight
