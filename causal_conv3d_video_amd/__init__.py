@@ -378,3 +378,10 @@ from .seq import (  # noqa: E402
     SEQ_EXPORTED_SYMBOLS, causal_conv1d_backward, causal_conv1d_forward, causal_conv1d_plan, make_conv1d_desc,
     make_join_desc, make_scan_desc, norm_join_backward, norm_join_forward, norm_join_plan, selective_scan_backward,
     selective_scan_forward, selective_scan_plan)
+
+# The operators on heads and groups (include/cc3d_heads.h) share the sequence
+# operators' plans and argument checks.
+from .heads import (  # noqa: E402
+    HEADS_EXPORTED_SYMBOLS, group_norm_backward, group_norm_forward, group_norm_plan, linear_attention_backward,
+    linear_attention_forward, linear_attention_plan, make_group_norm_desc, make_linear_attention_desc, make_rotary_desc,
+    rotary_backward, rotary_forward, rotary_plan)

@@ -1,0 +1,157 @@
+// Rotary positions of the heads of q and k.
+//
+//   a' = A (a cos - b sin);  b' = A (a sin + b cos)      by position * f[j] for pair j
+//
+// One read and one write of everything and a few operations an element: bound by
+// memory.  A workgroup takes a few tokens.  The angles of a token are those of all
+// its heads, so they are computed once, in LDS: in turns, position * (f / 2 pi) in
+// 64 bits, of which the whole part is dropped before anything is rounded to 32.
+// Then each thread turns eight channels (with their partners) at a time.
+#include <algorithm>
+
+#include "cc3d_heads_internal.h"
+#include "cc3d_seq_device.h"
+
+namespace {
+
+struct RotaryArgs {
+  const void* in[2];
+  void* out[2];
+  int64_t ib[2], ir[2], ob[2], orow[2];
+  int heads[2];
+  const int *positions, *offsets, *lengths;
+  int64_t all;  // N T
+  int t, d, rot, first, tokens, interleaved;
+  float amplitude, sign;
+  double turns[128];
+};
+
+// Pieces of a head that a thread takes at a time.  WIDE: eight channels that are
+// passed on, eight pairs of the half layout or four of the interleaved one, where
+// all borders are multiples of eight; else a channel that is passed on, or a pair.
+template <class T, bool WIDE>
+__global__ __launch_bounds__(cc3d::kRotaryThreads) void rotary(RotaryArgs a) {
+  extern __shared__ __attribute__((aligned(16))) float2 table[];  // [tokens][rot / 2]
+  const int half = a.rot / 2, tid = threadIdx.x;
+  const int64_t tok0 = int64_t(blockIdx.x) * a.tokens;
+  const int tokens = int(min(int64_t(a.tokens), a.all - tok0));
+  for (int i = tid; i < tokens * half; i += cc3d::kRotaryThreads) {
+    const int x = i / half, j = i - x * half;
+    const int64_t tok = tok0 + x, n = tok / a.t, t = tok - n * a.t;
+    const int64_t pos = a.positions ? int64_t(a.positions[tok]) : (a.offsets ? int64_t(a.offsets[n]) : 0) + t;
+    double turns = double(pos) * a.turns[j];
+    turns -= rint(turns);
+    float s, c;
+    sincospif(float(2.0 * turns), &s, &c);
+    table[i] = float2{c * a.amplitude, s * a.amplitude * a.sign};
+  }
+  __syncthreads();
+  const int turned = WIDE ? (a.interleaved ? a.rot / 8 : a.rot / 16) : half;
+  const int per = turned + (a.d - a.rot) / (WIDE ? 8 : 1);
+  const int each = per * (a.heads[0] + a.heads[1]);
+  const int step_head = cc3d::kRotaryThreads / per, step_piece = cc3d::kRotaryThreads - step_head * per;
+  for (int x = 0; x < tokens; ++x) {
+    const int64_t tok = tok0 + x, n = tok / a.t, t = tok - n * a.t;
+    const bool on = !a.lengths || t < a.lengths[n];
+    const float2* cs = table + x * half;
+    int head = tid / per, piece = tid - head * per;
+    for (int i = tid; i < each; i += cc3d::kRotaryThreads) {
+      const int w = head >= a.heads[0], h = w ? head - a.heads[0] : head;
+      const T* p = static_cast<const T*>(a.in[w]) + n * a.ib[w] + t * a.ir[w] + int64_t(h) * a.d;
+      T* q = static_cast<T*>(a.out[w]) + n * a.ob[w] + t * a.orow[w] + int64_t(h) * a.d;
+      if constexpr (WIDE) {
+        if (piece >= turned) {
+          int c = (piece - turned) * 8;
+          if (c >= a.first) c += a.rot;
+          Raw8<T> v = on ? load8(p + c) : zero8<T>();
+          using Q = typename Quad<T>::type;
+#pragma unroll
+          for (int k = 0; k < int(sizeof(T) / 2); ++k) reinterpret_cast<Q*>(q + c)[k] = v.q[k];
+        } else if (a.interleaved) {
+          const int c = a.first + piece * 8;
+          const Raw8<T> v = on ? load8(p + c) : zero8<T>();
+          float o[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = cs[piece * 4 + k];
+            const float u = get8(v, 2 * k), z = get8(v, 2 * k + 1);
+            o[2 * k] = on ? u * f.x - z * f.y : 0.f;
+            o[2 * k + 1] = on ? u * f.y + z * f.x : 0.f;
+          }
+          store8(q + c, o);
+        } else {
+          const int c = a.first + piece * 8;
+          const Raw8<T> v = on ? load8(p + c) : zero8<T>(), y = on ? load8(p + c + half) : zero8<T>();
+          float o[8], r[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float2 f = cs[piece * 8 + k];
+            const float u = get8(v, k), z = get8(y, k);
+            o[k] = on ? u * f.x - z * f.y : 0.f;
+            r[k] = on ? u * f.y + z * f.x : 0.f;
+          }
+          store8(q + c, o);
+          store8(q + c + half, r);
+        }
+      } else if (piece >= turned) {
+        int c = piece - turned;
+        if (c >= a.first) c += a.rot;
+        q[c] = on ? p[c] : T(0);
+      } else {
+        const int c = a.first + (a.interleaved ? 2 * piece : piece), e = c + (a.interleaved ? 1 : half);
+        const float u = on ? to_f32(p[c]) : 0.f, z = on ? to_f32(p[e]) : 0.f;
+        const float2 f = cs[piece];
+        q[c] = from_f32<T>(on ? u * f.x - z * f.y : 0.f);
+        q[e] = from_f32<T>(on ? u * f.y + z * f.x : 0.f);
+      }
+      head += step_head;
+      piece += step_piece;
+      if (piece >= per) {
+        piece -= per;
+        ++head;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+namespace cc3d {
+
+int launch_rotary(const cc3d_rotary_plan& p, const cc3d_rotary_args_t& c, bool backward, void* stream) {
+  const auto& d = p.d;
+  RotaryArgs a{};
+  const cc3d_rows_t in[2] = {c.q, c.k}, out[2] = {c.q_out, c.k_out};
+  for (int w = 0; w < 2; ++w) {
+    a.in[w] = in[w].p;
+    a.out[w] = out[w].p;
+    a.ib[w] = in[w].batch;
+    a.ir[w] = in[w].row;
+    a.ob[w] = out[w].batch;
+    a.orow[w] = out[w].row;
+  }
+  a.heads[0] = d.q_heads;
+  a.heads[1] = d.k_heads;
+  a.positions = c.positions;
+  a.offsets = c.offsets;
+  a.lengths = c.lengths;
+  a.all = int64_t(d.n) * d.t;
+  a.t = d.t;
+  a.d = d.d;
+  a.rot = d.rot;
+  a.first = d.first;
+  a.tokens = p.tokens;
+  a.interleaved = d.layout == CC3D_ROTARY_INTERLEAVED;
+  a.amplitude = float(d.amplitude);
+  a.sign = backward ? -1.f : 1.f;
+  std::copy(p.turns, p.turns + d.rot / 2, a.turns);
+  const bool wide = d.d % 8 == 0 && d.first % 8 == 0 && d.rot % (a.interleaved ? 8 : 16) == 0;
+  const int64_t workgroups = (a.all + p.tokens - 1) / p.tokens;
+  const int lds = p.tokens * d.rot / 2 * int(sizeof(float2));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  auto go = [&](auto* kernel) { return launch(kernel, workgroups, kRotaryThreads, lds, s, a); };
+  if (d.dtype == CC3D_BF16) return wide ? go(&rotary<bf16_s, true>) : go(&rotary<bf16_s, false>);
+  return wide ? go(&rotary<float, true>) : go(&rotary<float, false>);
+}
+
+}  // namespace cc3d
