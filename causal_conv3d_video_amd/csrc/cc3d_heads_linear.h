@@ -76,11 +76,11 @@ struct LinArgs {
   double* part;  // [N][H][segments][blocks]
 };
 
-// Runs of one type (cc3d_heads_linear_bf16.hip, cc3d_heads_linear_f32.hip):
-// out: with outputs, else what each segment adds to the state; dec: with the
-// decay's derivative.
-int linear_runs_bf16(LinArgs& a, int pad, bool out, bool dec, hipStream_t s);
-int linear_runs_f32(LinArgs& a, int pad, bool out, bool dec, hipStream_t s);
+// Runs of one type and kind of widths (cc3d_heads_linear_*.hip).  out: with
+// outputs, else what each segment adds to the state; dec: with the decay's
+// derivative.
+using LinStart = int(LinArgs& a, int pad, bool out, bool dec, hipStream_t s);
+LinStart linear_bf16_eights, linear_bf16_rest, linear_bf16_less, linear_f32_eights, linear_f32_rest, linear_f32_less;
 
 }  // namespace cc3d
 
@@ -104,6 +104,19 @@ __device__ __forceinline__ float fade(float g2, int d) { return d == 0 ? 1.f : _
 // exp(g d) - 1: a state that fades by a little is moved by it, S + S (exp(g d) - 1), so that
 // the factor's own rounding (up to 2^-25 beside 1) is not taken again at every block.
 __device__ __forceinline__ float fade_m1(float g, int d) { return d == 0 ? 0.f : float(expm1(double(g) * d)); }
+
+// A value that is the same for all lanes, kept in a scalar register: arguments
+// would be read from memory again wherever they are used.
+__device__ __forceinline__ int pin(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float pin(float v) { return __uint_as_float(unsigned(pin(int(__float_as_uint(v))))); }
+__device__ __forceinline__ int64_t pin(int64_t v) {
+  return int64_t(uint64_t(unsigned(pin(int(uint64_t(v) >> 32)))) << 32 | unsigned(pin(int(uint64_t(v)))));
+}
+// (by way of the global address space, which an address made of a number has lost)
+template <class T>
+__device__ __forceinline__ T* pin(T* p) {
+  return (T*)(__attribute__((address_space(1))) T*)(pin(int64_t(reinterpret_cast<intptr_t>(p))));
+}
 
 __device__ __forceinline__ f32x4_s zero4() { return f32x4_s{0.f, 0.f, 0.f, 0.f}; }
 
@@ -218,28 +231,81 @@ struct Mat<float> {
   }
 };
 
-// Eight columns from `col` of a row `width` wide; zeros past it.
-template <class T>
-__device__ __forceinline__ Raw8<T> load_cols(const T* row, int col, int width) {
-  if (col + 8 <= width) return load8(row + col);
-  if (col < width) return load_some(row + col, width - col);
-  return zero8<T>();
-}
+// How the widths C and E divide into eights.
+enum {
+  kEights,  // both are multiples of eight
+  kRest,    // both are eight or more
+  kLess     // one is less than eight
+};
+
+// Eight columns from `col` of rows `width` wide, zeros past it, loaded a block
+// ahead: a load under a condition would be waited for where the branches meet, so
+// every load is made, from the last valid token where there is no further one and
+// from the row's last eight columns (before which the row, if not this part of it,
+// has others) where it would leave the row; it is put right when it is used.
+template <class T, int KIND>
+struct Cols8 {
+  int c, shift;  // where it is loaded, and how many elements too early; 8: all is zero
+  __device__ __forceinline__ Cols8(int col, int width)
+      : c(KIND == kLess ? col : min(col, width - 8)), shift(col >= width ? 8 : KIND == kRest ? col - c : 0) {}
+  __device__ __forceinline__ Raw8<T> load(const T* row, int width) const {
+    if constexpr (KIND == kLess) {
+      Raw8<T> r;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) set8(r, j, row[min(c + j, width - 1)]);
+      return r;
+    } else {
+      return load8(row + c);
+    }
+  }
+  __device__ __forceinline__ Raw8<T> finish(Raw8<T> v, bool on, int width) const {
+    constexpr int kWords = int(sizeof(T)) * 2;
+    unsigned w[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = v.q[i / 4][i % 4];
+    if constexpr (KIND == kRest) {
+      auto down = [&](int words, bool by) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = by ? (i + words < kWords ? w[i + words] : 0u) : w[i];
+      };
+      if constexpr (sizeof(T) == 2) {
+        down(2, shift & 4);
+        down(1, shift & 2);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+          w[i] = shift & 1 ? (w[i] >> 16 | (i + 1 < kWords ? w[i + 1] << 16 : 0u)) : w[i];
+      } else {
+        down(4, shift & 4);
+        down(2, shift & 2);
+        down(1, shift & 1);
+      }
+    }
+    on = on & (shift < 8);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) v.q[i / 4][i % 4] = on ? w[i] : 0u;
+    if constexpr (KIND == kLess) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j >= width) set8(v, j, T(0));
+    }
+    return v;
+  }
+};
 
 // Four columns of a result.
-template <class T>
+template <class T, int KIND>
 __device__ __forceinline__ void store_cols(T* row, int col, int width, f32x4_s v) {
-  if (col + 4 <= width) {
+  if (KIND == kEights ? col < width : col + 4 <= width) {
     if constexpr (sizeof(T) == 2) {
       *reinterpret_cast<u32x2_by2*>(row + col) = u32x2_h{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     } else {
       *reinterpret_cast<u32x4_by4*>(row + col) = __builtin_bit_cast(u32x4_s, v);
     }
-    return;
-  }
+  } else if (KIND != kEights) {
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (col + i < width) row[col + i] = from_f32<T>(v[i]);
+    for (int i = 0; i < 3; ++i)
+      if (col + i < width) row[col + i] = from_f32<T>(v[i]);
+  }
 }
 
 // LDS of a workgroup, in elements of T: rows of k, rows of v, the rows of f v in
@@ -257,8 +323,8 @@ struct LinTiles {
   static constexpr int kBytes = kTotal * int(sizeof(T));
 };
 
-template <class T, int DP, bool OUT, bool DEC>
-__global__ __launch_bounds__(cc3d::kLinThreads) void linear_run(LinArgs a) {
+template <class T, int DP, int KIND, bool OUT, bool DEC>
+__global__ __launch_bounds__(cc3d::kLinThreads, DEC || sizeof(T) == 4 || DP == 256 ? 1 : 2) void linear_run(LinArgs a) {
   using M = Mat<T>;
   using L = LinTiles<T, DP, OUT, DEC>;
   using Frag = typename M::Frag;
@@ -268,54 +334,90 @@ __global__ __launch_bounds__(cc3d::kLinThreads) void linear_run(LinArgs a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ int odd[2];  // a block of v holds an infinity or NaN
   T* lds = reinterpret_cast<T*>(smem);
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, lane16 = lane % 16, quad = lane / 16;
+  const int tid = threadIdx.x, lane = tid % 64, wave = pin(tid / 64), lane16 = lane % 16, quad = lane / 16;
 
   int which = 0;
   while (which + 1 < a.runs && blockIdx.x >= a.run[which + 1].first) ++which;
   const LinRun& r = a.run[which];
   const int starts = OUT ? a.segs : a.segs - 1;
-  int64_t id = blockIdx.x - r.first;
-  const int block = int(id % r.blocks);
-  id /= r.blocks;
-  const int s = int(id % starts);
+  unsigned id = blockIdx.x - r.first;
+  const int blocks = r.blocks, block = int(id % blocks);
+  id /= blocks;
+  const int s = pin(int(id % starts));
   id /= starts;
-  const int h = int(id % a.heads);
-  const int64_t n = id / a.heads, nh = n * a.heads + h;
+  const int h = pin(int(id % a.heads)), n = pin(int(id / a.heads));
+  const int64_t nh = int64_t(n) * a.heads + h;
   const int e0 = block * kCols;
-  const int len = valid_tokens(a.lengths, int(n), a.t);
-  const int begin = s * a.seg, end = min(begin + a.seg, len);
+  const int len = pin(valid_tokens(a.lengths, n, a.t));
+  const int begin = s * a.seg, end = pin(min(begin + a.seg, len));
+  const int c_all = pin(r.c), width = pin(min(kCols, r.e - e0));
+  const int sc = pin(r.sc), se = pin(r.se), rev = pin(r.rev), r_lead = pin(r.lead);
+  const float update = pin(r.update);
 
-  const T* q = static_cast<const T*>(r.q) + n * r.qb + int64_t(h / r.qper) * r.c;
-  const T* k = static_cast<const T*>(r.k) + n * r.kb + int64_t(h / r.kper) * r.c;
-  const T* v = static_cast<const T*>(r.v) + n * r.vb + int64_t(h / r.vper) * r.e + e0;
-  const int width = min(kCols, r.e - e0);
+  const T* q = pin(static_cast<const T*>(r.q) + n * r.qb + int64_t(h / r.qper) * r.c);
+  const T* k = pin(static_cast<const T*>(r.k) + n * r.kb + int64_t(h / r.kper) * r.c);
+  const T* v = pin(static_cast<const T*>(r.v) + n * r.vb + int64_t(h / r.vper) * r.e + e0);
+  const int64_t qr = pin(r.qr), kr = pin(r.kr), vr = pin(r.vr), o_row = pin(r.orow);
+  const int64_t o_at = pin(n * r.ob + int64_t(h) * r.e + e0);
+  char* o_p = pin(static_cast<char*>(r.o));
+  const int o_f32 = pin(r.o_f32);
   // token p of the recurrence
-  auto at = [&](int p) { return int64_t(r.rev ? len - 1 - p : p); };
+  auto at = [&](int p) { return int64_t(rev ? len - 1 - p : p); };
 
   const float g = a.log_decay ? a.log_decay[h] : 0.f, g2 = g * kLog2e;
-  const float whole_m1 = fade_m1(g, kTok);
+  const float whole_m1 = pin(fade_m1(g, kTok));
 
   // ---- the state before the segment, in the products' layout: element i of tile (mt, nt) is
   // c = 16 (wave kMt + mt) + 4 quad + i, e = 16 nt + lane16
   f32x4_s st[kMt][kNt], st2[DEC ? kMt : 1][DEC ? kNt : 1];
+  // f(mt, nt, c, e): the four elements from c on of column e
   auto each_state = [&](auto&& f) {
 #pragma unroll
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt)
+      for (int nt = 0; nt < kNt; ++nt) f(mt, nt, 16 * (wave * kMt + mt) + 4 * quad, 16 * nt + lane16);
+  };
+  // (unconditional loads, for the same reason as those of the rows)
+  auto load_state = [&](const float* p, int c, int e) {
+    f32x4_s v = zero4();
+    if (!p) return v;
+    const bool in = e < width;
+    p += (e0 + min(e, width - 1)) * se;
+    if (KIND == kEights && sc == 1) {
+      v = __builtin_bit_cast(f32x4_s, *reinterpret_cast<const u32x4_by4*>(p + min(c, c_all - 4)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = 16 * (wave * kMt + mt) + 4 * quad + i, e = 16 * nt + lane16;
-          f(mt, nt, i, c < r.c && e < width, c * r.sc + (e0 + e) * r.se);
-        }
+      for (int i = 0; i < 4; ++i) v[i] = (in & (c < c_all)) ? v[i] : 0.f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = p[min(c + i, c_all - 1) * sc];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = (in & (c + i < c_all)) ? v[i] : 0.f;
+    }
+    return v;
+  };
+  auto store_state = [&](float* p, int c, int e, f32x4_s v) {
+    if (!((e < width) & (c < c_all))) return;
+    p += (e0 + e) * se + c * sc;
+    if (KIND == kEights) {
+      if (sc == 1) {
+        *reinterpret_cast<u32x4_by4*>(p) = __builtin_bit_cast(u32x4_s, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i * sc] = v[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < c_all) p[i * sc] = v[i];
+    }
   };
   const int64_t size = int64_t(r.c) * r.e;
   const float* from = nullptr;
   if constexpr (OUT) from = s > 0 ? r.segs + (nh * (a.segs - 1) + s - 1) * size : r.from ? r.from + nh * size : nullptr;
-  each_state([&](int mt, int nt, int i, bool in, int off) { st[mt][nt][i] = from && in ? from[off] : 0.f; });
+  each_state([&](int mt, int nt, int c, int e) { st[mt][nt] = load_state(from, c, e); });
   if constexpr (DEC) {
     const float* from2 = OUT && s > 0 ? a.segs2 + (nh * (a.segs - 1) + s - 1) * size : nullptr;
-    each_state([&](int mt, int nt, int i, bool in, int off) { st2[mt][nt][i] = from2 && in ? from2[off] : 0.f; });
+    each_state([&](int mt, int nt, int c, int e) { st2[mt][nt] = load_state(from2, c, e); });
   }
   // its columns as rows of an operand
   auto put_state = [&] {
@@ -340,38 +442,55 @@ __global__ __launch_bounds__(cc3d::kLinThreads) void linear_run(LinArgs a) {
   const int i_tok = 16 * wave + lane16;
   float near[4][4], lead = 0.f;
   if constexpr (OUT) {
+    const float score = pin(r.score), inter = pin(r.inter);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int d = i_tok - (16 * t + 4 * quad + i);
-        near[t][i] = d >= 0 ? r.score * fade(g2, d) : 0.f;
+        near[t][i] = score * fade(g2, max(d, 0));
       }
-    lead = r.inter * fade(g2, i_tok + r.lead);
+    lead = inter * fade(g2, i_tok + r_lead);
   }
 
   // ---- rows of a block in flight
-  Raw8<T> kn[kVecK], vn[kVecV], qn[OUT ? kSteps : 1];
-  const int kc = tid % (DP / 8) * 8, krow = tid / (DP / 8), vc = tid % (kCols / 8) * 8, vrow = tid / (kCols / 8);
+  Raw8<T> kn[kVecK], vn[kVecV], qn[OUT ? kSteps : 1], xn[DEC && OUT ? kCols / 32 : 1];
+  f32x4_s xe[DEC && OUT ? kNt : 1];
+  const int krow = tid / (DP / 8), vrow = tid / (kCols / 8);
   constexpr int kStepK = 256 / (DP / 8), kStepV = 256 / (kCols / 8);
+  const Cols8<T, KIND> kc(tid % (DP / 8) * 8, c_all), vc(tid % (kCols / 8) * 8, width);
+  const T* x = DEC && OUT ? static_cast<const T*>(a.x) + n * a.xb + int64_t(h / a.xper) * r.e + e0 : nullptr;
   auto fetch = [&](int p0) {
 #pragma unroll
-    for (int x = 0; x < kVecK; ++x) {
-      const int p = p0 + krow + x * kStepK;
-      kn[x] = p < end ? load_cols(k + at(p) * r.kr, kc, r.c) : zero8<T>();
-    }
+    for (int y = 0; y < kVecK; ++y) kn[y] = kc.load(k + at(min(p0 + krow + y * kStepK, end - 1)) * kr, c_all);
 #pragma unroll
-    for (int x = 0; x < kVecV; ++x) {
-      const int p = p0 + vrow + x * kStepV;
-      vn[x] = p < end ? load_cols(v + at(p) * r.vr, vc, width) : zero8<T>();
-    }
+    for (int y = 0; y < kVecV; ++y) vn[y] = vc.load(v + at(min(p0 + vrow + y * kStepV, end - 1)) * vr, width);
     if constexpr (OUT) {
-      const int p = p0 + i_tok;
+      const int64_t i = at(min(p0 + i_tok, end - 1));
 #pragma unroll
-      for (int x = 0; x < kSteps; ++x)
-        qn[x] = p < end ? load_cols(q + at(p) * r.qr, 32 * x + 8 * quad, r.c) : zero8<T>();
+      for (int y = 0; y < kSteps; ++y) qn[y] = Cols8<T, KIND>(32 * y + 8 * quad, c_all).load(q + i * qr, c_all);
+      if constexpr (DEC) {
+        const T* row = x + i * a.xr;
+#pragma unroll
+        for (int y = 0; y < kCols / 32; ++y) xn[y] = Cols8<T, KIND>(32 * y + 8 * quad, width).load(row, width);
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) xe[nt][y] = to_f32(row[min(16 * nt + 4 * quad + y, width - 1)]);
+      }
     }
   };
+  // the factors of f v: all blocks but the last are whole
+  float fv[kVecV];
+  auto factors = [&](int m) {
+#pragma unroll
+    for (int y = 0; y < kVecV; ++y) {
+      const int left = m - 1 - (vrow + y * kStepV);
+      const float f = update * fade(g2, max(left + 1 - r_lead, 0));
+      fv[y] = left >= 0 ? f : 0.f;
+    }
+  };
+  factors(kTok);
   if (begin < end) fetch(begin);
   put_state();
   if (tid < 2) odd[tid] = 0;
@@ -384,32 +503,45 @@ __global__ __launch_bounds__(cc3d::kLinThreads) void linear_run(LinArgs a) {
     const int m = min(kTok, end - p0);
     // ---- stage k, v and f v
 #pragma unroll
-    for (int x = 0; x < kVecK; ++x) M::put8(lds + L::kK + (krow + x * kStepK) * kRowK + kc, kn[x]);
+    for (int y = 0; y < kVecK; ++y) {
+      const int j = krow + y * kStepK;
+      M::put8(lds + L::kK + j * kRowK + tid % (DP / 8) * 8, kc.finish(kn[y], j < m, c_all));
+    }
+    if (m < kTok) factors(m);
     bool bad = false;
 #pragma unroll
-    for (int x = 0; x < kVecV; ++x) {
-      const int j = vrow + x * kStepV, place = j * kRowV + vc;
+    for (int y = 0; y < kVecV; ++y) {
+      const int j = vrow + y * kStepV, place = j * kRowV + tid % (kCols / 8) * 8;
+      const Raw8<T> raw = vc.finish(vn[y], j < m, width);
       float f[8], f2[8];
-      const int left = m - 1 - j;
-      const float w = left >= 0 ? r.update * fade(g2, left + 1 - r.lead) : 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float u = get8(vn[x], i);
-        bad |= !(__builtin_fabsf(u) < __builtin_inff());
-        f[i] = u * w;
-        f2[i] = f[i] * float(left);
+        const float u = get8(raw, i);
+        bad = bad | !(__builtin_fabsf(u) < __builtin_inff());
+        f[i] = u * fv[y];
+        f2[i] = f[i] * float(m - 1 - j);
       }
       T* p = lds + L::kF + place;
       constexpr int kOne = kTok * kRowV;
       M::put8_split(p, p + kOne, f);
       if constexpr (DEC) M::put8_split(p + kOne * M::kParts, p + kOne * (M::kParts + 1), f2);
-      if constexpr (OUT) M::put8(lds + L::kV + place, vn[x]);
+      if constexpr (OUT) M::put8(lds + L::kV + place, raw);
     }
-    Frag qf[OUT ? kSteps : 1];
+    Frag qf[OUT ? kSteps : 1], xf[DEC && OUT ? kCols / 32 : 1];
+    f32x4_s xv[DEC && OUT ? kNt : 1];
     if constexpr (OUT) {
 #pragma unroll
-      for (int x = 0; x < kSteps; ++x) qf[x] = M::of(qn[x]);
+      for (int y = 0; y < kSteps; ++y) qf[y] = M::of(Cols8<T, KIND>(32 * y + 8 * quad, c_all).finish(qn[y], i_tok < m, c_all));
       if (bad) odd[turn] = 1;
+    }
+    if constexpr (DEC && OUT) {
+#pragma unroll
+      for (int y = 0; y < kCols / 32; ++y)
+        xf[y] = M::of(Cols8<T, KIND>(32 * y + 8 * quad, width).finish(xn[y], i_tok < m, width));
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) xv[nt][y] = ((i_tok < m) & (16 * nt + 4 * quad + y < width)) ? xe[nt][y] : 0.f;
     }
     __syncthreads();
     if (p0 + kTok < end) fetch(p0 + kTok);
@@ -418,16 +550,18 @@ __global__ __launch_bounds__(cc3d::kLinThreads) void linear_run(LinArgs a) {
       if (tid == 0) odd[turn ^ 1] = 0;
       if (16 * wave < m) {
         // ---- products q.k, transposed: element i of tile t is j = 16 t + 4 quad + i of the lane's token
-        f32x4_s pr[4];
+        // (waves 0 and 1 need the first two tiles)
+        f32x4_s pr[4] = {zero4(), zero4(), zero4(), zero4()};
+        const T* krows = lds + L::kK + lane16 * kRowK + 8 * quad;
+        auto scores = [&](auto first) {
+          constexpr int t0 = decltype(first)::value;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          pr[t] = zero4();
-          if (t <= wave) {
+          for (int y = 0; y < kSteps; ++y)
 #pragma unroll
-            for (int x = 0; x < kSteps; ++x)
-              pr[t] = M::mma(M::row(lds + L::kK + (16 * t + lane16) * kRowK + 32 * x + 8 * quad), qf[x], pr[t]);
-          }
-        }
+            for (int t = t0; t < t0 + 2; ++t) pr[t] = M::mma(M::row(krows + 16 * t * kRowK + 32 * y), qf[y], pr[t]);
+        };
+        scores(std::integral_constant<int, 0>());
+        if (wave >= 2) scores(std::integral_constant<int, 2>());
         const T* state = lds + L::kS + lane16 * kRowK + 8 * quad;
         if constexpr (!DEC) {
 #pragma unroll
@@ -437,18 +571,20 @@ __global__ __launch_bounds__(cc3d::kLinThreads) void linear_run(LinArgs a) {
           const Frag pf[2] = {M::of(pr[0], pr[1]), M::of(pr[2], pr[3])};
           f32x4_s o[kNt];
 #pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) {
-            o[nt] = zero4();
+          for (int nt = 0; nt < kNt; ++nt) o[nt] = zero4();
 #pragma unroll
-            for (int x = 0; x < kSteps; ++x) o[nt] = M::mma(M::row(state + 16 * nt * kRowK + 32 * x), qf[x], o[nt]);
+          for (int y = 0; y < kSteps; ++y)
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) o[nt] = M::mma(M::row(state + 16 * nt * kRowK + 32 * y), qf[y], o[nt]);
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[nt][i] *= lead;
-          }
           if (!odd[turn]) {
             const T* vt = M::col_at(lds + L::kV, kRowV, lane);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              if (2 * y <= wave) {
+              if (y == 0 || wave >= 2) {
 #pragma unroll
                 for (int nt = 0; nt < kNt; ++nt)
                   o[nt] = M::mma(M::col(vt + 32 * y * kRowV + 16 * nt, kRowV), pf[y], o[nt]);
@@ -473,27 +609,24 @@ __global__ __launch_bounds__(cc3d::kLinThreads) void linear_run(LinArgs a) {
             }
           }
           if (i_tok < m) {
-            const int64_t row = n * r.ob + at(p0 + i_tok) * r.orow + int64_t(h) * r.e + e0;
+            const int64_t row = o_at + at(p0 + i_tok) * o_row;
+            if (o_f32) {
 #pragma unroll
-            for (int nt = 0; nt < kNt; ++nt) {
-              if (r.o_f32) store_cols(static_cast<float*>(r.o) + row, 16 * nt + 4 * quad, width, o[nt]);
-              else store_cols(static_cast<T*>(r.o) + row, 16 * nt + 4 * quad, width, o[nt]);
+              for (int nt = 0; nt < kNt; ++nt)
+                store_cols<float, KIND>(reinterpret_cast<float*>(o_p) + row, 16 * nt + 4 * quad, width, o[nt]);
+            } else {
+#pragma unroll
+              for (int nt = 0; nt < kNt; ++nt)
+                store_cols<T, KIND>(reinterpret_cast<T*>(o_p) + row, 16 * nt + 4 * quad, width, o[nt]);
             }
           }
         } else {
           // ---- the decay's gradient: with x the rows of q, (i - j) f[i-j] (do[i] . v[j]) (x[i] . k[j]) of every pair
           // (here only these columns of x and k), and x[i] . f[i+1] (S2 + (i + 1) S) do[i]
-          const T* xrow = static_cast<const T*>(a.x) + n * a.xb + int64_t(h / a.xper) * r.e + e0;
-          const bool there = i_tok < m;
-          if (there) xrow += at(p0 + i_tok) * a.xr;
-          Frag xf[kCols / 32];
-#pragma unroll
-          for (int x = 0; x < kCols / 32; ++x)
-            xf[x] = M::of(there ? load_cols(xrow, 32 * x + 8 * quad, width) : zero8<T>());
           float sum = 0.f;
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            if (t <= wave) {
+            if (t < 2 || wave >= 2) {
               f32x4_s xk = zero4();
 #pragma unroll
               for (int x = 0; x < kCols / 32; ++x)
@@ -518,8 +651,8 @@ __global__ __launch_bounds__(cc3d::kLinThreads) void linear_run(LinArgs a) {
               }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int e = 16 * nt + 4 * quad + i;
-              if (there && e < width) sum += lead * fmaf(float(i_tok + 1), w[i], u[i]) * to_f32(xrow[e]);
+              const float term = lead * fmaf(float(i_tok + 1), w[i], u[i]) * xv[nt][i];
+              sum += ((i_tok < m) & (16 * nt + 4 * quad + i < width)) ? term : 0.f;
             }
           }
           decay += double(sum);
@@ -575,26 +708,30 @@ __global__ __launch_bounds__(cc3d::kLinThreads) void linear_run(LinArgs a) {
   float* to = nullptr;
   if constexpr (OUT) to = keeps && r.to ? r.to + nh * size : nullptr;
   else to = r.segs + (nh * (a.segs - 1) + s) * size;
-  if (to) each_state([&](int mt, int nt, int i, bool in, int off) { if (in) to[off] = st[mt][nt][i]; });
+  if (to) each_state([&](int mt, int nt, int c, int e) { store_state(to, c, e, st[mt][nt]); });
   if constexpr (DEC && !OUT) {
     float* to2 = a.segs2 + (nh * (a.segs - 1) + s) * size;
-    each_state([&](int mt, int nt, int i, bool in, int off) { if (in) to2[off] = st2[mt][nt][i]; });
+    each_state([&](int mt, int nt, int c, int e) { store_state(to2, c, e, st2[mt][nt]); });
   }
   if constexpr (OUT && !DEC) {
     const int last = min(begin + a.seg, a.t);
     for (int t = max(begin, len) + tid / kCols; t < last; t += cc3d::kLinThreads / kCols) {
       const int e = tid % kCols;
-      const int64_t place = n * r.ob + int64_t(t) * r.orow + int64_t(h) * r.e + e0 + e;
+      const int64_t place = o_at + int64_t(t) * o_row + e;
       if (e < width) {
-        if (r.o_f32) static_cast<float*>(r.o)[place] = 0.f;
-        else static_cast<T*>(r.o)[place] = T(0);
+        if (o_f32) reinterpret_cast<float*>(o_p)[place] = 0.f;
+        else reinterpret_cast<T*>(o_p)[place] = T(0);
       }
     }
   }
   if constexpr (OUT && DEC) {
     if (keeps) {
       const float* dto = a.dto + nh * size;
-      each_state([&](int mt, int nt, int i, bool in, int off) { if (in) decay += double(dto[off]) * double(st2[mt][nt][i]); });
+      each_state([&](int mt, int nt, int c, int e) {
+        const f32x4_s v = load_state(dto, c, e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) decay += ((c + i < c_all) & (e < width)) ? double(v[i]) * double(st2[mt][nt][i]) : 0.0;
+      });
     }
     double* box = reinterpret_cast<double*>(smem);  // (the last barrier above is behind every read of the tiles)
     __syncthreads();
@@ -608,21 +745,21 @@ __global__ __launch_bounds__(cc3d::kLinThreads) void linear_run(LinArgs a) {
   }
 }
 
-template <class T, int DP, bool OUT, bool DEC>
+template <class T, int DP, int KIND, bool OUT, bool DEC>
 int start_run(const LinArgs& a, int64_t workgroups, hipStream_t s) {
   constexpr int lds = LinTiles<T, DP, OUT, DEC>::kBytes;
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear_run<T, DP, OUT, DEC>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear_run<T, DP, KIND, OUT, DEC>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) {
       (void)hipGetLastError();
       return int(e);
     }
   }
-  return launch(linear_run<T, DP, OUT, DEC>, workgroups, cc3d::kLinThreads, lds, s, a);
+  return launch(linear_run<T, DP, KIND, OUT, DEC>, workgroups, cc3d::kLinThreads, lds, s, a);
 }
 
-template <class T>
+template <class T, int KIND>
 int start_runs(LinArgs& a, int pad, bool out, bool dec, hipStream_t s) {
   const int starts = out ? a.segs : a.segs - 1;
   int64_t workgroups = 0;
@@ -634,8 +771,9 @@ int start_runs(LinArgs& a, int pad, bool out, bool dec, hipStream_t s) {
   if (workgroups == 0) return 0;
   auto go = [&](auto d) {
     constexpr int DP = decltype(d)::value;
-    if (out) return dec ? start_run<T, DP, true, true>(a, workgroups, s) : start_run<T, DP, true, false>(a, workgroups, s);
-    return dec ? start_run<T, DP, false, true>(a, workgroups, s) : start_run<T, DP, false, false>(a, workgroups, s);
+    if (out)
+      return dec ? start_run<T, DP, KIND, true, true>(a, workgroups, s) : start_run<T, DP, KIND, true, false>(a, workgroups, s);
+    return dec ? start_run<T, DP, KIND, false, true>(a, workgroups, s) : start_run<T, DP, KIND, false, false>(a, workgroups, s);
   };
   if (pad == 64) return go(std::integral_constant<int, 64>());
   if (pad == 128) return go(std::integral_constant<int, 128>());

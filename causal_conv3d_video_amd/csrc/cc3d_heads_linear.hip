@@ -187,8 +187,12 @@ __global__ __launch_bounds__(256) void linear_decay(const double* part, float* o
 
 constexpr int64_t kGrid = 1 << 16;  // workgroups of the kernels that walk their work in turns
 
-int run(cc3d::LinArgs& a, int dtype, int pad, bool out, bool dec, hipStream_t s) {
-  return dtype == CC3D_BF16 ? cc3d::linear_runs_bf16(a, pad, out, dec, s) : cc3d::linear_runs_f32(a, pad, out, dec, s);
+int run(cc3d::LinArgs& a, const cc3d_linear_desc_t& d, int pad, bool out, bool dec, hipStream_t s) {
+  static cc3d::LinStart* const of[2][3] = {
+      {cc3d::linear_f32_eights, cc3d::linear_f32_rest, cc3d::linear_f32_less},
+      {cc3d::linear_bf16_eights, cc3d::linear_bf16_rest, cc3d::linear_bf16_less}};
+  const int kind = std::min(d.dk, d.dv) < 8 ? kLess : d.dk % 8 || d.dv % 8 ? kRest : kEights;
+  return of[d.dtype == CC3D_BF16][kind](a, pad, out, dec, s);
 }
 
 cc3d::LinArgs common(const cc3d_linear_plan& p, const cc3d_linear_args_t& c, int seg, int segs) {
@@ -248,13 +252,13 @@ int launch_linear_forward(const cc3d_linear_plan& p, const cc3d_linear_args_t& c
                     0, d.scale, d.scale, 1.f, c.h_in, c.h_out, static_cast<float*>(c.workspace), 0};
   const int pad = linear_pad(d.dk);
   if (a.segs > 1) {
-    int e = run(a, d.dtype, pad, false, false, s);
+    int e = run(a, d, pad, false, false, s);
     if (e) return e;
     JoinArgs j = join_of(a, int64_t(d.dk) * d.dv);
     j.way[0] = {c.h_in, a.run[0].segs, nullptr};
     if ((e = start_join(j, 1, s))) return e;
   }
-  return run(a, d.dtype, pad, true, false, s);
+  return run(a, d, pad, true, false, s);
 }
 
 int launch_linear_backward(const cc3d_linear_plan& p, const cc3d_linear_args_t& c, void* stream) {
@@ -305,13 +309,13 @@ int launch_linear_backward(const cc3d_linear_plan& p, const cc3d_linear_args_t& 
     if (dec || c.dq.p) {
       a.runs = 1;
       a.run[0] = rq;
-      if ((e = run(a, d.dtype, pad, false, dec, s))) return e;
+      if ((e = run(a, d, pad, false, dec, s))) return e;
       j.way[ways++] = {c.h_in, states, dec ? states2 : nullptr};
     }
     if (back) {
       a.runs = 1;
       a.run[0] = rv;
-      if ((e = run(a, d.dtype, pad, false, false, s))) return e;
+      if ((e = run(a, d, pad, false, false, s))) return e;
       j.way[ways++] = {c.dh_out, grads, nullptr};
     }
     if (ways && (e = start_join(j, ways, s))) return e;
@@ -319,7 +323,7 @@ int launch_linear_backward(const cc3d_linear_plan& p, const cc3d_linear_args_t& 
   if (dec) {
     a.runs = 1;
     a.run[0] = rq;
-    if ((e = run(a, d.dtype, pad, true, true, s))) return e;
+    if ((e = run(a, d, pad, true, true, s))) return e;
     e = launch(linear_decay, d.heads, 256, 0, s, decay, c.dlog_decay, d.n, d.heads, a.segs * a.run[0].blocks);
     if (e) return e;
   }
@@ -327,7 +331,7 @@ int launch_linear_backward(const cc3d_linear_plan& p, const cc3d_linear_args_t& 
   if (c.dq.p) a.run[a.runs++] = rq;
   if (c.dk.p) a.run[a.runs++] = rk;
   if (c.dv.p || c.dh_in) a.run[a.runs++] = rv;
-  if (a.runs && (e = run(a, d.dtype, pad, true, false, s))) return e;
+  if (a.runs && (e = run(a, d, pad, true, false, s))) return e;
   HeadSums sums{};
   int jobs = 0;
   int64_t most = 0;
