@@ -34,6 +34,7 @@ namespace cc3d {
 
 constexpr int kLinTokens = 64;   // tokens taken at a time
 constexpr int kLinThreads = 256;
+constexpr int kLinShort = 32;    // forward calls of up to so many tokens take them one after another
 
 // Widths as the kernels pad them, and how many columns of a state a workgroup
 // holds: its tiles, in fp32 with the decay's gradient, fill 160 KB at 256.

@@ -58,12 +58,12 @@ struct LinRun {
   const float* from;                         // state before the first token, or null
   float* to;                                 // after the last valid one, or null
   float* segs;                               // [N][H][segments - 1]: states before segments 1, 2, ...
-  unsigned first;                            // its first workgroup
 };
 
 struct LinArgs {
   LinRun run[3];
-  int runs;
+  int runs, parts;   // parts: workgroups of all runs that share a head and segment
+  unsigned units;    // heads of all sequences times segments
   int n, heads, t, seg, segs;
   const float* log_decay;
   const int* lengths;
@@ -336,16 +336,21 @@ __global__ __launch_bounds__(cc3d::kLinThreads, DEC || sizeof(T) == 4 || DP == 2
   T* lds = reinterpret_cast<T*>(smem);
   const int tid = threadIdx.x, lane = tid % 64, wave = pin(tid / 64), lane16 = lane % 16, quad = lane / 16;
 
-  int which = 0;
-  while (which + 1 < a.runs && blockIdx.x >= a.run[which + 1].first) ++which;
-  const LinRun& r = a.run[which];
+  // Workgroups go to the eight dies in turn, each with a cache of its own: those
+  // of one head and segment (its columns, its recurrences), which read the same
+  // rows, follow each other on one die.
   const int starts = OUT ? a.segs : a.segs - 1;
-  unsigned id = blockIdx.x - r.first;
-  const int blocks = r.blocks, block = int(id % blocks);
-  id /= blocks;
-  const int s = pin(int(id % starts));
-  id /= starts;
-  const int h = pin(int(id % a.heads)), n = pin(int(id / a.heads));
+  unsigned id = blockIdx.x / 8, unit = id / a.parts * 8 + blockIdx.x % 8;
+  int block = int(id % a.parts), which = 0;
+  while (which + 1 < a.runs && block >= a.run[which].blocks) block -= a.run[which++].blocks;
+  if (unit >= a.units) return;
+  const LinRun& r = a.run[which];
+  const int blocks = r.blocks;
+  const int turned = int(unit % starts);
+  unit /= starts;
+  const int h = pin(int(unit % a.heads)), n = pin(int(unit / a.heads));
+  // (a reversed recurrence of the same rows is at the other end of its segments)
+  const int s = pin(OUT && r.rev ? starts - 1 - turned : turned);
   const int64_t nh = int64_t(n) * a.heads + h;
   const int e0 = block * kCols;
   const int len = pin(valid_tokens(a.lengths, n, a.t));
@@ -741,7 +746,7 @@ __global__ __launch_bounds__(cc3d::kLinThreads, DEC || sizeof(T) == 4 || DP == 2
       if (tid < half) box[tid] += box[tid + half];
       __syncthreads();
     }
-    if (tid == 0) a.part[(nh * a.segs + s) * r.blocks + block] = box[0];
+    if (tid == 0) a.part[(nh * a.segs + s) * blocks + block] = box[0];
   }
 }
 
@@ -762,13 +767,11 @@ int start_run(const LinArgs& a, int64_t workgroups, hipStream_t s) {
 template <class T, int KIND>
 int start_runs(LinArgs& a, int pad, bool out, bool dec, hipStream_t s) {
   const int starts = out ? a.segs : a.segs - 1;
-  int64_t workgroups = 0;
-  for (int i = 0; i < a.runs; ++i) {
-    a.run[i].blocks = int(cc3d::linear_blocks(a.run[i].e, pad));
-    a.run[i].first = unsigned(workgroups);
-    workgroups += int64_t(a.n) * a.heads * starts * a.run[i].blocks;
-  }
-  if (workgroups == 0) return 0;
+  a.parts = 0;
+  for (int i = 0; i < a.runs; ++i) a.parts += a.run[i].blocks = int(cc3d::linear_blocks(a.run[i].e, pad));
+  a.units = unsigned(int64_t(a.n) * a.heads * starts);
+  if (a.units == 0) return 0;
+  const int64_t workgroups = (int64_t(a.units) + 7) / 8 * 8 * a.parts;
   auto go = [&](auto d) {
     constexpr int DP = decltype(d)::value;
     if (out)

@@ -6,93 +6,168 @@
 
 namespace {
 
-struct StepArgs {
+struct ShortArgs {
   const void *q, *k, *v;
   void* o;
-  int64_t qb, kb, vb, ob;
+  int64_t qb, kb, vb, ob, qr, kr, vr, orow;
   int qper, kper, vper;
-  int heads, dk, dv, lanes;  // lanes side by side along Dv, four columns each, a power of two
+  int heads, t, dk, dv, blocks;
   float scale;
   const float *log_decay, *h_in;
   float* h_out;
   const int* lengths;
 };
 
-// One token: S = f S + k^T v, o = scale q S, in fp32.  Reads and writes each
-// state once and does little besides: bound by memory.  A workgroup has one
-// head; its threads are rows of `lanes` lanes with four columns of the state
-// each, eight rows in flight before any is used; q S is summed over a thread's
-// rows, across the lanes of a wave and across the waves.
-template <class T>
-__global__ __launch_bounds__(256) void linear_step(StepArgs a) {
-  __shared__ float box[4][256];
-  const int tid = threadIdx.x, line = tid / a.lanes, lines = 256 / a.lanes, e = tid % a.lanes * 4;
-  const int64_t nh = blockIdx.x, n = nh / a.heads;
-  const int h = int(nh - n * a.heads), width = a.dv - e;
-  const bool on = valid_tokens(a.lengths, int(n), 1) > 0;
+// v added over the four groups of 16 lanes of a wave, in all of them.
+__device__ __forceinline__ float group_quads(float v) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// One value of two of a pair's, added to the other half of the pair's lanes: x
+// of the lower half of 64 (or of each 32) lanes, y of the upper.
+__device__ __forceinline__ float fold32(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float fold16(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Few tokens: the recurrence itself, S = f S + k^T v, o = scale q S, in fp32.
+// Reads and writes each state once and does little besides: bound by memory.  A
+// workgroup has 64 columns of a head's state, four a lane, 16 lines of R rows in
+// registers.  The rows of TOK tokens at a time pass through LDS, the next ones in
+// flight; q S of a token is summed over a thread's rows, and for all TOK together
+// across the lanes of a wave (each step adds two tokens' values at once, so half
+// remain) and, through LDS, across the waves.
+template <class T, int R, int TOK>
+__global__ __launch_bounds__(256) void linear_short(ShortArgs a) {
+  constexpr int kRows = 16 * R, kLoads = (2 * kRows + 64) * TOK / 256 + 1;
+  __shared__ float tile[TOK * (2 * kRows + 64)];  // [TOK][rows of q, of k, columns of v]
+  __shared__ float sums[4][TOK][64];
+  const int tid = threadIdx.x, line = tid / 16, e = tid % 16 * 4;
+  const unsigned nhb = blockIdx.x, nh = nhb / a.blocks, n = nh / a.heads;
+  const int h = int(nh - n * a.heads), e0 = int(nhb - nh * a.blocks) * 64, width = min(64, a.dv - e0);
+  const int len = valid_tokens(a.lengths, int(n), a.t);
   const T* q = static_cast<const T*>(a.q) + n * a.qb + int64_t(h / a.qper) * a.dk;
   const T* k = static_cast<const T*>(a.k) + n * a.kb + int64_t(h / a.kper) * a.dk;
-  const T* v = static_cast<const T*>(a.v) + n * a.vb + int64_t(h / a.vper) * a.dv;
-  const int64_t base = nh * a.dk * a.dv + e;
+  const T* v = static_cast<const T*>(a.v) + n * a.vb + int64_t(h / a.vper) * a.dv + e0;
+  T* o = static_cast<T*>(a.o) + n * a.ob + int64_t(h) * a.dv + e0;
+  const int64_t state = (int64_t(nh) * a.dk) * a.dv + e0 + e;
   const float f = a.log_decay ? __builtin_amdgcn_exp2f(a.log_decay[h] * kLog2e) : 1.f;
-  float vv[4], o[4] = {0.f, 0.f, 0.f, 0.f};
+
+  // (every load is made, where there is nothing to load from a place inside, and put right when it is used)
+  T next[kLoads];
+  auto fetch = [&](int t0) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) vv[i] = on && i < width ? to_f32(v[e + i]) : 0.f;
-  constexpr int kAhead = 8;
-  for (int c0 = line; c0 < a.dk; c0 += lines * kAhead) {
-    f32x4_s s[kAhead];
-    float kk[kAhead], qq[kAhead];
+    for (int x = 0; x < kLoads; ++x) {
+      const int i = tid + 256 * x, tok = min(i / (2 * kRows + 64), TOK - 1), at = i - i / (2 * kRows + 64) * (2 * kRows + 64);
+      const int64_t t = min(t0 + tok, max(len - 1, 0));
+      const T* p = at < kRows ? q + t * a.qr + min(at, a.dk - 1)
+                   : at < 2 * kRows ? k + t * a.kr + min(at - kRows, a.dk - 1) : v + t * a.vr + min(at - 2 * kRows, width - 1);
+      next[x] = *p;
+    }
+  };
+  if (len > 0) fetch(0);
+  f32x4_s s[R];
 #pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      const int c = c0 + x * lines;
-      s[x] = zero4();
-      kk[x] = qq[x] = 0.f;
-      if (c < a.dk && width > 0) {
-        if (on) {
-          kk[x] = to_f32(k[c]);
-          qq[x] = to_f32(q[c]);
-        }
-        if (a.h_in) {
-          const float* p = a.h_in + base + int64_t(c) * a.dv;
-          if (width >= 4) s[x] = __builtin_bit_cast(f32x4_s, *reinterpret_cast<const u32x4_by4*>(p));
-          else
+  for (int r = 0; r < R; ++r) {
+    const int c = line * R + r;
+    s[r] = zero4();
+    if (a.h_in && (c < a.dk) & (e < width)) {
+      const float* p = a.h_in + state + int64_t(c) * a.dv;
+      if (e + 4 <= width) s[r] = __builtin_bit_cast(f32x4_s, *reinterpret_cast<const u32x4_by4*>(p));
+      else
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-              if (i < width) s[x][i] = p[i];
+        for (int i = 0; i < 3; ++i)
+          if (e + i < width) s[r][i] = p[i];
+    }
+  }
+  for (int t0 = 0; t0 < len; t0 += TOK) {
+    const int m = min(TOK, len - t0);
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) {
+      const int i = tid + 256 * x, tok = i / (2 * kRows + 64), at = i - tok * (2 * kRows + 64);
+      const bool in = (tok < m) & (at < kRows ? at < a.dk : at < 2 * kRows ? at - kRows < a.dk : at - 2 * kRows < width);
+      if (i < TOK * (2 * kRows + 64)) tile[i] = in ? to_f32(next[x]) : 0.f;
+    }
+    __syncthreads();
+    if (t0 + TOK < len) fetch(t0 + TOK);
+    f32x4_s part[TOK];
+#pragma unroll
+    for (int tok = 0; tok < TOK; ++tok) {
+      part[tok] = zero4();
+      if (tok < m) {
+        const float* row = tile + tok * (2 * kRows + 64);
+        const f32x4_s vv = *reinterpret_cast<const f32x4_s*>(row + 2 * kRows + e);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float qq = row[line * R + r], kk = row[kRows + line * R + r];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[r][i] = fmaf(f, s[r][i], kk * vv[i]);
+            part[tok][i] = fmaf(qq, s[r][i], part[tok][i]);
+          }
         }
       }
     }
+    const int wave = tid / 64, quad = tid % 64 / 16;
+    if constexpr (TOK == 1) {
 #pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      const int c = c0 + x * lines;
-      if (c >= a.dk || width <= 0) continue;
+      for (int i = 0; i < 4; ++i) part[0][i] = group_quads(part[0][i]);
+      if (quad == 0) *reinterpret_cast<f32x4_s*>(&sums[wave][0][e]) = part[0];
+    } else {
+      // token x + TOK / 2 half in the upper lanes, then x + TOK / 4
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (on) s[x][i] = fmaf(f, s[x][i], kk[x] * vv[i]);
-        o[i] = on ? fmaf(qq[x], s[x][i], o[i]) : 0.f;
+      for (int x = 0; x < TOK / 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[x][i] = fold32(part[x][i], part[x + TOK / 2][i]);
+#pragma unroll
+      for (int x = 0; x < TOK / 4; ++x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[x][i] = fold16(part[x][i], part[x + TOK / 4][i]);
+        *reinterpret_cast<f32x4_s*>(&sums[wave][quad / 2 * (TOK / 2) + quad % 2 * (TOK / 4) + x][e]) = part[x];
       }
-      if (a.h_out) {
-        float* p = a.h_out + base + int64_t(c) * a.dv;
-        if (width >= 4) *reinterpret_cast<u32x4_by4*>(p) = __builtin_bit_cast(u32x4_s, s[x]);
-        else
+    }
+    __syncthreads();
 #pragma unroll
-          for (int i = 0; i < 3; ++i)
-            if (i < width) p[i] = s[x][i];
+    for (int x = 0; x < (TOK * 64 + 255) / 256; ++x) {
+      const int i = tid + 256 * x, tok = i / 64, col = i % 64;
+      if ((tok < m) & (col < width)) {
+        const float sum = (sums[0][tok][col] + sums[1][tok][col]) + (sums[2][tok][col] + sums[3][tok][col]);
+        o[(t0 + tok) * a.orow + col] = from_f32<T>(sum * a.scale);
       }
     }
   }
-  for (int d = a.lanes; d < 64; d *= 2)
+  for (int i = len * 64 + tid; i < a.t * 64; i += 256)
+    if (i % 64 < width) o[i / 64 * a.orow + i % 64] = T(0);
+  if (!a.h_out) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] += __shfl_xor(o[i], d);
-  if (tid % 64 < a.lanes) {
+  for (int r = 0; r < R; ++r) {
+    const int c = line * R + r;
+    if (!((c < a.dk) & (e < width))) continue;
+    float* p = a.h_out + state + int64_t(c) * a.dv;
+    if (e + 4 <= width) *reinterpret_cast<u32x4_by4*>(p) = __builtin_bit_cast(u32x4_s, s[r]);
+    else
 #pragma unroll
-    for (int i = 0; i < 4; ++i) box[tid / 64][e + i] = o[i];
+      for (int i = 0; i < 3; ++i)
+        if (e + i < width) p[i] = s[r][i];
   }
-  __syncthreads();
-  if (tid < a.dv) {
-    const float sum = (box[0][tid] + box[1][tid]) + (box[2][tid] + box[3][tid]);
-    static_cast<T*>(a.o)[n * a.ob + int64_t(h) * a.dv + tid] = from_f32<T>(sum * a.scale);
-  }
+}
+
+template <class T>
+int start_short(const ShortArgs& a, int64_t workgroups, hipStream_t s) {
+  auto go = [&](auto tok) {
+    constexpr int TOK = decltype(tok)::value;
+    if (a.dk <= 64) return launch(linear_short<T, 4, TOK>, workgroups, 256, 0, s, a);
+    if (a.dk <= 128) return launch(linear_short<T, 8, TOK>, workgroups, 256, 0, s, a);
+    return launch(linear_short<T, 16, TOK>, workgroups, 256, 0, s, a);
+  };
+  return a.t == 1 ? go(std::integral_constant<int, 1>()) : go(std::integral_constant<int, 8>());
 }
 
 struct JoinArgs {
@@ -236,20 +311,18 @@ namespace cc3d {
 int launch_linear_forward(const cc3d_linear_plan& p, const cc3d_linear_args_t& c, void* stream) {
   const auto& d = p.d;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (d.t == 1) {
-    StepArgs a{c.q.p, c.k.p, c.v.p, c.o.p, c.q.batch, c.k.batch, c.v.batch, c.o.batch, d.heads / d.q_heads,
-               d.heads / d.k_heads, d.heads / d.v_heads, d.heads, d.dk, d.dv, 1, d.scale, c.log_decay, c.h_in, c.h_out,
-               c.lengths};
-    while (a.lanes * 4 < d.dv) a.lanes *= 2;
-    const int64_t workgroups = int64_t(d.n) * d.heads;
-    return d.dtype == CC3D_BF16 ? launch(linear_step<bf16_s>, workgroups, 256, 0, s, a)
-                                : launch(linear_step<float>, workgroups, 256, 0, s, a);
+  if (d.t <= kLinShort) {
+    const ShortArgs a{c.q.p, c.k.p, c.v.p, c.o.p, c.q.batch, c.k.batch, c.v.batch, c.o.batch, c.q.row, c.k.row, c.v.row,
+                      c.o.row, d.heads / d.q_heads, d.heads / d.k_heads, d.heads / d.v_heads, d.heads, d.t, d.dk, d.dv,
+                      int((d.dv + 63) / 64), d.scale, c.log_decay, c.h_in, c.h_out, c.lengths};
+    const int64_t workgroups = int64_t(d.n) * d.heads * a.blocks;
+    return d.dtype == CC3D_BF16 ? start_short<bf16_s>(a, workgroups, s) : start_short<float>(a, workgroups, s);
   }
   LinArgs a = common(p, c, p.seg, p.segs);
   a.runs = 1;
   a.run[0] = LinRun{c.q.p, c.k.p, c.v.p, c.o.p, c.q.batch, c.q.row, c.k.batch, c.k.row, c.v.batch, c.v.row, c.o.batch,
                     c.o.row, d.heads / d.q_heads, d.heads / d.k_heads, d.heads / d.v_heads, d.dk, d.dv, d.dv, 1, 0, 0, 1,
-                    0, d.scale, d.scale, 1.f, c.h_in, c.h_out, static_cast<float*>(c.workspace), 0};
+                    0, d.scale, d.scale, 1.f, c.h_in, c.h_out, static_cast<float*>(c.workspace)};
   const int pad = linear_pad(d.dk);
   if (a.segs > 1) {
     int e = run(a, d, pad, false, false, s);
@@ -286,13 +359,13 @@ int launch_linear_backward(const cc3d_linear_plan& p, const cc3d_linear_args_t& 
   // dq: the recurrence of (do, v, k) over the transposed state; dk and dv: of (v, do, q) and (k, q, do), reversed
   const LinRun rq = out(LinRun{c.grad_o.p, c.v.p, c.k.p, nullptr, c.grad_o.batch, c.grad_o.row, c.v.batch, c.v.row,
                                c.k.batch, c.k.row, 0, 0, 1, vper, kper, d.dv, d.dk, 1, d.dv, 0, 0, 1, 0, d.scale, d.scale,
-                               1.f, c.h_in, nullptr, states, 0}, c.dq, qper, part_q);
+                               1.f, c.h_in, nullptr, states}, c.dq, qper, part_q);
   const LinRun rk = out(LinRun{c.v.p, c.grad_o.p, c.q.p, nullptr, c.v.batch, c.v.row, c.grad_o.batch, c.grad_o.row,
                                c.q.batch, c.q.row, 0, 0, vper, 1, qper, d.dv, d.dk, 1, d.dv, 0, 1, 0, 0, d.scale, 1.f,
-                               d.scale, c.dh_out, nullptr, grads, 0}, c.dk, kper, part_k);
+                               d.scale, c.dh_out, nullptr, grads}, c.dk, kper, part_k);
   const LinRun rv = out(LinRun{c.k.p, c.q.p, c.grad_o.p, nullptr, c.k.batch, c.k.row, c.q.batch, c.q.row, c.grad_o.batch,
                                c.grad_o.row, 0, 0, kper, qper, 1, d.dk, d.dv, d.dv, 1, 0, 1, 0, 0, d.scale, 1.f, d.scale,
-                               c.dh_out, c.dh_in, grads, 0}, c.dv, vper, part_v);
+                               c.dh_out, c.dh_in, grads}, c.dv, vper, part_v);
   LinArgs a = common(p, c, p.bwd_seg, p.bwd_segs);
   a.segs2 = states2;
   a.x = c.q.p;

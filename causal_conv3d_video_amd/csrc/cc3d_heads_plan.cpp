@@ -51,15 +51,17 @@ extern "C" cc3d_status_t linear_attention_plan(const cc3d_linear_desc_t* d, cc3d
   if (!within_span({d->n, d->t, d->heads, widest}) || !within_span({d->n, d->heads, d->dk, d->dv}))
     return refuse(CC3D_ERR_UNSUPPORTED);
   const int64_t nh = int64_t(d->n) * d->heads;
-  const int64_t units = nh * cc3d::linear_blocks(d->dv, cc3d::linear_pad(d->dk));
-  if (!cc3d::fits(d->t == 1 ? nh : units, cc3d::kLinThreads)) return refuse(CC3D_ERR_UNSUPPORTED);
+  const int64_t blocks = cc3d::linear_blocks(d->dv, cc3d::linear_pad(d->dk)), units = nh * blocks;
+  // (heads are rounded up to eight, one for each die)
+  if (!cc3d::fits(units + 7 * blocks, cc3d::kLinThreads)) return refuse(CC3D_ERR_UNSUPPORTED);
   auto* p = make_plan<cc3d_linear_plan>(d);
   if (!p) return CC3D_ERR_NO_MEMORY;
-  split_time(d->t, units, 2 * kUnits, &p->seg, &p->segs);
+  if (d->t > cc3d::kLinShort) split_time(d->t, units, 2 * kUnits, &p->seg, &p->segs);
   const int pad = cc3d::linear_pad(int(widest));
-  const int64_t bwd_units = nh * (2 * cc3d::linear_blocks(d->dk, pad) + cc3d::linear_blocks(d->dv, pad));
-  split_time(d->t, bwd_units, 2 * kUnits, &p->bwd_seg, &p->bwd_segs);
-  p->bwd_fits = cc3d::fits(bwd_units, cc3d::kLinThreads);  // (where it is split it is far below)
+  // Backward: the recurrence with the fewest workgroups (the decay's is one by itself) once over the compute units.
+  const int64_t of_k = cc3d::linear_blocks(d->dk, pad), of_v = cc3d::linear_blocks(d->dv, pad);
+  split_time(d->t, nh * of_k, kUnits, &p->bwd_seg, &p->bwd_segs);
+  p->bwd_fits = cc3d::fits((nh + 7) * (2 * of_k + of_v), cc3d::kLinThreads);  // (where it is split it is far below)
   p->info.chunks = p->segs;
   p->info.backward_chunks = p->bwd_segs;
   p->info.workspace_bytes = nh * (p->segs - 1) * d->dk * d->dv * 4;
