@@ -32,15 +32,17 @@ namespace cc3d {
 
 // --- linear attention
 
-constexpr int kLinTokens = 64;   // tokens taken at a time
-constexpr int kLinThreads = 256;
+constexpr int kLinTokens = 64;   // segments are multiples of so many tokens
 constexpr int kLinShort = 32;    // forward calls of up to so many tokens take them one after another
+constexpr int kLinThreads = 256; // at most, of any launch
 
-// Widths as the kernels pad them, and how many columns of a state a workgroup
-// holds: its tiles, in fp32 with the decay's gradient, fill 160 KB at 256.
+// Widths as the kernels pad them; tokens of a block (fp32 rows of 256 columns fill
+// 160 KB of LDS with fewer); columns of a state that a workgroup holds, 32 a wave,
+// where the widest recurrence of a launch has `width`.
 inline int linear_pad(int width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
-constexpr int linear_cols(int pad) { return pad == 256 ? 32 : 64; }
-inline int64_t linear_blocks(int width, int pad) { return (width + linear_cols(pad) - 1) / linear_cols(pad); }
+constexpr int linear_tokens(int elem, int pad) { return elem == 4 && pad == 256 ? 32 : 64; }
+constexpr int linear_cols(int width) { return width <= 64 ? 64 : 128; }
+inline int64_t linear_blocks(int width, int cols) { return (width + cols - 1) / cols; }
 
 // Parts of the backward call's workspace, in floats, in this order.
 struct LinearSpace {
@@ -58,8 +60,7 @@ inline LinearSpace linear_bwd_space(const cc3d_linear_plan& p) {
   s.dq = d.q_heads == d.heads ? 0 : up(el * d.dk);
   s.dk = d.k_heads == d.heads ? 0 : up(el * d.dk);
   s.dv = d.v_heads == d.heads ? 0 : up(el * d.dv);
-  const int pad = linear_pad(d.dk > d.dv ? d.dk : d.dv);
-  s.decay = up(2 * nh * p.bwd_segs * linear_blocks(d.dk, pad));  // (64 bits each)
+  s.decay = up(2 * nh * p.bwd_segs * linear_blocks(d.dk, linear_cols(d.dk)));  // (64 bits each)
   s.total = 3 * s.state + s.dq + s.dk + s.dv + s.decay;
   return s;
 }

@@ -14,16 +14,21 @@
 // the operands keep the names of the first here: contraction width C (of q and k)
 // and value width E (of v and o).
 //
-// A workgroup of four waves walks a segment of the time axis with the state of
-// one head, C by up to 64 columns of E, in registers (fp32, in the layout of the
-// matrix products' results) and, for the products with q, as a bf16 copy in LDS.
-// Wave w takes tokens 16w..16w+15 of a block: its rows of q stay in its registers
-// as operands of both products, and the products q.k, computed transposed, leave
-// the matrix cores in the very layout that their second product wants (the order
-// of the tokens inside a sum is free as long as both operands agree), so they
-// never pass through LDS.  Operands that need tokens along the registers are read
-// from LDS with the transposing load.  The next block's rows load while one is
-// computed.
+// A workgroup walks a segment of the time axis with the state of one head in
+// registers: each of its waves has 32 columns of E, all of C, as the 32 by 32
+// results of matrix products (fp32).  What is multiplied again never passes through
+// LDS on its way: the eight results of a lane in 16 rows are made neighbours by the
+// order in which rows and columns are read (`place`), so that a lane's results,
+// rounded, are its operand of the next product.  That holds for the state, which
+// meets q from registers, and for the products q.k, which only go to LDS because
+// all waves want those that one computed.  Operands whose tokens lie along the
+// registers are read from LDS with the transposing load.  The next block's rows load
+// while one is computed.
+//
+// With tiles of 16 by 16, the state's copy in LDS and each wave with 16 tokens of a
+// block, a compute unit took 4.7 us for 64 tokens of a 128 by 128 head with its
+// operands in cache: LDS, vector and matrix units one after the other, some 3 to
+// 4 thousand cycles each.  Tiles of 32 by 32 read half as much from LDS.
 //
 // Few heads leave compute units idle, so the time axis is split: linear_run
 // without outputs gives what each segment adds to the state, linear_join carries
@@ -37,6 +42,8 @@
 // as two bf16 as well and multiplies both products of its pairs in fp32.  fp32 tensors
 // use the fp32 matrix products throughout.
 #pragma once
+#include <algorithm>
+
 #include "cc3d_heads_internal.h"
 #include "cc3d_seq_device.h"
 
@@ -88,12 +95,10 @@ namespace {
 
 using cc3d::LinArgs;
 using cc3d::LinRun;
-constexpr int kTok = cc3d::kLinTokens;
 
 typedef __bf16 bf16x8_h __attribute__((ext_vector_type(8)));
 typedef short s16x4_h __attribute__((ext_vector_type(4)));
-typedef unsigned u32x2_h __attribute__((ext_vector_type(2)));
-typedef u32x2_h u32x2_by2 __attribute__((aligned(2)));
+typedef float f32x16_h __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ int valid_tokens(const int* lengths, int n, int t) {
   return lengths ? min(max(lengths[n], 0), t) : t;
@@ -119,71 +124,106 @@ __device__ __forceinline__ T* pin(T* p) {
 }
 
 __device__ __forceinline__ f32x4_s zero4() { return f32x4_s{0.f, 0.f, 0.f, 0.f}; }
+__device__ __forceinline__ f32x16_h zero16() { return f32x16_h(0.f); }
 
-// v rounded to bf16 and the rest, rounded too: v = hi + lo but for 2^-16 of it.
-__device__ __forceinline__ void split_bf16(float v, float w, unsigned& hi, unsigned& lo) {
-  hi = pack_bf16(v, w);
-  const float hv = __uint_as_float(hi << 16), hw = __uint_as_float(hi & 0xffff0000u);
-  // (infinite, or rounded to an infinity: no rest)
-  lo = pack_bf16(__builtin_fabsf(hv) == __builtin_inff() ? 0.f : v - hv, __builtin_fabsf(hw) == __builtin_inff() ? 0.f : w - hw);
+// Two values rounded in one instruction.
+typedef __bf16 bf16x2_h __attribute__((ext_vector_type(2)));
+typedef float f32x2_h __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ unsigned pack2(float lo, float hi) {
+  return __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2_h{lo, hi}, bf16x2_h));
 }
 
-// Operands of the matrix products: 32 terms of a sum for 16 rows, eight a lane
-// (row lane % 16, terms 8 (lane / 16) .. + 7 of a row in memory, or tokens
-// 4 (lane / 16) .. + 3 of two tiles of 16 where tokens are summed over).
+// What rounding v to hi leaves; nothing where that is an infinity (the median of
+// r, 0 and r is r, but 0 where r is no number).
+__device__ __forceinline__ float rest(float v, float hi) { return __builtin_amdgcn_fmed3f(v - hi, 0.f, v - hi); }
+
+// Two values rounded to bf16 and the rests, rounded too: v = hi + lo but for 2^-16 of it.
+__device__ __forceinline__ void split2(float v, float w, unsigned& hi, unsigned& lo) {
+  hi = pack2(v, w);
+  lo = pack2(rest(v, __uint_as_float(hi << 16)), rest(w, __uint_as_float(hi & 0xffff0000u)));
+}
+
+// Row (or column) m of 32 of a product's result holds place(m) of what it is
+// computed from.  A lane has the results m = 8 (r / 4) + 4 h + r % 4 of its column
+// (r of 16 registers, h its half of the wave), so place(m) = 16 (r / 8) + 8 h + r % 8:
+// eight neighbours in registers 0..7, the eight 16 on in 8..15.
+__device__ __forceinline__ int place(int m) { return m / 16 * 16 + m % 8 / 4 * 8 + m % 16 / 8 * 4 + m % 4; }
+
+// Operands of the matrix products: 16 terms of a sum for 32 rows, eight a lane
+// (row lane % 32, terms 8 (lane / 32) .. + 7).
 template <class T>
 struct Mat;
 
 template <>
 struct Mat<bf16_s> {
   using Frag = bf16x8_h;
+  // Elements between rows beside their own.  Rows of 16 bytes for 16 lanes meet all 64 banks where rows
+  // are an odd number of 16 bytes apart, and the transposing loads (four rows of 64 bytes) meet no bank
+  // more than twice where that is 12 or 36 words (of 64).
   static constexpr int kPad = 8;
+  static constexpr int pad_both(int width) { return width % 128 == 0 ? 24 : 8; }
   static constexpr int kParts = 2;  // of what is rounded on its way into a state
-  static __device__ __forceinline__ f32x4_s mma(Frag a, Frag b, f32x4_s c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  static __device__ __forceinline__ f32x16_h mma(Frag a, Frag b, f32x16_h c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
-  static __device__ __forceinline__ Frag of(const Raw8<bf16_s>& r) { return __builtin_bit_cast(Frag, r.q[0]); }
   static __device__ __forceinline__ Frag row(const bf16_s* p) {
     return __builtin_bit_cast(Frag, *reinterpret_cast<const u32x4_s*>(p));
   }
-  // four tokens below each other, at p and 16 rows on, of column lane % 16: p is the lane's place among
-  // the four rows of 16 columns that its 16 lanes read together
+  // eight rows from 8 h on of column place(lane % 32): p is the lane's place among the four rows of 16
+  // columns that its 16 lanes read together
   static __device__ __forceinline__ const bf16_s* col_at(const bf16_s* tile, int stride, int lane) {
-    return tile + (4 * (lane / 16) + lane % 16 / 4) * stride + 4 * (lane % 4);
+    const int chunk = lane % 4;  // of four columns: the middle ones change places
+    return tile + (lane / 32 * 8 + lane % 16 / 4) * stride + lane % 32 / 16 * 16 + 4 * (chunk % 2 * 2 + chunk / 2);
   }
   static __device__ __forceinline__ s16x4_h col4(const bf16_s* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
         (__attribute__((address_space(3))) s16x4_h*)(const_cast<bf16_s*>(p)));
   }
   static __device__ __forceinline__ Frag col(const bf16_s* p, int stride) {
-    const s16x4_h a = col4(p), b = col4(p + 16 * stride);
+    const s16x4_h a = col4(p), b = col4(p + 4 * stride);
     return __builtin_bit_cast(Frag, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   }
-  static __device__ __forceinline__ Frag of(f32x4_s a, f32x4_s b) {
-    return __builtin_bit_cast(Frag, u32x4_s{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]),
-                                            pack_bf16(b[2], b[3])});
+  // results 8 g .. 8 g + 7, rounded
+  template <int g>
+  static __device__ __forceinline__ Frag of(const f32x16_h& v) {
+    return __builtin_bit_cast(Frag, u32x4_s{pack2(v[8 * g], v[8 * g + 1]), pack2(v[8 * g + 2], v[8 * g + 3]),
+                                            pack2(v[8 * g + 4], v[8 * g + 5]), pack2(v[8 * g + 6], v[8 * g + 7])});
   }
-  static __device__ __forceinline__ void put4(bf16_s* p, f32x4_s v) {
-    *reinterpret_cast<u32x2_h*>(p) = u32x2_h{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-  }
-  static __device__ __forceinline__ void put4_split(bf16_s* p, bf16_s* q, f32x4_s v) {
-    u32x2_h hi, lo;
+  template <int g>
+  static __device__ __forceinline__ void split(const f32x16_h& v, Frag (&out)[kParts]) {
+    u32x4_s hi, lo;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      unsigned h, l;
-      split_bf16(v[2 * i], v[2 * i + 1], h, l);
-      hi[i] = h;
-      lo[i] = l;
+    for (int i = 0; i < 4; ++i) {
+      unsigned x, y;
+      split2(v[8 * g + 2 * i], v[8 * g + 2 * i + 1], x, y);
+      hi[i] = x;
+      lo[i] = y;
     }
-    *reinterpret_cast<u32x2_h*>(p) = hi;
-    *reinterpret_cast<u32x2_h*>(q) = lo;
+    out[0] = __builtin_bit_cast(Frag, hi);
+    out[1] = __builtin_bit_cast(Frag, lo);
   }
-  static __device__ __forceinline__ void put8(bf16_s* p, const Raw8<bf16_s>& r) {
-    *reinterpret_cast<u32x4_s*>(p) = r.q[0];
+  // f[i] times the eight terms, in kParts
+  static __device__ __forceinline__ void scaled(Frag v, const float (&f)[8], Frag (&out)[kParts]) {
+    const u32x4_s w = __builtin_bit_cast(u32x4_s, v);
+    u32x4_s hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      unsigned x, y;
+      split2(__uint_as_float(w[i] << 16) * f[2 * i], __uint_as_float(w[i] & 0xffff0000u) * f[2 * i + 1], x, y);
+      hi[i] = x;
+      lo[i] = y;
+    }
+    out[0] = __builtin_bit_cast(Frag, hi);
+    out[1] = __builtin_bit_cast(Frag, lo);
   }
-  static __device__ __forceinline__ void put8_split(bf16_s* p, bf16_s* q, const float* v) {
-    put4_split(p, q, f32x4_s{v[0], v[1], v[2], v[3]});
-    put4_split(p + 4, q + 4, f32x4_s{v[4], v[5], v[6], v[7]});
+  static __device__ __forceinline__ void put(bf16_s* p, Frag v) { *reinterpret_cast<u32x4_s*>(p) = __builtin_bit_cast(u32x4_s, v); }
+  static __device__ __forceinline__ void put(bf16_s* p, const Raw8<bf16_s>& r) { *reinterpret_cast<u32x4_s*>(p) = r.q[0]; }
+  // not zero where an element's exponent is full: an infinity or no number
+  static __device__ __forceinline__ unsigned full(const Raw8<bf16_s>& r) {
+    unsigned v = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v |= (r.q[0][i] & 0x7f807f80u) + 0x00800080u;
+    return v & 0x80008000u;
   }
 };
 
@@ -193,41 +233,54 @@ struct Mat<float> {
     float x[8];
   };
   static constexpr int kPad = 4;
+  static constexpr int pad_both(int) { return 4; }
   static constexpr int kParts = 1;
-  // (the eight products take the lanes' terms one after another: any order of the 32 does)
-  static __device__ __forceinline__ f32x4_s mma(const Frag& a, const Frag& b, f32x4_s c) {
+  // (the eight products take the lanes' terms one after another: any order of the 16 does)
+  static __device__ __forceinline__ f32x16_h mma(const Frag& a, const Frag& b, f32x16_h c) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x[i], b.x[i], c, 0, 0, 0);
+    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.x[i], b.x[i], c, 0, 0, 0);
     return c;
   }
-  static __device__ __forceinline__ Frag of(const Raw8<float>& r) { return __builtin_bit_cast(Frag, r); }
   static __device__ __forceinline__ Frag row(const float* p) {
     Raw8<float> r;
     r.q[0] = reinterpret_cast<const u32x4_s*>(p)[0];
     r.q[1] = reinterpret_cast<const u32x4_s*>(p)[1];
-    return of(r);
+    return __builtin_bit_cast(Frag, r);
   }
   static __device__ __forceinline__ const float* col_at(const float* tile, int stride, int lane) {
-    return tile + 4 * (lane / 16) * stride + lane % 16;
+    return tile + lane / 32 * 8 * stride + place(lane % 32);
   }
   static __device__ __forceinline__ Frag col(const float* p, int stride) {
     Frag f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f.x[i] = p[(i % 4 + i / 4 * 16) * stride];
+    for (int i = 0; i < 8; ++i) f.x[i] = p[i * stride];
     return f;
   }
-  static __device__ __forceinline__ Frag of(f32x4_s a, f32x4_s b) {
-    return Frag{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+  template <int g>
+  static __device__ __forceinline__ Frag of(const f32x16_h& v) {
+    Frag f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.x[i] = v[8 * g + i];
+    return f;
   }
-  static __device__ __forceinline__ void put4(float* p, f32x4_s v) { *reinterpret_cast<f32x4_s*>(p) = v; }
-  static __device__ __forceinline__ void put4_split(float* p, float*, f32x4_s v) { put4(p, v); }
-  static __device__ __forceinline__ void put8(float* p, const Raw8<float>& r) {
+  template <int g>
+  static __device__ __forceinline__ void split(const f32x16_h& v, Frag (&out)[kParts]) {
+    out[0] = of<g>(v);
+  }
+  static __device__ __forceinline__ void scaled(const Frag& v, const float (&f)[8], Frag (&out)[kParts]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[0].x[i] = v.x[i] * f[i];
+  }
+  static __device__ __forceinline__ void put(float* p, const Frag& v) { put(p, __builtin_bit_cast(Raw8<float>, v)); }
+  static __device__ __forceinline__ void put(float* p, const Raw8<float>& r) {
     reinterpret_cast<u32x4_s*>(p)[0] = r.q[0];
     reinterpret_cast<u32x4_s*>(p)[1] = r.q[1];
   }
-  static __device__ __forceinline__ void put8_split(float* p, float* q, const float* v) {
-    put4_split(p, q, f32x4_s{v[0], v[1], v[2], v[3]});
-    put4_split(p + 4, q + 4, f32x4_s{v[4], v[5], v[6], v[7]});
+  static __device__ __forceinline__ unsigned full(const Raw8<float>& r) {
+    unsigned v = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v |= (r.q[i / 4][i % 4] & 0x7f800000u) + 0x00800000u;
+    return v & 0x80000000u;
   }
 };
 
@@ -248,14 +301,14 @@ struct Cols8 {
   int c, shift;  // where it is loaded, and how many elements too early; 8: all is zero
   __device__ __forceinline__ Cols8(int col, int width)
       : c(KIND == kLess ? col : min(col, width - 8)), shift(col >= width ? 8 : KIND == kRest ? col - c : 0) {}
-  __device__ __forceinline__ Raw8<T> load(const T* row, int width) const {
+  __device__ __forceinline__ Raw8<T> load(const T* p, int width) const {  // p: at column c of a row
     if constexpr (KIND == kLess) {
       Raw8<T> r;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) set8(r, j, row[min(c + j, width - 1)]);
+      for (int j = 0; j < 8; ++j) set8(r, j, p[min(c + j, width - 1) - c]);
       return r;
     } else {
-      return load8(row + c);
+      return load8(p);
     }
   }
   __device__ __forceinline__ Raw8<T> finish(Raw8<T> v, bool on, int width) const {
@@ -292,49 +345,57 @@ struct Cols8 {
   }
 };
 
-// Four columns of a result.
+// Eight columns of a result.
 template <class T, int KIND>
-__device__ __forceinline__ void store_cols(T* row, int col, int width, f32x4_s v) {
-  if (KIND == kEights ? col < width : col + 4 <= width) {
+__device__ __forceinline__ void store_cols(T* row, int col, int width, const float* v) {
+  if (KIND == kEights ? col < width : col + 8 <= width) {
+    using Q = typename Quad<T>::type;
     if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<u32x2_by2*>(row + col) = u32x2_h{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+      *reinterpret_cast<Q*>(row + col) = u32x4_s{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
     } else {
-      *reinterpret_cast<u32x4_by4*>(row + col) = __builtin_bit_cast(u32x4_s, v);
+      store8(row + col, v);
     }
-  } else if (KIND != kEights) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (col + i < width) row[col + i] = from_f32<T>(v[i]);
+  } else if (KIND != kEights && col < width) {
+    store_some(row + col, width - col, v);
   }
 }
 
-// LDS of a workgroup, in elements of T: rows of k, rows of v, the rows of f v in
-// kParts (twice with the decay's derivative), the state's columns (with the
-// derivative: both, each in kParts; not without outputs).
-template <class T, int DP, bool OUT, bool DEC>
+// LDS of a workgroup, in elements of T: rows of q, of k and of v, the products q.k
+// as operands; with the decay's gradient, rows of x.
+template <class T, int DP, int CB, int TOK, bool OUT, bool DEC>
 struct LinTiles {
   using M = Mat<T>;
-  static constexpr int kCols = cc3d::linear_cols(DP);
-  static constexpr int kRowK = DP + M::kPad, kRowV = kCols + M::kPad;
-  static constexpr int kK = 0, kV = kK + kTok * kRowK, kF = kV + (OUT ? kTok * kRowV : 0);
-  static constexpr int kS = kF + kTok * kRowV * M::kParts * (DEC ? 2 : 1);
-  static constexpr int kStates = !OUT ? 0 : DEC ? 2 * M::kParts : 1;
-  static constexpr int kTotal = kS + kCols * kRowK * kStates;
-  static constexpr int kBytes = kTotal * int(sizeof(T));
+  static constexpr int kRowQ = DP + M::kPad, kRowK = DP + M::pad_both(DP), kRowV = CB + M::pad_both(CB);
+  static constexpr int kK = 0, kV = kK + TOK * kRowK, kQ = kV + TOK * kRowV, kP = kQ + (OUT ? TOK * kRowQ : 0);
+  static constexpr int kPairs = TOK == 64 ? 3 : 1;  // tiles of 32 by 32 pairs of tokens
+  static constexpr int kX = kP + (OUT && !DEC ? kPairs * 2 * 64 * 8 : 0);
+  static constexpr int kTotal = kX + (OUT && DEC ? TOK * kRowV : 0);
+  static constexpr int kBytes = kTotal * int(sizeof(T)) > 4096 ? kTotal * int(sizeof(T)) : 4096;
 };
 
-template <class T, int DP, int KIND, bool OUT, bool DEC>
-__global__ __launch_bounds__(cc3d::kLinThreads, DEC || sizeof(T) == 4 || DP == 256 ? 1 : 2) void linear_run(LinArgs a) {
+// Waves a SIMD that the registers are held to: two workgroups a compute unit where
+// their tiles and the state allow.
+template <class T, int DP, bool DEC>
+constexpr int linear_waves() {
+  return sizeof(T) == 2 && DP <= 128 && !DEC ? 2 : 1;
+}
+
+template <class T, int DP, int CB, int KIND, bool OUT, bool DEC>
+__global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_run(LinArgs a) {
   using M = Mat<T>;
-  using L = LinTiles<T, DP, OUT, DEC>;
   using Frag = typename M::Frag;
-  constexpr int kCols = L::kCols, kRowK = L::kRowK, kRowV = L::kRowV;
-  constexpr int kMt = DP / 64, kNt = kCols / 16, kSteps = DP / 32;  // a wave's tiles of the state, steps of a sum over C
-  constexpr int kVecK = DP / 32, kVecV = kCols / 32;                // eights of k and v that a thread stages
+  constexpr int TOK = cc3d::linear_tokens(sizeof(T), DP);  // tokens of a block
+  using L = LinTiles<T, DP, CB, TOK, OUT, DEC>;
+  constexpr int kThreads = 2 * CB, kWaves = CB / 32, kRowQ = L::kRowQ, kRowK = L::kRowK, kRowV = L::kRowV;
+  constexpr int kMt = DP / 32, kSteps = DP / 16, kIt = TOK / 32, kTs = TOK / 16;  // tiles and steps of C, of the tokens
+  constexpr int kVecK = TOK * DP / 8 / kThreads, kVecV = TOK * CB / 8 / kThreads;  // eights that a thread stages
+  constexpr int kStepK = kThreads / (DP / 8), kStepV = kThreads / (CB / 8);
+  constexpr bool kGrad = DEC && OUT;
+  static_assert(kVecK * kThreads * 8 == TOK * DP && kVecV * kThreads * 8 == TOK * CB, "threads");
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ int odd[2];  // a block of v holds an infinity or NaN
+  __shared__ int odd[2];  // a block of k or v holds an infinity or NaN
   T* lds = reinterpret_cast<T*>(smem);
-  const int tid = threadIdx.x, lane = tid % 64, wave = pin(tid / 64), lane16 = lane % 16, quad = lane / 16;
+  const int tid = threadIdx.x, lane = tid % 64, wave = pin(tid / 64), il = lane % 32, hh = lane / 32;
 
   // Workgroups go to the eight dies in turn, each with a cache of its own: those
   // of one head and segment (its columns, its recurrences), which read the same
@@ -352,376 +413,385 @@ __global__ __launch_bounds__(cc3d::kLinThreads, DEC || sizeof(T) == 4 || DP == 2
   // (a reversed recurrence of the same rows is at the other end of its segments)
   const int s = pin(OUT && r.rev ? starts - 1 - turned : turned);
   const int64_t nh = int64_t(n) * a.heads + h;
-  const int e0 = block * kCols;
+  const int e0 = block * CB;
   const int len = pin(valid_tokens(a.lengths, n, a.t));
   const int begin = s * a.seg, end = pin(min(begin + a.seg, len));
-  const int c_all = pin(r.c), width = pin(min(kCols, r.e - e0));
+  const int c_all = pin(r.c), width = pin(min(CB, r.e - e0));
   const int sc = pin(r.sc), se = pin(r.se), rev = pin(r.rev), r_lead = pin(r.lead);
-  const float update = pin(r.update);
 
-  const T* q = pin(static_cast<const T*>(r.q) + n * r.qb + int64_t(h / r.qper) * r.c);
-  const T* k = pin(static_cast<const T*>(r.k) + n * r.kb + int64_t(h / r.kper) * r.c);
-  const T* v = pin(static_cast<const T*>(r.v) + n * r.vb + int64_t(h / r.vper) * r.e + e0);
-  const int64_t qr = pin(r.qr), kr = pin(r.kr), vr = pin(r.vr), o_row = pin(r.orow);
-  const int64_t o_at = pin(n * r.ob + int64_t(h) * r.e + e0);
+  // Rows of a block are at 32-bit offsets from its first token; a place may be up to
+  // seven elements before a row's (Cols8), so offsets count from eight before.
+  constexpr unsigned kBias = KIND == kRest ? 8 : 0, kSize = sizeof(T);
+  const T* q = pin(static_cast<const T*>(r.q) + n * r.qb + int64_t(h / r.qper) * r.c - kBias);
+  const T* k = pin(static_cast<const T*>(r.k) + n * r.kb + int64_t(h / r.kper) * r.c - kBias);
+  const T* v = pin(static_cast<const T*>(r.v) + n * r.vb + int64_t(h / r.vper) * r.e + e0 - kBias);
+  const T* x = nullptr;
+  if constexpr (kGrad) x = pin(static_cast<const T*>(a.x) + n * a.xb + int64_t(h / a.xper) * r.e + e0 - kBias);
+  const int qr = pin(int(r.qr)), kr = pin(int(r.kr)), vr = pin(int(r.vr)), o_row = pin(int(r.orow)), xr = kGrad ? pin(int(a.xr)) : 0;
   char* o_p = pin(static_cast<char*>(r.o));
+  const int64_t o_at = pin(n * r.ob + int64_t(h) * r.e + e0);
   const int o_f32 = pin(r.o_f32);
-  // token p of the recurrence
-  auto at = [&](int p) { return int64_t(rev ? len - 1 - p : p); };
+  auto by = [](const T* p, unsigned bytes) { return reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + bytes); };
+  auto first_token = [&](int p0, int m) { return int64_t(rev ? len - p0 - m : p0); };
 
-  const float g = a.log_decay ? a.log_decay[h] : 0.f, g2 = g * kLog2e;
-  const float whole_m1 = pin(fade_m1(g, kTok));
+  // ---- rows of a block in flight.  A block of m < TOK tokens has them as its last rows, behind rows of zeros.
+  Raw8<T> kn[kVecK], vn[kVecV], qn[OUT ? kVecK : 1], xn[kGrad ? kVecV : 1];
+  const int krow = tid / (DP / 8), kcol = tid % (DP / 8) * 8, vrow = tid / (CB / 8), vcol = tid % (CB / 8) * 8;
+  const Cols8<T, KIND> kc(kcol, c_all), vc(vcol, width);
+  auto fetch = [&](int p0) {
+    const int m = min(TOK, end - p0);
+    const int64_t t = first_token(p0, m);
+    const T *kb = k + t * kr, *vb = v + t * vr;
+    auto place_of = [&](int j, int stride, const Cols8<T, KIND>& c) {
+      const int tok = max(j - (TOK - m), 0);
+      return (unsigned(rev ? m - 1 - tok : tok) * unsigned(stride) + unsigned(c.c) + kBias) * kSize;
+    };
+#pragma unroll
+    for (int y = 0; y < kVecK; ++y) kn[y] = kc.load(by(kb, place_of(krow + y * kStepK, kr, kc)), c_all);
+#pragma unroll
+    for (int y = 0; y < kVecV; ++y) vn[y] = vc.load(by(vb, place_of(vrow + y * kStepV, vr, vc)), width);
+    if constexpr (OUT) {
+      const T* qb = q + t * qr;
+#pragma unroll
+      for (int y = 0; y < kVecK; ++y) qn[y] = kc.load(by(qb, place_of(krow + y * kStepK, qr, kc)), c_all);
+    }
+    if constexpr (kGrad) {
+      const T* xb = x + t * xr;
+#pragma unroll
+      for (int y = 0; y < kVecV; ++y) xn[y] = vc.load(by(xb, place_of(vrow + y * kStepV, xr, vc)), width);
+    }
+  };
+  if (begin < end) fetch(begin);
 
-  // ---- the state before the segment, in the products' layout: element i of tile (mt, nt) is
-  // c = 16 (wave kMt + mt) + 4 quad + i, e = 16 nt + lane16
-  f32x4_s st[kMt][kNt], st2[DEC ? kMt : 1][DEC ? kNt : 1];
-  // f(mt, nt, c, e): the four elements from c on of column e
-  auto each_state = [&](auto&& f) {
+  // ---- the state before the segment: result i of tile mt is c = 32 mt + 16 (i / 8) + 8 hh + i % 8 of the lane's column
+  f32x16_h st[kMt], st2[DEC ? kMt : 1];
+  const int col = 32 * wave + place(il);  // of the lane
+  const bool has = 32 * wave < width;     // the wave has columns
+  // (unconditional loads, for the same reason as those of the rows)
+  auto load_state = [&](const float* p, f32x16_h (&v)[kMt]) {
+    const bool in = col < width;
+    p += (e0 + min(col, width - 1)) * se;
 #pragma unroll
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) f(mt, nt, 16 * (wave * kMt + mt) + 4 * quad, 16 * nt + lane16);
-  };
-  // (unconditional loads, for the same reason as those of the rows)
-  auto load_state = [&](const float* p, int c, int e) {
-    f32x4_s v = zero4();
-    if (!p) return v;
-    const bool in = e < width;
-    p += (e0 + min(e, width - 1)) * se;
-    if (KIND == kEights && sc == 1) {
-      v = __builtin_bit_cast(f32x4_s, *reinterpret_cast<const u32x4_by4*>(p + min(c, c_all - 4)));
+      for (int g = 0; g < 2; ++g) {
+        const int c = 32 * mt + 16 * g + 8 * hh;
+        if (KIND == kEights && sc == 1) {
+          const u32x4_by4* w = reinterpret_cast<const u32x4_by4*>(p + min(c, c_all - 8));
+          const f32x4_s lo = __builtin_bit_cast(f32x4_s, w[0]), hi = __builtin_bit_cast(f32x4_s, w[1]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = (in & (c < c_all)) ? v[i] : 0.f;
-    } else {
+          for (int i = 0; i < 4; ++i) {
+            v[mt][8 * g + i] = (in & (c < c_all)) ? lo[i] : 0.f;
+            v[mt][8 * g + 4 + i] = (in & (c < c_all)) ? hi[i] : 0.f;
+          }
+        } else {
+          float u[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = p[min(c + i, c_all - 1) * sc];
+          for (int i = 0; i < 8; ++i) u[i] = p[min(c + i, c_all - 1) * sc];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = (in & (c + i < c_all)) ? v[i] : 0.f;
-    }
-    return v;
-  };
-  auto store_state = [&](float* p, int c, int e, f32x4_s v) {
-    if (!((e < width) & (c < c_all))) return;
-    p += (e0 + e) * se + c * sc;
-    if (KIND == kEights) {
-      if (sc == 1) {
-        *reinterpret_cast<u32x4_by4*>(p) = __builtin_bit_cast(u32x4_s, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i * sc] = v[i];
+          for (int i = 0; i < 8; ++i) v[mt][8 * g + i] = (in & (c + i < c_all)) ? u[i] : 0.f;
+        }
       }
-    } else {
+  };
+  auto store_state = [&](float* p, const f32x16_h (&v)[kMt]) {
+    if (col >= width) return;
+    p += (e0 + col) * se;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c + i < c_all) p[i * sc] = v[i];
-    }
+    for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int c = 32 * mt + 16 * g + 8 * hh;
+        if (KIND == kEights) {
+          if (c >= c_all) continue;
+          if (sc == 1) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              reinterpret_cast<u32x4_by4*>(p + c)[i] =
+                  __builtin_bit_cast(u32x4_s, f32x4_s{v[mt][8 * g + 4 * i], v[mt][8 * g + 4 * i + 1], v[mt][8 * g + 4 * i + 2],
+                                                      v[mt][8 * g + 4 * i + 3]});
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[(c + i) * sc] = v[mt][8 * g + i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < c_all) p[(c + i) * sc] = v[mt][8 * g + i];
+        }
+      }
   };
   const int64_t size = int64_t(r.c) * r.e;
   const float* from = nullptr;
   if constexpr (OUT) from = s > 0 ? r.segs + (nh * (a.segs - 1) + s - 1) * size : r.from ? r.from + nh * size : nullptr;
-  each_state([&](int mt, int nt, int c, int e) { st[mt][nt] = load_state(from, c, e); });
+  if (from && has) {
+    load_state(from, st);
+  } else {
+#pragma unroll
+    for (int mt = 0; mt < kMt; ++mt) st[mt] = zero16();
+  }
   if constexpr (DEC) {
-    const float* from2 = OUT && s > 0 ? a.segs2 + (nh * (a.segs - 1) + s - 1) * size : nullptr;
-    each_state([&](int mt, int nt, int c, int e) { st2[mt][nt] = load_state(from2, c, e); });
-  }
-  // its columns as rows of an operand
-  auto put_state = [&] {
-    if constexpr (OUT) {
+    if (OUT && s > 0 && has) {
+      load_state(a.segs2 + (nh * (a.segs - 1) + s - 1) * size, st2);
+    } else {
 #pragma unroll
-      for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < kNt; ++nt) {
-          T* p = lds + L::kS + (16 * nt + lane16) * kRowK + 16 * (wave * kMt + mt) + 4 * quad;
-          constexpr int kOne = kCols * kRowK;
-          if constexpr (DEC) {
-            M::put4_split(p, p + kOne, st[mt][nt]);
-            M::put4_split(p + kOne * M::kParts, p + kOne * (M::kParts + 1), st2[mt][nt]);
-          } else {
-            M::put4(p, st[mt][nt]);
-          }
-        }
+      for (int mt = 0; mt < kMt; ++mt) st2[mt] = zero16();
     }
-  };
+  }
 
-  // ---- constants of a lane: its token i of a block, the factors f[i-j] of its products q.k
-  const int i_tok = 16 * wave + lane16;
-  float near[4][4], lead = 0.f;
+  // ---- factors, all of them f of a number of tokens, never of less than none.  Token j of a block (from its end)
+  // adds f[TOK-1-j] = f[16 (TOK/16-1-j/16)] f[15-j%16], and tokens i of the second tile and j of the first are
+  // f[il+1] f[31-jl] apart: a few by step, in scalar registers, times a few by lane.
+  const float g = a.log_decay ? a.log_decay[h] : 0.f, g2 = g * kLog2e;
+  const float whole_m1 = pin(fade_m1(g, TOK)), last_m1 = begin < end ? pin(fade_m1(g, (end - begin - 1) % TOK + 1)) : 0.f;
+  float fq[8], diag[OUT ? 16 : 1], f_lane = 0.f, f_step[kTs];
+#pragma unroll
+  for (int b = 0; b < 8; ++b) fq[b] = fade(g2, 15 - 8 * hh - b);
+#pragma unroll
+  for (int y = 0; y < kTs; ++y) f_step[y] = pin(fade(g2, 16 * y));
+  const float f_last = pin(r.update) * fade(g2, 1 - r_lead), inter = pin(r.inter), score = pin(r.score);
   if constexpr (OUT) {
-    const float score = pin(r.score), inter = pin(r.inter);
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = i_tok - (16 * t + 4 * quad + i);
-        near[t][i] = score * fade(g2, max(d, 0));
-      }
-    lead = inter * fade(g2, i_tok + r_lead);
+    for (int b = 0; b < 16; ++b) diag[b] = score * fade(g2, max(il - (16 * (b / 8) + 8 * hh + b % 8), 0));
+    f_lane = score * fade(g2, il + 1);
   }
-
-  // ---- rows of a block in flight
-  Raw8<T> kn[kVecK], vn[kVecV], qn[OUT ? kSteps : 1], xn[DEC && OUT ? kCols / 32 : 1];
-  f32x4_s xe[DEC && OUT ? kNt : 1];
-  const int krow = tid / (DP / 8), vrow = tid / (kCols / 8);
-  constexpr int kStepK = 256 / (DP / 8), kStepV = 256 / (kCols / 8);
-  const Cols8<T, KIND> kc(tid % (DP / 8) * 8, c_all), vc(tid % (kCols / 8) * 8, width);
-  const T* x = DEC && OUT ? static_cast<const T*>(a.x) + n * a.xb + int64_t(h / a.xper) * r.e + e0 : nullptr;
-  auto fetch = [&](int p0) {
-#pragma unroll
-    for (int y = 0; y < kVecK; ++y) kn[y] = kc.load(k + at(min(p0 + krow + y * kStepK, end - 1)) * kr, c_all);
-#pragma unroll
-    for (int y = 0; y < kVecV; ++y) vn[y] = vc.load(v + at(min(p0 + vrow + y * kStepV, end - 1)) * vr, width);
-    if constexpr (OUT) {
-      const int64_t i = at(min(p0 + i_tok, end - 1));
-#pragma unroll
-      for (int y = 0; y < kSteps; ++y) qn[y] = Cols8<T, KIND>(32 * y + 8 * quad, c_all).load(q + i * qr, c_all);
-      if constexpr (DEC) {
-        const T* row = x + i * a.xr;
-#pragma unroll
-        for (int y = 0; y < kCols / 32; ++y) xn[y] = Cols8<T, KIND>(32 * y + 8 * quad, width).load(row, width);
-#pragma unroll
-        for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) xe[nt][y] = to_f32(row[min(16 * nt + 4 * quad + y, width - 1)]);
-      }
-    }
-  };
-  // the factors of f v: all blocks but the last are whole
-  float fv[kVecV];
-  auto factors = [&](int m) {
-#pragma unroll
-    for (int y = 0; y < kVecV; ++y) {
-      const int left = m - 1 - (vrow + y * kStepV);
-      const float f = update * fade(g2, max(left + 1 - r_lead, 0));
-      fv[y] = left >= 0 ? f : 0.f;
-    }
-  };
-  factors(kTok);
-  if (begin < end) fetch(begin);
-  put_state();
   if (tid < 2) odd[tid] = 0;
   __syncthreads();
 
   double decay = 0.0;
   const bool keeps = OUT ? s + 1 == a.segs && (r.to || (DEC && a.dto)) : true;  // the state after the segment is asked for
   int turn = 0;
-  for (int p0 = begin; p0 < end; p0 += kTok, turn ^= 1) {
-    const int m = min(kTok, end - p0);
-    // ---- stage k, v and f v
+  for (int p0 = begin; p0 < end; p0 += TOK, turn ^= 1) {
+    const int m = min(TOK, end - p0), none = TOK - m;
+    const bool more = p0 + TOK < end;
+    // (what follows from these is cheap, and would be kept in registers over all blocks)
+    asm volatile("" : "+v"(fq[0]), "+v"(fq[1]), "+v"(fq[2]), "+v"(fq[3]), "+v"(fq[4]), "+v"(fq[5]), "+v"(fq[6]), "+v"(fq[7]));
+    // ---- stage the rows
+    const bool whole = m == TOK && c_all == DP && width == CB;  // nothing to put right
+    unsigned full = 0;
 #pragma unroll
     for (int y = 0; y < kVecK; ++y) {
       const int j = krow + y * kStepK;
-      M::put8(lds + L::kK + j * kRowK + tid % (DP / 8) * 8, kc.finish(kn[y], j < m, c_all));
+      if (!whole) kn[y] = kc.finish(kn[y], j >= none, c_all);
+      full |= M::full(kn[y]);
+      M::put(lds + L::kK + j * kRowK + kcol, kn[y]);
+      if constexpr (OUT) {
+        if (!whole) qn[y] = kc.finish(qn[y], j >= none, c_all);
+        M::put(lds + L::kQ + j * kRowQ + kcol, qn[y]);
+      }
     }
-    if (m < kTok) factors(m);
-    bool bad = false;
 #pragma unroll
     for (int y = 0; y < kVecV; ++y) {
-      const int j = vrow + y * kStepV, place = j * kRowV + tid % (kCols / 8) * 8;
-      const Raw8<T> raw = vc.finish(vn[y], j < m, width);
-      float f[8], f2[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float u = get8(raw, i);
-        bad = bad | !(__builtin_fabsf(u) < __builtin_inff());
-        f[i] = u * fv[y];
-        f2[i] = f[i] * float(m - 1 - j);
+      const int j = vrow + y * kStepV;
+      if (!whole) vn[y] = vc.finish(vn[y], j >= none, width);
+      full |= M::full(vn[y]);
+      M::put(lds + L::kV + j * kRowV + vcol, vn[y]);
+      if constexpr (kGrad) {
+        if (!whole) xn[y] = vc.finish(xn[y], j >= none, width);
+        M::put(lds + L::kX + j * kRowV + vcol, xn[y]);
       }
-      T* p = lds + L::kF + place;
-      constexpr int kOne = kTok * kRowV;
-      M::put8_split(p, p + kOne, f);
-      if constexpr (DEC) M::put8_split(p + kOne * M::kParts, p + kOne * (M::kParts + 1), f2);
-      if constexpr (OUT) M::put8(lds + L::kV + place, raw);
     }
-    Frag qf[OUT ? kSteps : 1], xf[DEC && OUT ? kCols / 32 : 1];
-    f32x4_s xv[DEC && OUT ? kNt : 1];
-    if constexpr (OUT) {
-#pragma unroll
-      for (int y = 0; y < kSteps; ++y) qf[y] = M::of(Cols8<T, KIND>(32 * y + 8 * quad, c_all).finish(qn[y], i_tok < m, c_all));
-      if (bad) odd[turn] = 1;
-    }
-    if constexpr (DEC && OUT) {
-#pragma unroll
-      for (int y = 0; y < kCols / 32; ++y)
-        xf[y] = M::of(Cols8<T, KIND>(32 * y + 8 * quad, width).finish(xn[y], i_tok < m, width));
-#pragma unroll
-      for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) xv[nt][y] = ((i_tok < m) & (16 * nt + 4 * quad + y < width)) ? xe[nt][y] : 0.f;
-    }
+    if (full) odd[turn] = 1;
     __syncthreads();
-    if (p0 + kTok < end) fetch(p0 + kTok);
+    if (more) fetch(p0 + TOK);
+    const bool strange = pin(odd[turn]) != 0;
 
+    const T* q_row = lds + L::kQ + il * kRowQ + 8 * hh;
     if constexpr (OUT) {
-      if (tid == 0) odd[turn ^ 1] = 0;
-      if (16 * wave < m) {
-        // ---- products q.k, transposed: element i of tile t is j = 16 t + 4 quad + i of the lane's token
-        // (waves 0 and 1 need the first two tiles)
-        f32x4_s pr[4] = {zero4(), zero4(), zero4(), zero4()};
-        const T* krows = lds + L::kK + lane16 * kRowK + 8 * quad;
-        auto scores = [&](auto first) {
-          constexpr int t0 = decltype(first)::value;
+      // ---- products q.k of 32 by 32 tokens (second tile by first, and both by themselves), transposed, a wave each in turn:
+      // result b is token j = 16 (b / 8) + 8 hh + b % 8 of its tile, of the lane's token
+      float sum = 0.f;
 #pragma unroll
-          for (int y = 0; y < kSteps; ++y)
+      for (int p = 0; p < (L::kPairs + kWaves - 1) / kWaves; ++p) {
+        const int pair = p * kWaves + wave, it = pair > 0, jt = pair > 1;
+        if (pair >= L::kPairs) break;
+        f32x16_h pr = zero16();
+        const T *kp = lds + L::kK + (32 * jt + place(il)) * kRowK + 8 * hh, *qp = q_row + 32 * it * kRowQ;
 #pragma unroll
-            for (int t = t0; t < t0 + 2; ++t) pr[t] = M::mma(M::row(krows + 16 * t * kRowK + 32 * y), qf[y], pr[t]);
-        };
-        scores(std::integral_constant<int, 0>());
-        if (wave >= 2) scores(std::integral_constant<int, 2>());
-        const T* state = lds + L::kS + lane16 * kRowK + 8 * quad;
-        if constexpr (!DEC) {
+        for (int y = 0; y < kSteps; ++y) pr = M::mma(M::row(kp + 16 * y), M::row(qp + 16 * y), pr);
+        if (pair == 1) {
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pr[t][i] = 16 * t + 4 * quad + i <= i_tok ? pr[t][i] * near[t][i] : 0.f;
-          const Frag pf[2] = {M::of(pr[0], pr[1]), M::of(pr[2], pr[3])};
-          f32x4_s o[kNt];
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) o[nt] = zero4();
-#pragma unroll
-          for (int y = 0; y < kSteps; ++y)
-#pragma unroll
-            for (int nt = 0; nt < kNt; ++nt) o[nt] = M::mma(M::row(state + 16 * nt * kRowK + 32 * y), qf[y], o[nt]);
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[nt][i] *= lead;
-          if (!odd[turn]) {
-            const T* vt = M::col_at(lds + L::kV, kRowV, lane);
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              if (y == 0 || wave >= 2) {
-#pragma unroll
-                for (int nt = 0; nt < kNt; ++nt)
-                  o[nt] = M::mma(M::col(vt + 32 * y * kRowV + 16 * nt, kRowV), pf[y], o[nt]);
-              }
-            }
-          } else {
-            // an infinity or NaN among the block's v meets no product of an earlier token, not even a zero one
-            for (int j = 0; j < kTok; ++j) {
-              float p = 0.f;
-#pragma unroll
-              for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) p = 16 * t + i == j / 16 * 16 + j % 4 ? pr[t][i] : p;
-              p = __shfl(p, j % 16 / 4 * 16 + lane16);
-              if (j <= i_tok) {
-#pragma unroll
-                for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    o[nt][i] = fmaf(p, to_f32(lds[L::kV + j * kRowV + 16 * nt + 4 * quad + i]), o[nt][i]);
-              }
-            }
-          }
-          if (i_tok < m) {
-            const int64_t row = o_at + at(p0 + i_tok) * o_row;
-            if (o_f32) {
-#pragma unroll
-              for (int nt = 0; nt < kNt; ++nt)
-                store_cols<float, KIND>(reinterpret_cast<float*>(o_p) + row, 16 * nt + 4 * quad, width, o[nt]);
-            } else {
-#pragma unroll
-              for (int nt = 0; nt < kNt; ++nt)
-                store_cols<T, KIND>(reinterpret_cast<T*>(o_p) + row, 16 * nt + 4 * quad, width, o[nt]);
-            }
-          }
+          for (int b = 0; b < 16; ++b) pr[b] *= f_lane * f_step[1 - b / 8] * fq[b % 8];
         } else {
-          // ---- the decay's gradient: with x the rows of q, (i - j) f[i-j] (do[i] . v[j]) (x[i] . k[j]) of every pair
-          // (here only these columns of x and k), and x[i] . f[i+1] (S2 + (i + 1) S) do[i]
-          float sum = 0.f;
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            if (t < 2 || wave >= 2) {
-              f32x4_s xk = zero4();
+          for (int b = 0; b < 16; ++b) pr[b] = 16 * (b / 8) + 8 * hh + b % 8 <= il ? pr[b] * diag[b] : 0.f;
+        }
+        if constexpr (!DEC) {
+          T* at = lds + L::kP + (pair * 128 + lane) * 8;
+          M::put(at, M::template of<0>(pr));
+          M::put(at + 512, M::template of<1>(pr));
+        } else {
+          // the decay's gradient: with x the rows of q, (i - j) f[i-j] (do[i] . v[j]) (x[i] . k[j]) of every pair (of
+          // these columns of x and k)
+          f32x16_h xk = zero16();
+          const T *vp = lds + L::kV + (32 * jt + place(il)) * kRowV + 8 * hh, *xp = lds + L::kX + (32 * it + il) * kRowV + 8 * hh;
 #pragma unroll
-              for (int x = 0; x < kCols / 32; ++x)
-                xk = M::mma(M::row(lds + L::kV + (16 * t + lane16) * kRowV + 32 * x + 8 * quad), xf[x], xk);
+          for (int y = 0; y < CB / 16; ++y) xk = M::mma(M::row(vp + 16 * y), M::row(xp + 16 * y), xk);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int d = i_tok - (16 * t + 4 * quad + i);
-                sum += d > 0 ? float(d) * near[t][i] * pr[t][i] * xk[i] : 0.f;
-              }
-            }
+          for (int b = 0; b < 16; ++b) {
+            const int d = 32 * (it - jt) + il - (16 * (b / 8) + 8 * hh + b % 8);
+            const float term = float(d) * pr[b] * xk[b];
+            sum += d > 0 ? term : 0.f;
           }
-          constexpr int kOne = kCols * kRowK;
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) {
-            f32x4_s u = zero4(), w = zero4();
-#pragma unroll
-            for (int y = 0; y < M::kParts; ++y)
-#pragma unroll
-              for (int x = 0; x < kSteps; ++x) {
-                w = M::mma(M::row(state + y * kOne + 16 * nt * kRowK + 32 * x), qf[x], w);
-                u = M::mma(M::row(state + (M::kParts + y) * kOne + 16 * nt * kRowK + 32 * x), qf[x], u);
-              }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float term = lead * fmaf(float(i_tok + 1), w[i], u[i]) * xv[nt][i];
-              sum += ((i_tok < m) & (16 * nt + 4 * quad + i < width)) ? term : 0.f;
-            }
-          }
-          decay += double(sum);
         }
       }
+      // ---- f[i+1] q S
+      if constexpr (!DEC) {
+        f32x16_h o[kIt];
+        auto before = [&] {
+#pragma unroll
+          for (int it = 0; it < kIt; ++it) o[it] = zero16();
+#pragma unroll
+          for (int y = 0; y < kSteps; ++y) {
+            const Frag sf = y % 2 ? M::template of<1>(st[y / 2]) : M::template of<0>(st[y / 2]);
+#pragma unroll
+            for (int it = 0; it < kIt; ++it) o[it] = M::mma(sf, M::row(q_row + 32 * it * kRowQ + 16 * y), o[it]);
+          }
+#pragma unroll
+          for (int it = 0; it < kIt; ++it) {
+            const float lead = inter * fade(g2, max(32 * it + il - none + r_lead, 0));
+#pragma unroll
+            for (int b = 0; b < 16; ++b) o[it][b] *= lead;
+          }
+        };
+        if (has) before();
+        __syncthreads();
+        if (tid == 0) odd[turn ^ 1] = 0;
+        if (has) {
+          // ---- the products meet v
+          const T* vt = M::col_at(lds + L::kV, kRowV, lane) + 32 * wave;
+          const T* pp = lds + L::kP + lane * 8;
+#pragma unroll
+          for (int y = 0; y < kTs; ++y) {
+            const Frag vf = M::col(vt + 16 * y * kRowV, kRowV);
+            if (y < 2) o[0] = M::mma(vf, M::row(pp + y * 512), o[0]);
+            if constexpr (kIt > 1) o[1] = M::mma(vf, M::row(pp + (y + 2) * 512), o[1]);
+          }
+          if (strange) {
+            // an infinity or NaN among the block's v meets no product of an earlier token, not even a zero one
+            before();
+#pragma unroll
+            for (int it = 0; it < kIt; ++it)
+              for (int j = 0; j < 32 * it + 32; ++j) {
+                const int jl = j % 32, pair = it + j / 32;
+                if (j > 32 * it + il) continue;
+                const float p = to_f32(lds[L::kP + ((pair * 2 + jl / 16) * 64 + jl % 16 / 8 * 32 + il) * 8 + j % 8]);
+                const T* row = lds + L::kV + j * kRowV + 32 * wave + 8 * hh;
+#pragma unroll
+                for (int b = 0; b < 16; ++b) o[it][b] = fmaf(p, to_f32(row[16 * (b / 8) + b % 8]), o[it][b]);
+              }
+          }
+          const int64_t t = o_at + first_token(p0, m) * o_row;
+#pragma unroll
+          for (int it = 0; it < kIt; ++it) {
+            const int tok = 32 * it + il - none;
+            if (tok < 0) continue;
+            const int64_t at = t + int64_t(unsigned(rev ? m - 1 - tok : tok) * uint64_t(o_row));
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              float u[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) u[i] = o[it][8 * g + i];
+              const int e = 32 * wave + 16 * g + 8 * hh;
+              if (o_f32) store_cols<float, KIND>(reinterpret_cast<float*>(o_p) + at, e, width, u);
+              else store_cols<T, KIND>(reinterpret_cast<T*>(o_p) + at, e, width, u);
+            }
+          }
+        }
+      } else {
+        // ... and x[i] . f[i+1] (S2 + (i + 1) S) do[i]
+        if (has) {
+#pragma unroll
+          for (int it = 0; it < kIt; ++it) {
+            f32x16_h u = zero16(), w = zero16();
+#pragma unroll
+            for (int y = 0; y < kSteps; ++y) {
+              const Frag qf = M::row(q_row + 32 * it * kRowQ + 16 * y);
+              Frag f[M::kParts], f2[M::kParts];
+              if (y % 2) {
+                M::template split<1>(st[y / 2], f);
+                M::template split<1>(st2[y / 2], f2);
+              } else {
+                M::template split<0>(st[y / 2], f);
+                M::template split<0>(st2[y / 2], f2);
+              }
+#pragma unroll
+              for (int part = 0; part < M::kParts; ++part) {
+                w = M::mma(f[part], qf, w);
+                u = M::mma(f2[part], qf, u);
+              }
+            }
+            const int tok = 32 * it + il - none;
+            const float lead = inter * fade(g2, max(tok + r_lead, 0)), after = float(tok + 1);
+            const T* xrow = lds + L::kX + (32 * it + il) * kRowV + 32 * wave + 8 * hh;
+#pragma unroll
+            for (int b = 0; b < 16; ++b) {
+              const float term = lead * fmaf(after, w[b], u[b]) * to_f32(xrow[16 * (b / 8) + b % 8]);
+              sum += ((tok >= 0) & (32 * wave + 16 * (b / 8) + 8 * hh + b % 8 < width)) ? term : 0.f;
+            }
+          }
+        }
+        decay += double(sum);
+      }
     }
+    if (!(more || keeps)) break;  // (for all threads of the workgroup)
 
-    // ---- the state after the block
-    if (keeps || p0 + kTok < end) {
-      const float m1 = m == kTok ? whole_m1 : fade_m1(g, m);
-      const T* kt = M::col_at(lds + L::kK, kRowK, lane);
-      const T* ft = M::col_at(lds + L::kF, kRowV, lane);
-      constexpr int kOne = kTok * kRowV;
+    // ---- the state after the block, 16 tokens at a time
+    if (has) {
+      const float m1 = m == TOK ? whole_m1 : last_m1;
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (DEC) {
-              const float both = fmaf(float(m), st[mt][nt][i], st2[mt][nt][i]);
-              st2[mt][nt][i] = fmaf(both, m1, both);
-            }
-            st[mt][nt][i] = fmaf(st[mt][nt][i], m1, st[mt][nt][i]);
+        for (int b = 0; b < 16; ++b) {
+          if constexpr (DEC) {
+            const float both = fmaf(float(m), st[mt][b], st2[mt][b]);
+            st2[mt][b] = fmaf(both, m1, both);
           }
+          st[mt][b] = fmaf(st[mt][b], m1, st[mt][b]);
+        }
+      const T* kt = M::col_at(lds + L::kK, kRowK, lane);
+      const T* vt = M::col_at(lds + L::kV, kRowV, lane) + 32 * wave;
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        if (32 * y < m) {
-          Frag kf[kMt];
+      for (int y = 0; y < kTs; ++y) {
+        const Frag vf = M::col(vt + 16 * y * kRowV, kRowV);
+        float fy[8];
 #pragma unroll
-          for (int mt = 0; mt < kMt; ++mt) kf[mt] = M::col(kt + 32 * y * kRowK + 16 * (wave * kMt + mt), kRowK);
+        for (int i = 0; i < 8; ++i) fy[i] = fq[i] * (f_step[kTs - 1 - y] * f_last);
+        Frag f[M::kParts], f2[M::kParts];
+        M::scaled(vf, fy, f);
+        if constexpr (DEC) {
 #pragma unroll
-          for (int nt = 0; nt < kNt; ++nt)
+          for (int i = 0; i < 8; ++i) fy[i] *= float(TOK - 1 - (16 * y + 8 * hh + i));
+          M::scaled(vf, fy, f2);
+        }
 #pragma unroll
-            for (int part = 0; part < M::kParts; ++part) {
-              const Frag f = M::col(ft + part * kOne + 32 * y * kRowV + 16 * nt, kRowV);
+        for (int mt = 0; mt < kMt; ++mt) {
+          const Frag kf = M::col(kt + 16 * y * kRowK + 32 * mt, kRowK);
 #pragma unroll
-              for (int mt = 0; mt < kMt; ++mt) st[mt][nt] = M::mma(kf[mt], f, st[mt][nt]);
-              if constexpr (DEC) {
-                const Frag f2 = M::col(ft + (M::kParts + part) * kOne + 32 * y * kRowV + 16 * nt, kRowV);
-#pragma unroll
-                for (int mt = 0; mt < kMt; ++mt) st2[mt][nt] = M::mma(kf[mt], f2, st2[mt][nt]);
-              }
-            }
+          for (int part = 0; part < M::kParts; ++part) {
+            st[mt] = M::mma(kf, f[part], st[mt]);
+            if constexpr (DEC) st2[mt] = M::mma(kf, f2[part], st2[mt]);
+          }
         }
       }
     }
     __syncthreads();
-    if (p0 + kTok < end) put_state();
+    if (!OUT || DEC) {
+      if (tid == 0) odd[turn ^ 1] = 0;  // (unused there)
+    }
   }
 
   // ---- what is left behind: the state, zeros for the tokens that are not valid, the decay's sum
   float* to = nullptr;
   if constexpr (OUT) to = keeps && r.to ? r.to + nh * size : nullptr;
   else to = r.segs + (nh * (a.segs - 1) + s) * size;
-  if (to) each_state([&](int mt, int nt, int c, int e) { store_state(to, c, e, st[mt][nt]); });
+  if (to && has) store_state(to, st);
   if constexpr (DEC && !OUT) {
-    float* to2 = a.segs2 + (nh * (a.segs - 1) + s) * size;
-    each_state([&](int mt, int nt, int c, int e) { store_state(to2, c, e, st2[mt][nt]); });
+    if (has) store_state(a.segs2 + (nh * (a.segs - 1) + s) * size, st2);
   }
   if constexpr (OUT && !DEC) {
     const int last = min(begin + a.seg, a.t);
-    for (int t = max(begin, len) + tid / kCols; t < last; t += cc3d::kLinThreads / kCols) {
-      const int e = tid % kCols;
+    for (int t = max(begin, len) + tid / CB; t < last; t += kThreads / CB) {
+      const int e = tid % CB;
       const int64_t place = o_at + int64_t(t) * o_row + e;
       if (e < width) {
         if (o_f32) reinterpret_cast<float*>(o_p)[place] = 0.f;
@@ -729,20 +799,23 @@ __global__ __launch_bounds__(cc3d::kLinThreads, DEC || sizeof(T) == 4 || DP == 2
       }
     }
   }
-  if constexpr (OUT && DEC) {
-    if (keeps) {
-      const float* dto = a.dto + nh * size;
-      each_state([&](int mt, int nt, int c, int e) {
-        const f32x4_s v = load_state(dto, c, e);
+  if constexpr (kGrad) {
+    if (keeps && has) {
+      f32x16_h d[kMt];
+      load_state(a.dto + nh * size, d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) decay += ((c + i < c_all) & (e < width)) ? double(v[i]) * double(st2[mt][nt][i]) : 0.0;
-      });
+      for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+        for (int b = 0; b < 16; ++b) {
+          const int c = 32 * mt + 16 * (b / 8) + 8 * hh + b % 8;
+          decay += ((c < c_all) & (col < width)) ? double(d[mt][b]) * double(st2[mt][b]) : 0.0;
+        }
     }
-    double* box = reinterpret_cast<double*>(smem);  // (the last barrier above is behind every read of the tiles)
+    double* box = reinterpret_cast<double*>(smem);
     __syncthreads();
     box[tid] = decay;
     __syncthreads();
-    for (int half = cc3d::kLinThreads / 2; half > 0; half /= 2) {
+    for (int half = kThreads / 2; half > 0; half /= 2) {
       if (tid < half) box[tid] += box[tid + half];
       __syncthreads();
     }
@@ -750,37 +823,45 @@ __global__ __launch_bounds__(cc3d::kLinThreads, DEC || sizeof(T) == 4 || DP == 2
   }
 }
 
-template <class T, int DP, int KIND, bool OUT, bool DEC>
+template <class T, int DP, int CB, int KIND, bool OUT, bool DEC>
 int start_run(const LinArgs& a, int64_t workgroups, hipStream_t s) {
-  constexpr int lds = LinTiles<T, DP, OUT, DEC>::kBytes;
+  constexpr int lds = LinTiles<T, DP, CB, cc3d::linear_tokens(sizeof(T), DP), OUT, DEC>::kBytes;
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear_run<T, DP, KIND, OUT, DEC>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear_run<T, DP, CB, KIND, OUT, DEC>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) {
       (void)hipGetLastError();
       return int(e);
     }
   }
-  return launch(linear_run<T, DP, KIND, OUT, DEC>, workgroups, cc3d::kLinThreads, lds, s, a);
+  return launch(linear_run<T, DP, CB, KIND, OUT, DEC>, workgroups, 2 * CB, lds, s, a);
 }
 
 template <class T, int KIND>
 int start_runs(LinArgs& a, int pad, bool out, bool dec, hipStream_t s) {
   const int starts = out ? a.segs : a.segs - 1;
+  int widest = 0;
+  for (int i = 0; i < a.runs; ++i) widest = std::max(widest, a.run[i].e);
+  const int cols = cc3d::linear_cols(widest);
   a.parts = 0;
-  for (int i = 0; i < a.runs; ++i) a.parts += a.run[i].blocks = int(cc3d::linear_blocks(a.run[i].e, pad));
+  for (int i = 0; i < a.runs; ++i) a.parts += a.run[i].blocks = (a.run[i].e + cols - 1) / cols;
   a.units = unsigned(int64_t(a.n) * a.heads * starts);
   if (a.units == 0) return 0;
   const int64_t workgroups = (int64_t(a.units) + 7) / 8 * 8 * a.parts;
-  auto go = [&](auto d) {
-    constexpr int DP = decltype(d)::value;
+  auto go = [&](auto d, auto c) {
+    constexpr int DP = decltype(d)::value, CB = decltype(c)::value;
     if (out)
-      return dec ? start_run<T, DP, KIND, true, true>(a, workgroups, s) : start_run<T, DP, KIND, true, false>(a, workgroups, s);
-    return dec ? start_run<T, DP, KIND, false, true>(a, workgroups, s) : start_run<T, DP, KIND, false, false>(a, workgroups, s);
+      return dec ? start_run<T, DP, CB, KIND, true, true>(a, workgroups, s)
+                 : start_run<T, DP, CB, KIND, true, false>(a, workgroups, s);
+    return dec ? start_run<T, DP, CB, KIND, false, true>(a, workgroups, s)
+               : start_run<T, DP, CB, KIND, false, false>(a, workgroups, s);
   };
-  if (pad == 64) return go(std::integral_constant<int, 64>());
-  if (pad == 128) return go(std::integral_constant<int, 128>());
-  return go(std::integral_constant<int, 256>());
+  const std::integral_constant<int, 64> c64;
+  const std::integral_constant<int, 128> c128;
+  const std::integral_constant<int, 256> c256;
+  if (pad == 64) return cols == 64 ? go(c64, c64) : go(c64, c128);
+  if (pad == 128) return cols == 64 ? go(c128, c64) : go(c128, c128);
+  return cols == 64 ? go(c256, c64) : go(c256, c128);
 }
 
 }  // namespace

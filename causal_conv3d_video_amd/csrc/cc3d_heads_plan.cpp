@@ -16,6 +16,10 @@ bool within_span(std::initializer_list<int64_t> sizes) {
   return true;
 }
 
+// Elements between two tokens of linear attention: places inside 64 tokens are
+// 32 bits of bytes.
+constexpr int64_t kMaxHeadRow = (int64_t(1) << 24) - 1;
+
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
 }  // namespace
@@ -51,15 +55,16 @@ extern "C" cc3d_status_t linear_attention_plan(const cc3d_linear_desc_t* d, cc3d
   if (!within_span({d->n, d->t, d->heads, widest}) || !within_span({d->n, d->heads, d->dk, d->dv}))
     return refuse(CC3D_ERR_UNSUPPORTED);
   const int64_t nh = int64_t(d->n) * d->heads;
-  const int64_t blocks = cc3d::linear_blocks(d->dv, cc3d::linear_pad(d->dk)), units = nh * blocks;
+  const int64_t blocks = cc3d::linear_blocks(d->dv, cc3d::linear_cols(d->dv)), units = nh * blocks;
+  const int64_t short_units = nh * cc3d::linear_blocks(d->dv, 64);
   // (heads are rounded up to eight, one for each die)
-  if (!cc3d::fits(units + 7 * blocks, cc3d::kLinThreads)) return refuse(CC3D_ERR_UNSUPPORTED);
+  if (!cc3d::fits(units + 7 * blocks, cc3d::kLinThreads) || !cc3d::fits(short_units, cc3d::kLinThreads)) return refuse(CC3D_ERR_UNSUPPORTED);
   auto* p = make_plan<cc3d_linear_plan>(d);
   if (!p) return CC3D_ERR_NO_MEMORY;
-  if (d->t > cc3d::kLinShort) split_time(d->t, units, 2 * kUnits, &p->seg, &p->segs);
-  const int pad = cc3d::linear_pad(int(widest));
+  if (d->t > cc3d::kLinShort) split_time(d->t, units, kUnits, &p->seg, &p->segs);
+  const int cols = cc3d::linear_cols(int(widest));
   // Backward: the recurrence with the fewest workgroups (the decay's is one by itself) once over the compute units.
-  const int64_t of_k = cc3d::linear_blocks(d->dk, pad), of_v = cc3d::linear_blocks(d->dv, pad);
+  const int64_t of_k = cc3d::linear_blocks(d->dk, cols), of_v = cc3d::linear_blocks(d->dv, cols);
   split_time(d->t, nh * of_k, kUnits, &p->bwd_seg, &p->bwd_segs);
   p->bwd_fits = cc3d::fits((nh + 7) * (2 * of_k + of_v), cc3d::kLinThreads);  // (where it is split it is far below)
   p->info.chunks = p->segs;
@@ -89,6 +94,14 @@ void linear_inputs(Check& c, const cc3d_linear_desc_t& d, const cc3d_linear_args
 }
 }  // namespace
 
+namespace {
+bool far_heads(const cc3d_linear_desc_t& d, std::initializer_list<const cc3d_rows_t*> views) {
+  for (const cc3d_rows_t* v : views)
+    if (d.t > 1 && v->p && v->row > kMaxHeadRow) return true;
+  return false;
+}
+}  // namespace
+
 extern "C" cc3d_status_t linear_attention_forward(cc3d_linear_plan_t p, const cc3d_linear_args_t* a, void* stream) {
   if (!p || !a) return refuse(CC3D_ERR_INVALID_ARG);
   const auto& d = p->d;
@@ -99,6 +112,7 @@ extern "C" cc3d_status_t linear_attention_forward(cc3d_linear_plan_t p, const cc
   c.same_allowed(a->h_in, a->h_out);
   c.workspace(a->workspace, a->workspace_bytes, p->info.workspace_bytes);
   if (!c.ok()) return refuse(CC3D_ERR_INVALID_ARG);
+  if (far_heads(d, {&a->q, &a->k, &a->v, &a->o})) return refuse(CC3D_ERR_UNSUPPORTED);
   return launched(cc3d::launch_linear_forward(*p, *a, stream));
 }
 
@@ -118,7 +132,8 @@ extern "C" cc3d_status_t linear_attention_backward(cc3d_linear_plan_t p, const c
   c.require(!a->dlog_decay || a->log_decay);
   c.workspace(a->workspace, a->workspace_bytes, p->info.backward_workspace_bytes);
   if (!c.ok()) return refuse(CC3D_ERR_INVALID_ARG);
-  if (!p->bwd_fits) return refuse(CC3D_ERR_UNSUPPORTED);
+  if (!p->bwd_fits || far_heads(d, {&a->q, &a->k, &a->v, &a->grad_o, &a->dq, &a->dk, &a->dv}))
+    return refuse(CC3D_ERR_UNSUPPORTED);
   return launched(cc3d::launch_linear_backward(*p, *a, stream));
 }
 

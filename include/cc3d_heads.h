@@ -46,7 +46,8 @@ extern "C" {
  *   dlog_decay = sum over sequences and tokens of <G[t], exp(log_decay) S[t-1]>
  * Gradients of shared heads are sums over the heads that share them.  The
  * states are computed again from h_in; nothing is kept by the forward call.
- * Any gradient may be left out.
+ * Any gradient may be left out.  Views whose tokens are 2^24 elements or more
+ * apart are refused as unsupported (but with T = 1).
  *
  * Tokens are taken 64 at a time with matrix products.  With bf16 tensors the
  * products of a token's q with the k of its 64 (and with the state before them)
