@@ -46,7 +46,8 @@ inline int64_t linear_blocks(int width, int cols) { return (width + cols - 1) / 
 
 // Parts of the backward call's workspace, in floats, in this order.
 struct LinearSpace {
-  int64_t state;    // one set of segments' states
+  int64_t state;    // one set of segments' states (there are two)
+  int64_t blocks;   // each block's state before it, as registers hold it: for the decay's gradient
   int64_t dq, dk, dv;  // sums of shared heads, before they are joined; 0 where no head is shared
   int64_t decay;    // partial sums of dlog_decay
   int64_t total;
@@ -60,8 +61,11 @@ inline LinearSpace linear_bwd_space(const cc3d_linear_plan& p) {
   s.dq = d.q_heads == d.heads ? 0 : up(el * d.dk);
   s.dk = d.k_heads == d.heads ? 0 : up(el * d.dk);
   s.dv = d.v_heads == d.heads ? 0 : up(el * d.dv);
-  s.decay = up(2 * nh * p.bwd_segs * linear_blocks(d.dk, linear_cols(d.dk)));  // (64 bits each)
-  s.total = 3 * s.state + s.dq + s.dk + s.dv + s.decay;
+  const int pad = linear_pad(d.dk > d.dv ? d.dk : d.dv), cols = linear_cols(d.dk);
+  const int64_t tokens = linear_tokens(d.dtype == CC3D_BF16 ? 2 : 4, pad);
+  s.blocks = nh * ((d.t + tokens - 1) / tokens) * linear_blocks(d.dk, cols) * pad * cols;
+  s.decay = up(2 * 2 * nh * p.bwd_segs * linear_blocks(d.dk, cols));  // (two recurrences, 64 bits each)
+  s.total = 2 * s.state + s.blocks + s.dq + s.dk + s.dv + s.decay;
   return s;
 }
 

@@ -41,6 +41,18 @@
 // fp32 result and is carried.  The decay's gradient, fp32 too, takes the state
 // as two bf16 as well and multiplies both products of its pairs in fp32.  fp32 tensors
 // use the fp32 matrix products throughout.
+//
+// The decay's gradient is the sum over all blocks of what depends on g there, S the
+// state before the block and G the gradient of the state behind it:
+//
+//   sum over i > j of (i-j) f[i-j] scale (q[i] . k[j]) (do[i] . v[j])  +
+//   sum over i of (i+1) f[i+1] scale q[i] S do[i]  +  m f[m] <S, G>  +  sum over j of (m-1-j) f[m-1-j] k[j] G v[j]
+//
+// The first two fall out of dq's recurrence, the last out of dk's; for <S, G> dq's
+// leaves every block's S behind, as its registers hold it, and dk's, which has the
+// same rows of tokens in reverse, reads it.  (The derivative of the state carried
+// along beside it, which needs neither, doubles the products and the registers: 170 of
+// 240 us of a backward pass of 2 by 2049 tokens.)
 #pragma once
 #include <algorithm>
 
@@ -62,9 +74,16 @@ struct LinRun {
   int lead;                                  // 1: the state before a block meets its token i as f[i+1]; 0: as f[i]
   int o_f32;                                 // o is fp32 whatever T
   float score, inter, update;                // factors of the three sums
-  const float* from;                         // state before the first token, or null
-  float* to;                                 // after the last valid one, or null
-  float* segs;                               // [N][H][segments - 1]: states before segments 1, 2, ...
+  const float* from;                         // state before the first token (reversed: behind the last), or null
+  float* to;                                 // after the last valid one (reversed: before the first), or null
+  float* segs;                               // [N][H][segments - 1]: states between segments
+  // with the decay's gradient: rows that the part of the state that came in meets; whether pairs count here
+  const void* x;
+  int64_t xb, xr;
+  int xper, pairs;
+  float* put;        // each block's state before it, as registers hold it
+  const float* get;  // the same of another recurrence, which meets this one's
+  double* part;      // [N][H][segments][blocks]
 };
 
 struct LinArgs {
@@ -74,18 +93,11 @@ struct LinArgs {
   int n, heads, t, seg, segs;
   const float* log_decay;
   const int* lengths;
-  // the decay's gradient (of run[0], dq's): the derivative of the states by the decay, q itself, dh_out
-  float* segs2;
-  const void* x;
-  int64_t xb, xr;
-  int xper;
-  const float* dto;
-  double* part;  // [N][H][segments][blocks]
 };
 
 // Runs of one type and kind of widths (cc3d_heads_linear_*.hip).  out: with
 // outputs, else what each segment adds to the state; dec: with the decay's
-// derivative.
+// gradient.
 using LinStart = int(LinArgs& a, int pad, bool out, bool dec, hipStream_t s);
 LinStart linear_bf16_eights, linear_bf16_rest, linear_bf16_less, linear_f32_eights, linear_f32_rest, linear_f32_less;
 
@@ -368,20 +380,20 @@ struct LinTiles {
   static constexpr int kRowQ = DP + M::kPad, kRowK = DP + M::pad_both(DP), kRowV = CB + M::pad_both(CB);
   static constexpr int kK = 0, kV = kK + TOK * kRowK, kQ = kV + TOK * kRowV, kP = kQ + (OUT ? TOK * kRowQ : 0);
   static constexpr int kPairs = TOK == 64 ? 3 : 1;  // tiles of 32 by 32 pairs of tokens
-  static constexpr int kX = kP + (OUT && !DEC ? kPairs * 2 * 64 * 8 : 0);
-  static constexpr int kTotal = kX + (OUT && DEC ? TOK * kRowV : 0);
+  static constexpr int kX = kP + (OUT ? kPairs * 2 * 64 * 8 : 0);
+  static constexpr int kTotal = kX + (DEC ? TOK * kRowV : 0);
   static constexpr int kBytes = kTotal * int(sizeof(T)) > 4096 ? kTotal * int(sizeof(T)) : 4096;
 };
 
-// Waves a SIMD that the registers are held to: two workgroups a compute unit where
-// their tiles and the state allow.
-template <class T, int DP, bool DEC>
+// Waves a SIMD that the registers are held to: what the tiles let a compute unit
+// hold, where the state allows it.
+template <class T, int DP, int CB>
 constexpr int linear_waves() {
-  return sizeof(T) == 2 && DP <= 128 && !DEC ? 2 : 1;
+  return sizeof(T) == 2 && (DP == 64 || (DP == 128 && CB == 128)) ? 2 : 1;
 }
 
 template <class T, int DP, int CB, int KIND, bool OUT, bool DEC>
-__global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_run(LinArgs a) {
+__global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_run(LinArgs a) {
   using M = Mat<T>;
   using Frag = typename M::Frag;
   constexpr int TOK = cc3d::linear_tokens(sizeof(T), DP);  // tokens of a block
@@ -390,7 +402,6 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_r
   constexpr int kMt = DP / 32, kSteps = DP / 16, kIt = TOK / 32, kTs = TOK / 16;  // tiles and steps of C, of the tokens
   constexpr int kVecK = TOK * DP / 8 / kThreads, kVecV = TOK * CB / 8 / kThreads;  // eights that a thread stages
   constexpr int kStepK = kThreads / (DP / 8), kStepV = kThreads / (CB / 8);
-  constexpr bool kGrad = DEC && OUT;
   static_assert(kVecK * kThreads * 8 == TOK * DP && kVecV * kThreads * 8 == TOK * CB, "threads");
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ int odd[2];  // a block of k or v holds an infinity or NaN
@@ -407,11 +418,9 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_r
   if (unit >= a.units) return;
   const LinRun& r = a.run[which];
   const int blocks = r.blocks;
-  const int turned = int(unit % starts);
+  const int s = pin(int(unit % starts) + (!OUT && r.rev ? 1 : 0));
   unit /= starts;
   const int h = pin(int(unit % a.heads)), n = pin(int(unit / a.heads));
-  // (a reversed recurrence of the same rows is at the other end of its segments)
-  const int s = pin(OUT && r.rev ? starts - 1 - turned : turned);
   const int64_t nh = int64_t(n) * a.heads + h;
   const int e0 = block * CB;
   const int len = pin(valid_tokens(a.lengths, n, a.t));
@@ -426,21 +435,22 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_r
   const T* k = pin(static_cast<const T*>(r.k) + n * r.kb + int64_t(h / r.kper) * r.c - kBias);
   const T* v = pin(static_cast<const T*>(r.v) + n * r.vb + int64_t(h / r.vper) * r.e + e0 - kBias);
   const T* x = nullptr;
-  if constexpr (kGrad) x = pin(static_cast<const T*>(a.x) + n * a.xb + int64_t(h / a.xper) * r.e + e0 - kBias);
-  const int qr = pin(int(r.qr)), kr = pin(int(r.kr)), vr = pin(int(r.vr)), o_row = pin(int(r.orow)), xr = kGrad ? pin(int(a.xr)) : 0;
+  if constexpr (DEC) x = pin(static_cast<const T*>(r.x) + n * r.xb + int64_t(h / r.xper) * r.e + e0 - kBias);
+  const int qr = pin(int(r.qr)), kr = pin(int(r.kr)), vr = pin(int(r.vr)), o_row = pin(int(r.orow)), xr = DEC ? pin(int(r.xr)) : 0;
   char* o_p = pin(static_cast<char*>(r.o));
   const int64_t o_at = pin(n * r.ob + int64_t(h) * r.e + e0);
-  const int o_f32 = pin(r.o_f32);
+  const int o_f32 = pin(r.o_f32), pairs = DEC ? pin(r.pairs) : 0;
+  float* put = DEC ? pin(r.put) : nullptr;
+  const float* get = DEC ? pin(r.get) : nullptr;
   auto by = [](const T* p, unsigned bytes) { return reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + bytes); };
-  auto first_token = [&](int p0, int m) { return int64_t(rev ? len - p0 - m : p0); };
 
   // ---- rows of a block in flight.  A block of m < TOK tokens has them as its last rows, behind rows of zeros.
-  Raw8<T> kn[kVecK], vn[kVecV], qn[OUT ? kVecK : 1], xn[kGrad ? kVecV : 1];
+  Raw8<T> kn[kVecK], vn[kVecV], qn[OUT ? kVecK : 1], xn[DEC ? kVecV : 1];
   const int krow = tid / (DP / 8), kcol = tid % (DP / 8) * 8, vrow = tid / (CB / 8), vcol = tid % (CB / 8) * 8;
   const Cols8<T, KIND> kc(kcol, c_all), vc(vcol, width);
   auto fetch = [&](int p0) {
     const int m = min(TOK, end - p0);
-    const int64_t t = first_token(p0, m);
+    const int64_t t = p0;
     const T *kb = k + t * kr, *vb = v + t * vr;
     auto place_of = [&](int j, int stride, const Cols8<T, KIND>& c) {
       const int tok = max(j - (TOK - m), 0);
@@ -455,16 +465,18 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_r
 #pragma unroll
       for (int y = 0; y < kVecK; ++y) qn[y] = kc.load(by(qb, place_of(krow + y * kStepK, qr, kc)), c_all);
     }
-    if constexpr (kGrad) {
+    if constexpr (DEC) {
       const T* xb = x + t * xr;
 #pragma unroll
       for (int y = 0; y < kVecV; ++y) xn[y] = vc.load(by(xb, place_of(vrow + y * kStepV, xr, vc)), width);
     }
   };
-  if (begin < end) fetch(begin);
+  // blocks of the segment's tokens, from the last one where time is reversed
+  const int count = (max(end - begin, 0) + TOK - 1) / TOK, first = begin + (rev ? (count - 1) * TOK : 0), step = rev ? -TOK : TOK;
+  if (count > 0) fetch(first);
 
   // ---- the state before the segment: result i of tile mt is c = 32 mt + 16 (i / 8) + 8 hh + i % 8 of the lane's column
-  f32x16_h st[kMt], st2[DEC ? kMt : 1];
+  f32x16_h st[kMt];
   const int col = 32 * wave + place(il);  // of the lane
   const bool has = 32 * wave < width;     // the wave has columns
   // (unconditional loads, for the same reason as those of the rows)
@@ -522,27 +534,21 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_r
   };
   const int64_t size = int64_t(r.c) * r.e;
   const float* from = nullptr;
-  if constexpr (OUT) from = s > 0 ? r.segs + (nh * (a.segs - 1) + s - 1) * size : r.from ? r.from + nh * size : nullptr;
+  const int slot = rev ? s : s - 1;  // of the state before the segment
+  if constexpr (OUT)
+    from = slot >= 0 && slot < a.segs - 1 ? r.segs + (nh * (a.segs - 1) + slot) * size : r.from ? r.from + nh * size : nullptr;
   if (from && has) {
     load_state(from, st);
   } else {
 #pragma unroll
     for (int mt = 0; mt < kMt; ++mt) st[mt] = zero16();
   }
-  if constexpr (DEC) {
-    if (OUT && s > 0 && has) {
-      load_state(a.segs2 + (nh * (a.segs - 1) + s - 1) * size, st2);
-    } else {
-#pragma unroll
-      for (int mt = 0; mt < kMt; ++mt) st2[mt] = zero16();
-    }
-  }
 
   // ---- factors, all of them f of a number of tokens, never of less than none.  Token j of a block (from its end)
   // adds f[TOK-1-j] = f[16 (TOK/16-1-j/16)] f[15-j%16], and tokens i of the second tile and j of the first are
   // f[il+1] f[31-jl] apart: a few by step, in scalar registers, times a few by lane.
   const float g = a.log_decay ? a.log_decay[h] : 0.f, g2 = g * kLog2e;
-  const float whole_m1 = pin(fade_m1(g, TOK)), last_m1 = begin < end ? pin(fade_m1(g, (end - begin - 1) % TOK + 1)) : 0.f;
+  const float whole_m1 = pin(fade_m1(g, TOK)), last_m1 = count > 0 ? pin(fade_m1(g, (end - begin - 1) % TOK + 1)) : 0.f;
   float fq[8], diag[OUT ? 16 : 1], f_lane = 0.f, f_step[kTs];
 #pragma unroll
   for (int b = 0; b < 8; ++b) fq[b] = fade(g2, 15 - 8 * hh - b);
@@ -558,11 +564,11 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_r
   __syncthreads();
 
   double decay = 0.0;
-  const bool keeps = OUT ? s + 1 == a.segs && (r.to || (DEC && a.dto)) : true;  // the state after the segment is asked for
+  const bool keeps = OUT ? (rev ? s == 0 : s + 1 == a.segs) && r.to : true;  // the state after the segment is asked for
   int turn = 0;
-  for (int p0 = begin; p0 < end; p0 += TOK, turn ^= 1) {
+  for (int b0 = 0, p0 = first; b0 < count; ++b0, p0 += step, turn ^= 1) {
     const int m = min(TOK, end - p0), none = TOK - m;
-    const bool more = p0 + TOK < end;
+    const bool more = b0 + 1 < count;
     // (what follows from these is cheap, and would be kept in registers over all blocks)
     asm volatile("" : "+v"(fq[0]), "+v"(fq[1]), "+v"(fq[2]), "+v"(fq[3]), "+v"(fq[4]), "+v"(fq[5]), "+v"(fq[6]), "+v"(fq[7]));
     // ---- stage the rows
@@ -585,14 +591,14 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_r
       if (!whole) vn[y] = vc.finish(vn[y], j >= none, width);
       full |= M::full(vn[y]);
       M::put(lds + L::kV + j * kRowV + vcol, vn[y]);
-      if constexpr (kGrad) {
+      if constexpr (DEC) {
         if (!whole) xn[y] = vc.finish(xn[y], j >= none, width);
         M::put(lds + L::kX + j * kRowV + vcol, xn[y]);
       }
     }
-    if (full) odd[turn] = 1;
+    if (OUT && full) odd[turn] = 1;
     __syncthreads();
-    if (more) fetch(p0 + TOK);
+    if (more) fetch(p0 + step);
     const bool strange = pin(odd[turn]) != 0;
 
     const T* q_row = lds + L::kQ + il * kRowQ + 8 * hh;
@@ -615,122 +621,130 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_r
 #pragma unroll
           for (int b = 0; b < 16; ++b) pr[b] = 16 * (b / 8) + 8 * hh + b % 8 <= il ? pr[b] * diag[b] : 0.f;
         }
-        if constexpr (!DEC) {
-          T* at = lds + L::kP + (pair * 128 + lane) * 8;
-          M::put(at, M::template of<0>(pr));
-          M::put(at + 512, M::template of<1>(pr));
-        } else {
-          // the decay's gradient: with x the rows of q, (i - j) f[i-j] (do[i] . v[j]) (x[i] . k[j]) of every pair (of
-          // these columns of x and k)
-          f32x16_h xk = zero16();
-          const T *vp = lds + L::kV + (32 * jt + place(il)) * kRowV + 8 * hh, *xp = lds + L::kX + (32 * it + il) * kRowV + 8 * hh;
+        T* at = lds + L::kP + (pair * 128 + lane) * 8;
+        M::put(at, M::template of<0>(pr));
+        M::put(at + 512, M::template of<1>(pr));
+        if constexpr (DEC) {
+          // the decay's gradient: (i - j) f[i-j] (q[i] . k[j]) (x[i] . v[j]) of every pair (of these columns of x and v)
+          if (pairs) {
+            f32x16_h xv = zero16();
+            const T *vp = lds + L::kV + (32 * jt + place(il)) * kRowV + 8 * hh, *xp = lds + L::kX + (32 * it + il) * kRowV + 8 * hh;
 #pragma unroll
-          for (int y = 0; y < CB / 16; ++y) xk = M::mma(M::row(vp + 16 * y), M::row(xp + 16 * y), xk);
+            for (int y = 0; y < CB / 16; ++y) xv = M::mma(M::row(vp + 16 * y), M::row(xp + 16 * y), xv);
 #pragma unroll
-          for (int b = 0; b < 16; ++b) {
-            const int d = 32 * (it - jt) + il - (16 * (b / 8) + 8 * hh + b % 8);
-            const float term = float(d) * pr[b] * xk[b];
-            sum += d > 0 ? term : 0.f;
+            for (int b = 0; b < 16; ++b) {
+              const int d = 32 * (it - jt) + il - (16 * (b / 8) + 8 * hh + b % 8);
+              const float term = float(d) * pr[b] * xv[b];
+              sum += d > 0 ? term : 0.f;
+            }
           }
         }
       }
       // ---- f[i+1] q S
-      if constexpr (!DEC) {
-        f32x16_h o[kIt];
-        auto before = [&] {
+      f32x16_h o[kIt];
+      auto before = [&] {
 #pragma unroll
-          for (int it = 0; it < kIt; ++it) o[it] = zero16();
+        for (int it = 0; it < kIt; ++it) o[it] = zero16();
 #pragma unroll
-          for (int y = 0; y < kSteps; ++y) {
-            const Frag sf = y % 2 ? M::template of<1>(st[y / 2]) : M::template of<0>(st[y / 2]);
-#pragma unroll
-            for (int it = 0; it < kIt; ++it) o[it] = M::mma(sf, M::row(q_row + 32 * it * kRowQ + 16 * y), o[it]);
+        for (int y = 0; y < kSteps; ++y) {
+          Frag sf[M::kParts];
+          if constexpr (DEC) {
+            if (y % 2) M::template split<1>(st[y / 2], sf);
+            else M::template split<0>(st[y / 2], sf);
+          } else {
+            sf[0] = y % 2 ? M::template of<1>(st[y / 2]) : M::template of<0>(st[y / 2]);
           }
 #pragma unroll
-          for (int it = 0; it < kIt; ++it) {
-            const float lead = inter * fade(g2, max(32 * it + il - none + r_lead, 0));
+          for (int part = 0; part < (DEC ? M::kParts : 1); ++part)
 #pragma unroll
-            for (int b = 0; b < 16; ++b) o[it][b] *= lead;
-          }
-        };
-        if (has) before();
-        __syncthreads();
-        if (tid == 0) odd[turn ^ 1] = 0;
-        if (has) {
-          // ---- the products meet v
-          const T* vt = M::col_at(lds + L::kV, kRowV, lane) + 32 * wave;
-          const T* pp = lds + L::kP + lane * 8;
-#pragma unroll
-          for (int y = 0; y < kTs; ++y) {
-            const Frag vf = M::col(vt + 16 * y * kRowV, kRowV);
-            if (y < 2) o[0] = M::mma(vf, M::row(pp + y * 512), o[0]);
-            if constexpr (kIt > 1) o[1] = M::mma(vf, M::row(pp + (y + 2) * 512), o[1]);
-          }
-          if (strange) {
-            // an infinity or NaN among the block's v meets no product of an earlier token, not even a zero one
-            before();
-#pragma unroll
-            for (int it = 0; it < kIt; ++it)
-              for (int j = 0; j < 32 * it + 32; ++j) {
-                const int jl = j % 32, pair = it + j / 32;
-                if (j > 32 * it + il) continue;
-                const float p = to_f32(lds[L::kP + ((pair * 2 + jl / 16) * 64 + jl % 16 / 8 * 32 + il) * 8 + j % 8]);
-                const T* row = lds + L::kV + j * kRowV + 32 * wave + 8 * hh;
-#pragma unroll
-                for (int b = 0; b < 16; ++b) o[it][b] = fmaf(p, to_f32(row[16 * (b / 8) + b % 8]), o[it][b]);
-              }
-          }
-          const int64_t t = o_at + first_token(p0, m) * o_row;
-#pragma unroll
-          for (int it = 0; it < kIt; ++it) {
-            const int tok = 32 * it + il - none;
-            if (tok < 0) continue;
-            const int64_t at = t + int64_t(unsigned(rev ? m - 1 - tok : tok) * uint64_t(o_row));
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              float u[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) u[i] = o[it][8 * g + i];
-              const int e = 32 * wave + 16 * g + 8 * hh;
-              if (o_f32) store_cols<float, KIND>(reinterpret_cast<float*>(o_p) + at, e, width, u);
-              else store_cols<T, KIND>(reinterpret_cast<T*>(o_p) + at, e, width, u);
-            }
-          }
+            for (int it = 0; it < kIt; ++it) o[it] = M::mma(sf[part], M::row(q_row + 32 * it * kRowQ + 16 * y), o[it]);
         }
-      } else {
-        // ... and x[i] . f[i+1] (S2 + (i + 1) S) do[i]
+#pragma unroll
+        for (int it = 0; it < kIt; ++it) {
+          const float lead = inter * fade(g2, max(32 * it + il - none + r_lead, 0));
+#pragma unroll
+          for (int b = 0; b < 16; ++b) o[it][b] *= lead;
+        }
+      };
+      if (has) before();
+      if constexpr (DEC) {
+        // ... what came in, by the tokens since; and the state that another recurrence had here
         if (has) {
 #pragma unroll
           for (int it = 0; it < kIt; ++it) {
-            f32x16_h u = zero16(), w = zero16();
-#pragma unroll
-            for (int y = 0; y < kSteps; ++y) {
-              const Frag qf = M::row(q_row + 32 * it * kRowQ + 16 * y);
-              Frag f[M::kParts], f2[M::kParts];
-              if (y % 2) {
-                M::template split<1>(st[y / 2], f);
-                M::template split<1>(st2[y / 2], f2);
-              } else {
-                M::template split<0>(st[y / 2], f);
-                M::template split<0>(st2[y / 2], f2);
-              }
-#pragma unroll
-              for (int part = 0; part < M::kParts; ++part) {
-                w = M::mma(f[part], qf, w);
-                u = M::mma(f2[part], qf, u);
-              }
-            }
-            const int tok = 32 * it + il - none;
-            const float lead = inter * fade(g2, max(tok + r_lead, 0)), after = float(tok + 1);
             const T* xrow = lds + L::kX + (32 * it + il) * kRowV + 32 * wave + 8 * hh;
+            const int tok = 32 * it + il - none;
+            float met = 0.f;
 #pragma unroll
-            for (int b = 0; b < 16; ++b) {
-              const float term = lead * fmaf(after, w[b], u[b]) * to_f32(xrow[16 * (b / 8) + b % 8]);
-              sum += ((tok >= 0) & (32 * wave + 16 * (b / 8) + 8 * hh + b % 8 < width)) ? term : 0.f;
-            }
+            for (int b = 0; b < 16; ++b) met = fmaf(o[it][b], to_f32(xrow[16 * (b / 8) + b % 8]), met);
+            sum += tok >= 0 ? float(tok + r_lead) * met : 0.f;
+          }
+          const int64_t at = (((nh * ((a.t + TOK - 1) / TOK) + p0 / TOK) * blocks + block) * kWaves + wave) * (kMt * 1024) + lane * 4;
+          if (put) {
+#pragma unroll
+            for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f32x4_s*>(put + at + (mt * 4 + i) * 256) =
+                    f32x4_s{st[mt][4 * i], st[mt][4 * i + 1], st[mt][4 * i + 2], st[mt][4 * i + 3]};
+          }
+          if (get) {
+            float met = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const f32x4_s u = *reinterpret_cast<const f32x4_s*>(get + at + (mt * 4 + i) * 256);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) met = fmaf(u[j], st[mt][4 * i + j], met);
+              }
+            sum += float(m) * (1.f + (m == TOK ? whole_m1 : last_m1)) * met;
           }
         }
         decay += double(sum);
+      }
+      __syncthreads();
+      if (tid == 0) odd[turn ^ 1] = 0;
+      if (has && o_p) {
+        // ---- the products meet v
+        const T* vt = M::col_at(lds + L::kV, kRowV, lane) + 32 * wave;
+        const T* pp = lds + L::kP + lane * 8;
+#pragma unroll
+        for (int y = 0; y < kTs; ++y) {
+          const Frag vf = M::col(vt + 16 * y * kRowV, kRowV);
+          if (y < 2) o[0] = M::mma(vf, M::row(pp + y * 512), o[0]);
+          if constexpr (kIt > 1) o[1] = M::mma(vf, M::row(pp + (y + 2) * 512), o[1]);
+        }
+        if (strange) {
+          // an infinity or NaN among the block's v meets no product of an earlier token, not even a zero one
+          before();
+#pragma unroll
+          for (int it = 0; it < kIt; ++it)
+            for (int j = 0; j < 32 * it + 32; ++j) {
+              const int jl = j % 32, pair = it + j / 32;
+              if (j > 32 * it + il) continue;
+              const float p = to_f32(lds[L::kP + ((pair * 2 + jl / 16) * 64 + jl % 16 / 8 * 32 + il) * 8 + j % 8]);
+              const T* row = lds + L::kV + j * kRowV + 32 * wave + 8 * hh;
+#pragma unroll
+              for (int b = 0; b < 16; ++b) o[it][b] = fmaf(p, to_f32(row[16 * (b / 8) + b % 8]), o[it][b]);
+            }
+        }
+        const int64_t t = o_at + int64_t(p0) * o_row;
+#pragma unroll
+        for (int it = 0; it < kIt; ++it) {
+          const int tok = 32 * it + il - none;
+          if (tok < 0) continue;
+          const int64_t at = t + int64_t(unsigned(rev ? m - 1 - tok : tok) * uint64_t(o_row));
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = o[it][8 * g + i];
+            const int e = 32 * wave + 16 * g + 8 * hh;
+            if (o_f32) store_cols<float, KIND>(reinterpret_cast<float*>(o_p) + at, e, width, u);
+            else store_cols<T, KIND>(reinterpret_cast<T*>(o_p) + at, e, width, u);
+          }
+        }
       }
     }
     if (!(more || keeps)) break;  // (for all threads of the workgroup)
@@ -742,10 +756,6 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_r
       for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
         for (int b = 0; b < 16; ++b) {
-          if constexpr (DEC) {
-            const float both = fmaf(float(m), st[mt][b], st2[mt][b]);
-            st2[mt][b] = fmaf(both, m1, both);
-          }
           st[mt][b] = fmaf(st[mt][b], m1, st[mt][b]);
         }
       const T* kt = M::col_at(lds + L::kK, kRowK, lane);
@@ -756,39 +766,25 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_r
         float fy[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) fy[i] = fq[i] * (f_step[kTs - 1 - y] * f_last);
-        Frag f[M::kParts], f2[M::kParts];
+        Frag f[M::kParts];
         M::scaled(vf, fy, f);
-        if constexpr (DEC) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) fy[i] *= float(TOK - 1 - (16 * y + 8 * hh + i));
-          M::scaled(vf, fy, f2);
-        }
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt) {
           const Frag kf = M::col(kt + 16 * y * kRowK + 32 * mt, kRowK);
 #pragma unroll
-          for (int part = 0; part < M::kParts; ++part) {
-            st[mt] = M::mma(kf, f[part], st[mt]);
-            if constexpr (DEC) st2[mt] = M::mma(kf, f2[part], st2[mt]);
-          }
+          for (int part = 0; part < M::kParts; ++part) st[mt] = M::mma(kf, f[part], st[mt]);
         }
       }
     }
     __syncthreads();
-    if (!OUT || DEC) {
-      if (tid == 0) odd[turn ^ 1] = 0;  // (unused there)
-    }
   }
 
   // ---- what is left behind: the state, zeros for the tokens that are not valid, the decay's sum
   float* to = nullptr;
   if constexpr (OUT) to = keeps && r.to ? r.to + nh * size : nullptr;
-  else to = r.segs + (nh * (a.segs - 1) + s) * size;
+  else to = r.segs + (nh * (a.segs - 1) + (rev ? s - 1 : s)) * size;
   if (to && has) store_state(to, st);
-  if constexpr (DEC && !OUT) {
-    if (has) store_state(a.segs2 + (nh * (a.segs - 1) + s) * size, st2);
-  }
-  if constexpr (OUT && !DEC) {
+  if (OUT && o_p) {
     const int last = min(begin + a.seg, a.t);
     for (int t = max(begin, len) + tid / CB; t < last; t += kThreads / CB) {
       const int e = tid % CB;
@@ -799,18 +795,7 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_r
       }
     }
   }
-  if constexpr (kGrad) {
-    if (keeps && has) {
-      f32x16_h d[kMt];
-      load_state(a.dto + nh * size, d);
-#pragma unroll
-      for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-        for (int b = 0; b < 16; ++b) {
-          const int c = 32 * mt + 16 * (b / 8) + 8 * hh + b % 8;
-          decay += ((c < c_all) & (col < width)) ? double(d[mt][b]) * double(st2[mt][b]) : 0.0;
-        }
-    }
+  if constexpr (DEC) {
     double* box = reinterpret_cast<double*>(smem);
     __syncthreads();
     box[tid] = decay;
@@ -819,7 +804,7 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, DEC>())) void linear_r
       if (tid < half) box[tid] += box[tid + half];
       __syncthreads();
     }
-    if (tid == 0) a.part[(nh * a.segs + s) * blocks + block] = box[0];
+    if (tid == 0) r.part[(nh * a.segs + s) * blocks + block] = box[0];
   }
 }
 
@@ -850,11 +835,9 @@ int start_runs(LinArgs& a, int pad, bool out, bool dec, hipStream_t s) {
   const int64_t workgroups = (int64_t(a.units) + 7) / 8 * 8 * a.parts;
   auto go = [&](auto d, auto c) {
     constexpr int DP = decltype(d)::value, CB = decltype(c)::value;
-    if (out)
-      return dec ? start_run<T, DP, CB, KIND, true, true>(a, workgroups, s)
-                 : start_run<T, DP, CB, KIND, true, false>(a, workgroups, s);
-    return dec ? start_run<T, DP, CB, KIND, false, true>(a, workgroups, s)
-               : start_run<T, DP, CB, KIND, false, false>(a, workgroups, s);
+    if (!out) return start_run<T, DP, CB, KIND, false, false>(a, workgroups, s);
+    return dec ? start_run<T, DP, CB, KIND, true, true>(a, workgroups, s)
+               : start_run<T, DP, CB, KIND, true, false>(a, workgroups, s);
   };
   const std::integral_constant<int, 64> c64;
   const std::integral_constant<int, 128> c128;

@@ -173,8 +173,8 @@ int start_short(const ShortArgs& a, int64_t workgroups, hipStream_t s) {
 struct JoinArgs {
   struct Way {
     const float* from;  // [N][H][size], or null
-    float* segs;        // [N][H][segments - 1][size]: what a segment adds; becomes the state after it
-    float* segs2;       // the derivative by the decay, or null
+    float* segs;        // [N][H][segments - 1][size]: what a segment adds; becomes the state between two
+    int rev;            // from the last segment to the first
   } way[2];
   int64_t items, size;  // states of all heads, floats of one
   int heads, t, seg, segs;
@@ -182,37 +182,31 @@ struct JoinArgs {
   const int* lengths;
 };
 
-// States across segments: after[s] = f[tokens of s] before[s] + added[s], and
-// of its derivative S2 by the decay f (S2 + tokens S) + added2.  Four segments'
-// loads are in flight.
+// States across segments: after[s] = f[tokens of s] before[s] + added[s].  Eight
+// segments' loads are in flight.
 __global__ __launch_bounds__(256) void linear_join(JoinArgs a) {
   const JoinArgs::Way w = a.way[blockIdx.y];
+  const int between = a.segs - 1;
   for (int64_t item = int64_t(blockIdx.x) * 256 + threadIdx.x; item < a.items; item += int64_t(gridDim.x) * 256) {
     const int64_t nh = item / a.size, off = item - nh * a.size, n = nh / a.heads;
     const float g = a.log_decay ? a.log_decay[nh - n * a.heads] : 0.f;
     const int len = valid_tokens(a.lengths, int(n), a.t);
     const float whole = fade_m1(g, a.seg);
-    float* p = w.segs + nh * (a.segs - 1) * a.size + off;
-    float* p2 = w.segs2 ? w.segs2 + nh * (a.segs - 1) * a.size + off : nullptr;
-    float s = w.from ? w.from[item] : 0.f, s2 = 0.f;
-    for (int x0 = 0; x0 < a.segs - 1; x0 += 4) {
-      float u[4], u2[4];
+    // (slot x lies between segments x and x + 1)
+    float* p = w.segs + (nh * between + (w.rev ? between - 1 : 0)) * a.size + off;
+    const int64_t step = w.rev ? -a.size : a.size;
+    float s = w.from ? w.from[item] : 0.f;
+    for (int x0 = 0; x0 < between; x0 += 8) {
+      float u[8];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const bool in = x0 + x < a.segs - 1;
-        u[x] = in ? p[(x0 + x) * a.size] : 0.f;
-        u2[x] = in && p2 ? p2[(x0 + x) * a.size] : 0.f;
-      }
+      for (int x = 0; x < 8; ++x) u[x] = p[min(x0 + x, between - 1) * step];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (x0 + x >= a.segs - 1) break;
-        const int tokens = min(max(len - (x0 + x) * a.seg, 0), a.seg);
-        const float m1 = tokens == a.seg ? whole : fade_m1(g, tokens);
-        const float both = fmaf(float(tokens), s, s2);
-        s2 = fmaf(both, m1, both) + u2[x];
-        s = fmaf(s, m1, s) + u[x];
-        p[(x0 + x) * a.size] = s;
-        if (p2) p2[(x0 + x) * a.size] = s2;
+      for (int x = 0; x < 8; ++x) {
+        if (x0 + x >= between) break;
+        const int segment = w.rev ? between - x0 - x : x0 + x;
+        const int tokens = min(max(len - segment * a.seg, 0), a.seg);
+        s = fmaf(s, tokens == a.seg ? whole : fade_m1(g, tokens), s) + u[x];
+        p[(x0 + x) * step] = s;
       }
     }
   }
@@ -242,7 +236,8 @@ __global__ __launch_bounds__(256) void linear_heads(HeadSums a) {
   }
 }
 
-// dlog_decay: a workgroup's partial sums of one head, each thread's in order, then a tree.
+// dlog_decay: the partial sums of one head (of two recurrences, n sequences each, in one row of 2 n), each
+// thread's in order, then a tree.
 __global__ __launch_bounds__(256) void linear_decay(const double* part, float* out, int n, int heads, int each) {
   __shared__ double box[256];
   const int h = blockIdx.x, tid = threadIdx.x;
@@ -295,6 +290,21 @@ JoinArgs join_of(const cc3d::LinArgs& a, int64_t size) {
   return j;
 }
 
+void set_rows(cc3d::LinRun& r, const cc3d_rows_t& q, int qper, const cc3d_rows_t& k, int kper, const cc3d_rows_t& v, int vper) {
+  r.q = q.p;
+  r.qb = q.batch;
+  r.qr = q.row;
+  r.qper = qper;
+  r.k = k.p;
+  r.kb = k.batch;
+  r.kr = k.row;
+  r.kper = kper;
+  r.v = v.p;
+  r.vb = v.batch;
+  r.vr = v.row;
+  r.vper = vper;
+}
+
 int start_join(const JoinArgs& j, int ways, hipStream_t s) {
   void* at[] = {const_cast<JoinArgs*>(&j)};
   const int64_t blocks = std::min((j.items + 255) / 256, kGrid);
@@ -320,15 +330,27 @@ int launch_linear_forward(const cc3d_linear_plan& p, const cc3d_linear_args_t& c
   }
   LinArgs a = common(p, c, p.seg, p.segs);
   a.runs = 1;
-  a.run[0] = LinRun{c.q.p, c.k.p, c.v.p, c.o.p, c.q.batch, c.q.row, c.k.batch, c.k.row, c.v.batch, c.v.row, c.o.batch,
-                    c.o.row, d.heads / d.q_heads, d.heads / d.k_heads, d.heads / d.v_heads, d.dk, d.dv, d.dv, 1, 0, 0, 1,
-                    0, d.scale, d.scale, 1.f, c.h_in, c.h_out, static_cast<float*>(c.workspace)};
+  LinRun& r = a.run[0];
+  set_rows(r, c.q, d.heads / d.q_heads, c.k, d.heads / d.k_heads, c.v, d.heads / d.v_heads);
+  r.o = c.o.p;
+  r.ob = c.o.batch;
+  r.orow = c.o.row;
+  r.c = d.dk;
+  r.e = d.dv;
+  r.sc = d.dv;
+  r.se = 1;
+  r.lead = 1;
+  r.score = r.inter = d.scale;
+  r.update = 1.f;
+  r.from = c.h_in;
+  r.to = c.h_out;
+  r.segs = static_cast<float*>(c.workspace);
   const int pad = linear_pad(d.dk);
   if (a.segs > 1) {
     int e = run(a, d, pad, false, false, s);
     if (e) return e;
     JoinArgs j = join_of(a, int64_t(d.dk) * d.dv);
-    j.way[0] = {c.h_in, a.run[0].segs, nullptr};
+    j.way[0] = {c.h_in, r.segs, 0};
     if ((e = start_join(j, 1, s))) return e;
   }
   return run(a, d, pad, true, false, s);
@@ -338,72 +360,106 @@ int launch_linear_backward(const cc3d_linear_plan& p, const cc3d_linear_args_t& 
   const auto& d = p.d;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const LinearSpace space = linear_bwd_space(p);
-  float* w = static_cast<float*>(c.workspace);
-  float* states = w;
-  float* states2 = states + space.state;
-  float* grads = states2 + space.state;
-  float* part_q = grads + space.state;
+  float* states = static_cast<float*>(c.workspace);
+  float* grads = states + space.state;
+  float* blocks = grads + space.state;
+  float* part_q = blocks + space.blocks;
   float* part_k = part_q + space.dq;
   float* part_v = part_k + space.dk;
   double* decay = reinterpret_cast<double*>(part_v + space.dv);
   const int qper = d.heads / d.q_heads, kper = d.heads / d.k_heads, vper = d.heads / d.v_heads;
   const int pad = linear_pad(std::max(d.dk, d.dv));
+  const bool dec = c.dlog_decay;
   // results go to the caller's view, or where heads are shared to partial sums [N][T][heads][D]
-  auto out = [&](LinRun r, const cc3d_rows_t& v, int per, float* part) {
+  auto out = [&](LinRun& r, const cc3d_rows_t& v, int per, float* part) {
+    if (!v.p) return;
     r.o = per == 1 ? v.p : part;
     r.o_f32 = per > 1;
     r.ob = per == 1 ? v.batch : int64_t(d.t) * d.heads * r.e;
     r.orow = per == 1 ? v.row : int64_t(d.heads) * r.e;
-    return r;
   };
-  // dq: the recurrence of (do, v, k) over the transposed state; dk and dv: of (v, do, q) and (k, q, do), reversed
-  const LinRun rq = out(LinRun{c.grad_o.p, c.v.p, c.k.p, nullptr, c.grad_o.batch, c.grad_o.row, c.v.batch, c.v.row,
-                               c.k.batch, c.k.row, 0, 0, 1, vper, kper, d.dv, d.dk, 1, d.dv, 0, 0, 1, 0, d.scale, d.scale,
-                               1.f, c.h_in, nullptr, states}, c.dq, qper, part_q);
-  const LinRun rk = out(LinRun{c.v.p, c.grad_o.p, c.q.p, nullptr, c.v.batch, c.v.row, c.grad_o.batch, c.grad_o.row,
-                               c.q.batch, c.q.row, 0, 0, vper, 1, qper, d.dv, d.dk, 1, d.dv, 0, 1, 0, 0, d.scale, 1.f,
-                               d.scale, c.dh_out, nullptr, grads}, c.dk, kper, part_k);
-  const LinRun rv = out(LinRun{c.k.p, c.q.p, c.grad_o.p, nullptr, c.k.batch, c.k.row, c.q.batch, c.q.row, c.grad_o.batch,
-                               c.grad_o.row, 0, 0, kper, qper, 1, d.dk, d.dv, d.dv, 1, 0, 1, 0, 0, d.scale, 1.f, d.scale,
-                               c.dh_out, c.dh_in, grads}, c.dv, vper, part_v);
+  // dq: the recurrence of (do, v, k) over the transposed state
+  LinRun q{};
+  set_rows(q, c.grad_o, 1, c.v, vper, c.k, kper);
+  q.c = d.dv;
+  q.e = d.dk;
+  q.sc = 1;
+  q.se = d.dv;
+  q.lead = 1;
+  q.score = q.inter = d.scale;
+  q.update = 1.f;
+  q.from = c.h_in;
+  q.segs = states;
+  out(q, c.dq, qper, part_q);
+  // dk: that of (v, do, q), reversed
+  LinRun k = q;
+  set_rows(k, c.v, vper, c.grad_o, 1, c.q, qper);
+  k.o = nullptr;
+  k.rev = 1;
+  k.lead = 0;
+  k.inter = 1.f;
+  k.update = d.scale;
+  k.from = c.dh_out;
+  k.segs = grads;
+  out(k, c.dk, kper, part_k);
+  // dv: of (k, q, do), reversed
+  LinRun v = k;
+  set_rows(v, c.k, kper, c.q, qper, c.grad_o, 1);
+  v.o = nullptr;
+  v.c = d.dk;
+  v.e = d.dv;
+  v.sc = d.dv;
+  v.se = 1;
+  v.to = c.dh_in;
+  out(v, c.dv, vper, part_v);
+  // the decay's gradient
+  auto meets = [&](LinRun& r, const cc3d_rows_t& x, int per) {
+    r.x = x.p;
+    r.xb = x.batch;
+    r.xr = x.row;
+    r.xper = per;
+  };
+  const int64_t parts = int64_t(d.n) * d.heads * p.bwd_segs * linear_blocks(d.dk, linear_cols(d.dk));
+  meets(q, c.q, qper);
+  q.pairs = 1;
+  q.put = blocks;
+  q.part = decay;
+  meets(k, c.k, kper);
+  k.get = blocks;
+  k.part = decay + parts;
+
   LinArgs a = common(p, c, p.bwd_seg, p.bwd_segs);
-  a.segs2 = states2;
-  a.x = c.q.p;
-  a.xb = c.q.batch;
-  a.xr = c.q.row;
-  a.xper = qper;
-  a.dto = c.dh_out;
-  a.part = decay;
-  const bool dec = c.dlog_decay, back = c.dk.p || c.dv.p || c.dh_in;
+  const bool forth = dec || c.dq.p, back = dec || c.dk.p || c.dv.p || c.dh_in;
   int e = 0;
   if (a.segs > 1) {
     JoinArgs j = join_of(a, int64_t(d.dk) * d.dv);
     int ways = 0;
-    if (dec || c.dq.p) {
-      a.runs = 1;
-      a.run[0] = rq;
-      if ((e = run(a, d, pad, false, dec, s))) return e;
-      j.way[ways++] = {c.h_in, states, dec ? states2 : nullptr};
+    if (forth) {
+      a.run[a.runs++] = q;
+      j.way[ways++] = {c.h_in, states, 0};
     }
     if (back) {
-      a.runs = 1;
-      a.run[0] = rv;
-      if ((e = run(a, d, pad, false, false, s))) return e;
-      j.way[ways++] = {c.dh_out, grads, nullptr};
+      a.run[a.runs++] = v;
+      j.way[ways++] = {c.dh_out, grads, 1};
     }
+    if (ways && (e = run(a, d, pad, false, false, s))) return e;
     if (ways && (e = start_join(j, ways, s))) return e;
   }
-  if (dec) {
-    a.runs = 1;
-    a.run[0] = rq;
-    if ((e = run(a, d, pad, true, true, s))) return e;
-    e = launch(linear_decay, d.heads, 256, 0, s, decay, c.dlog_decay, d.n, d.heads, a.segs * a.run[0].blocks);
-    if (e) return e;
-  }
   a.runs = 0;
-  if (c.dq.p) a.run[a.runs++] = rq;
-  if (c.dk.p) a.run[a.runs++] = rk;
-  if (c.dv.p || c.dh_in) a.run[a.runs++] = rv;
+  if (dec) {
+    for (const LinRun* r : {&q, &k}) {  // (one after the other: the second reads what the first leaves)
+      a.runs = 1;
+      a.run[0] = *r;
+      if ((e = run(a, d, pad, true, true, s))) return e;
+    }
+    a.runs = 0;
+    e = launch(linear_decay, d.heads, 256, 0, s, decay, c.dlog_decay, 2 * d.n, d.heads, int(parts / (int64_t(d.n) * d.heads)));
+    if (e) return e;
+  } else {
+    if (c.dq.p) a.run[a.runs++] = q;
+    if (c.dk.p) a.run[a.runs++] = k;
+  }
+  if (c.dv.p || c.dh_in) a.run[a.runs++] = v;
   if (a.runs && (e = run(a, d, pad, true, false, s))) return e;
   HeadSums sums{};
   int jobs = 0;

@@ -30,12 +30,18 @@ constexpr double kTwoPi = 6.283185307179586476925286766559;
 
 namespace {
 
-// Segments of the time axis: as many as bring `units` workgroups a segment to
-// `want`, whole blocks of 64 tokens, at least two each (a segment costs two
-// passes over a state besides).
-void split_time(int32_t t, int64_t units, int64_t want, int32_t* seg, int32_t* segs) {
-  const int64_t blocks = ceildiv(t, cc3d::kLinTokens);
-  const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(ceildiv(want, units), blocks / 2));
+// Segments of the time axis, whole blocks of 64 tokens, where `units` workgroups
+// alone leave compute units idle: as many as make one workgroup of four waves or two
+// of two (64 columns of a state and fewer) a compute unit, rounded down.  8192 tokens
+// of 16 heads of 128 in 71 us at 16 segments, 73 at 32 and 104 at 8; of 64 in 42 at 32,
+// 50 at 16.  Two segments cost their second walk over the tokens and gain little: 192
+// heads of 128, 1024 tokens, 67 us whole and 94 in two, 256 heads of 64 of 2048 tokens
+// 99 and 105; 128 of 128, 2048 tokens, 124 and 126, in four 117.  512 tokens of 4 heads
+// in 17 us block by block and 28 in two.
+void split_time(int32_t t, int64_t units, int cols, int32_t* seg, int32_t* segs) {
+  const int64_t blocks = ceildiv(t, cc3d::kLinTokens), want = cols == 64 ? 2 * kUnits : kUnits;
+  int64_t pieces = std::min(want / units, blocks);
+  if (pieces < 3) pieces = 1;
   const int64_t each = ceildiv(blocks, pieces);
   *seg = int32_t(each * cc3d::kLinTokens);
   *segs = int32_t(ceildiv(blocks, each));
@@ -61,11 +67,12 @@ extern "C" cc3d_status_t linear_attention_plan(const cc3d_linear_desc_t* d, cc3d
   if (!cc3d::fits(units + 7 * blocks, cc3d::kLinThreads) || !cc3d::fits(short_units, cc3d::kLinThreads)) return refuse(CC3D_ERR_UNSUPPORTED);
   auto* p = make_plan<cc3d_linear_plan>(d);
   if (!p) return CC3D_ERR_NO_MEMORY;
-  if (d->t > cc3d::kLinShort) split_time(d->t, units, kUnits, &p->seg, &p->segs);
+  if (d->t > cc3d::kLinShort) split_time(d->t, units, cc3d::linear_cols(d->dv), &p->seg, &p->segs);
   const int cols = cc3d::linear_cols(int(widest));
-  // Backward: the recurrence with the fewest workgroups (the decay's is one by itself) once over the compute units.
+  // Backward: by dq's recurrence, which is a launch by itself where the decay's gradient is asked for (2 by 2049
+  // tokens, 16 heads, 64 by 128: 154 us at 11 segments, 174 at 7, 186 at 17).
   const int64_t of_k = cc3d::linear_blocks(d->dk, cols), of_v = cc3d::linear_blocks(d->dv, cols);
-  split_time(d->t, nh * of_k, kUnits, &p->bwd_seg, &p->bwd_segs);
+  split_time(d->t, nh * of_k, cc3d::linear_cols(d->dk), &p->bwd_seg, &p->bwd_segs);
   p->bwd_fits = cc3d::fits((nh + 7) * (2 * of_k + of_v), cc3d::kLinThreads);  // (where it is split it is far below)
   p->info.chunks = p->segs;
   p->info.backward_chunks = p->bwd_segs;
