@@ -87,6 +87,20 @@ __device__ __forceinline__ int valid_rows(const GroupArgs& a, int64_t n) {
   return a.lengths ? min(max(a.lengths[n], 0), a.p) : a.p;
 }
 
+// A thread's rows of a sample, or of a run of rows: row0, row0 + step, ... below end.
+template <class T, int KIND, int ROWS>
+struct Rows8 {
+  Raw8<T> v[ROWS];
+  __device__ __forceinline__ void load(const Cols<T, KIND>& cols, const void* p, int64_t at, int64_t stride, int row0, int step,
+                                       int end) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int row = row0 + r * step;
+      v[r] = row < end ? cols.load(p, at + row * stride + cols.c0) : zero8<T>();
+    }
+  }
+};
+
 // The sums of groups over the lines of each sample of a workgroup: V sums at
 // once, a term a lane (WHOLE) or a channel.  LDS: box [V][lines][terms of a row],
 // then sum [V][samples of the workgroup][groups].

@@ -3,42 +3,45 @@
 
 namespace {
 
-// ---- whole samples in registers: mean, then the squares about it, then the results
-template <class T, int KIND, bool WHOLE>
-__global__ __launch_bounds__(1024) void group_whole(GroupArgs a) {
-  constexpr int kRows = cc3d::kGroupRows, kTerms = Lane<T, KIND, WHOLE>::kTerms;
+// ---- whole samples in registers: mean, then the squares about it, then the results.
+// ROWS: of a thread; THREADS: at most.  The next samples' rows load while some are worked on.
+template <class T, int KIND, bool WHOLE, int ROWS, int THREADS>
+__global__ __launch_bounds__(THREADS) void group_whole(GroupArgs a) {
+  constexpr int kTerms = Lane<T, KIND, WHOLE>::kTerms;
   extern __shared__ __attribute__((aligned(16))) float box[];
   const Lane<T, KIND, WHOLE> l(a);
   const int samples = l.lines / a.line_n, row0 = l.line % a.line_n;
   const Raw8<T> rw = l.cols.param(a.w, 1.f), rb = l.cols.param(a.b, 0.f);
+  const int64_t step = int64_t(gridDim.x) * samples;
+  Rows8<T, KIND, ROWS> next;
+  int64_t n = int64_t(blockIdx.x) * samples + l.line / a.line_n;
+  int next_len = n < a.n ? valid_rows(a, n) : 0;
+  next.load(l.cols, a.x, n * a.xb, a.xr, row0, a.line_n, next_len);
   // (every thread of the workgroup takes part in the barriers of every turn)
-  for (int64_t n0 = int64_t(blockIdx.x) * samples; n0 < a.n; n0 += int64_t(gridDim.x) * samples) {
-    const int64_t n = n0 + l.line / a.line_n;
-    const int len = n < a.n ? valid_rows(a, n) : 0;
-    Raw8<T> v[kRows];
+  for (int64_t n0 = int64_t(blockIdx.x) * samples; n0 < a.n; n0 += step, n += step) {
+    const Rows8<T, KIND, ROWS> x = next;
+    const int len = next_len;
+    next_len = n + step < a.n ? valid_rows(a, n + step) : 0;
+    next.load(l.cols, a.x, (n + step) * a.xb, a.xr, row0, a.line_n, next_len);
     float sum[1][kTerms] = {};
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int row = row0 + r * a.line_n;
-      v[r] = row < len ? l.cols.load(a.x, n * a.xb + row * a.xr + l.cols.c0) : zero8<T>();
-    }
+    for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum[0][WHOLE ? 0 : j] += get8(v[r], j);
+      for (int j = 0; j < 8; ++j) sum[0][WHOLE ? 0 : j] += get8(x.v[r], j);
     sample_sums(a, l, box, sum);
     const float inv = len > 0 ? 1.f / (float(len) * float(a.cg)) : 0.f;
     float mean[kTerms], sq[1][kTerms] = {};
 #pragma unroll
     for (int j = 0; j < kTerms; ++j) mean[j] = sum[0][j] * inv;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
-      if (row0 + r * a.line_n < len)
+    for (int r = 0; r < ROWS; ++r) {
+      const bool there = row0 + r * a.line_n < len;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = get8(v[r], j) - mean[WHOLE ? 0 : j];
-          sq[0][WHOLE ? 0 : j] = fmaf(d, d, sq[0][WHOLE ? 0 : j]);
-        }
+      for (int j = 0; j < 8; ++j) {
+        const float d = there ? get8(x.v[r], j) - mean[WHOLE ? 0 : j] : 0.f;
+        sq[0][WHOLE ? 0 : j] = fmaf(d, d, sq[0][WHOLE ? 0 : j]);
+      }
+    }
     sample_sums(a, l, box, sq);
     float rs[kTerms];
 #pragma unroll
@@ -51,13 +54,13 @@ __global__ __launch_bounds__(1024) void group_whole(GroupArgs a) {
           reinterpret_cast<float2*>(a.stats)[n * a.groups + g] = float2{mean[j], rs[j]};
       });
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
       const int row = row0 + r * a.line_n;
       if (row >= a.p) continue;
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float u = fmaf((get8(v[r], j) - mean[WHOLE ? 0 : j]) * rs[WHOLE ? 0 : j], get8(rw, j), get8(rb, j));
+        const float u = fmaf((get8(x.v[r], j) - mean[WHOLE ? 0 : j]) * rs[WHOLE ? 0 : j], get8(rw, j), get8(rb, j));
         o[j] = row < len ? (a.act == CC3D_ACT_SILU ? u * sigmoid_f32(u) : u) : 0.f;
       }
       l.cols.store(a.y, n * a.yb + row * a.yr + l.cols.c0, o);
@@ -88,20 +91,18 @@ __global__ __launch_bounds__(1024) void group_stats(GroupArgs a) {
 #pragma unroll
   for (int j = 0; j < kTerms; ++j) have[j] = {0.f, 0.f};
   float count = 0.f;
+  Rows8<T, KIND, kRows> next;
+  next.load(l.cols, a.x, n * a.xb, a.xr, begin + l.line, l.lines, end);
   for (int r0 = begin + l.line; r0 < end; r0 += l.lines * kRows) {
-    Raw8<T> v[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int row = r0 + r * l.lines;
-      v[r] = row < end ? l.cols.load(a.x, n * a.xb + row * a.xr + l.cols.c0) : zero8<T>();
-    }
+    const Rows8<T, KIND, kRows> x = next;
+    next.load(l.cols, a.x, n * a.xb, a.xr, r0 + l.lines * kRows, l.lines, end);
     const int there = min(kRows, (end - r0 + l.lines - 1) / l.lines);
     const float now = float(there * kEach), inv = __builtin_amdgcn_rcpf(now);
     float sum[kTerms] = {};
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[WHOLE ? 0 : j] += get8(v[r], j);
+      for (int j = 0; j < 8; ++j) sum[WHOLE ? 0 : j] += get8(x.v[r], j);
     Moments m[kTerms];
 #pragma unroll
     for (int j = 0; j < kTerms; ++j) m[j] = {sum[j] * inv, 0.f};
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(1024) void group_stats(GroupArgs a) {
       if (r < there)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float d = get8(v[r], j) - m[WHOLE ? 0 : j].mean;
+          const float d = get8(x.v[r], j) - m[WHOLE ? 0 : j].mean;
           m[WHOLE ? 0 : j].m2 = fmaf(d, d, m[WHOLE ? 0 : j].m2);
         }
     const float both = __builtin_amdgcn_rcpf(count + now);
@@ -208,8 +209,10 @@ template <class T, int KIND, bool WHOLE>
 __global__ __launch_bounds__(1024) void group_apply(GroupArgs a) {
   constexpr int kTerms = Lane<T, KIND, WHOLE>::kTerms, kRows = 4;
   const Lane<T, KIND, WHOLE> l(a);
-  const int64_t n = blockIdx.x / a.splits;
-  const int split = int(blockIdx.x - n * a.splits), len = valid_rows(a, n);
+  // (from the last run to the first: those are in the last-level cache from the sums)
+  const unsigned run = gridDim.x - 1 - blockIdx.x;
+  const int64_t n = run / a.splits;
+  const int split = int(run - n * a.splits), len = valid_rows(a, n);
   const int begin = split * a.rows, end = min(begin + a.rows, a.p);
   float mean[kTerms], f[8], b[8];
   const Raw8<T> rw = l.cols.param(a.w, 1.f), rb = l.cols.param(a.b, 0.f);
@@ -228,13 +231,11 @@ __global__ __launch_bounds__(1024) void group_apply(GroupArgs a) {
       f[j] *= s.y;
     }
   });
+  Rows8<T, KIND, kRows> next;
+  next.load(l.cols, a.x, n * a.xb, a.xr, begin + l.line, l.lines, min(end, len));
   for (int r0 = begin + l.line; r0 < end; r0 += l.lines * kRows) {
-    Raw8<T> v[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int row = r0 + r * l.lines;
-      v[r] = row < min(end, len) ? l.cols.load(a.x, n * a.xb + row * a.xr + l.cols.c0) : zero8<T>();
-    }
+    const Rows8<T, KIND, kRows> x = next;
+    next.load(l.cols, a.x, n * a.xb, a.xr, r0 + l.lines * kRows, l.lines, min(end, len));
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int row = r0 + r * l.lines;
@@ -242,7 +243,7 @@ __global__ __launch_bounds__(1024) void group_apply(GroupArgs a) {
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float u = fmaf(get8(v[r], j) - mean[WHOLE ? 0 : j], f[j], b[j]);
+        const float u = fmaf(get8(x.v[r], j) - mean[WHOLE ? 0 : j], f[j], b[j]);
         o[j] = row < len ? (a.act == CC3D_ACT_SILU ? u * sigmoid_f32(u) : u) : 0.f;
       }
       l.cols.store(a.y, n * a.yb + row * a.yr + l.cols.c0, o);
@@ -254,7 +255,10 @@ template <class T, int KIND, bool WHOLE>
 struct RunWhole {
   static int run(const cc3d_group_plan& p, const GroupArgs& a, hipStream_t s) {
     const int threads = cc3d::group_threads(a.c);
-    return launch_lds(&group_whole<T, KIND, WHOLE>, p.workers, threads, sample_lds(a, WHOLE, 1, threads), s, a);
+    auto go = [&](auto* kernel) { return launch_lds(kernel, p.workers, threads, sample_lds(a, WHOLE, 1, threads), s, a); };
+    if (a.p == 1) return threads == 256 ? go(&group_whole<T, KIND, WHOLE, 1, 256>) : go(&group_whole<T, KIND, WHOLE, 1, 1024>);
+    return threads == 256 ? go(&group_whole<T, KIND, WHOLE, cc3d::kGroupRows, 256>)
+                          : go(&group_whole<T, KIND, WHOLE, cc3d::kGroupRows, 1024>);
   }
 };
 

@@ -48,10 +48,11 @@ __device__ __forceinline__ void fold_lines(const GroupArgs& a, const Lane<T, KIN
   }
 }
 
-// ---- whole samples in registers
-template <class T, int KIND, bool WHOLE>
-__global__ __launch_bounds__(1024) void group_whole_bwd(GroupArgs a) {
-  constexpr int kRows = cc3d::kGroupRows, kTerms = Lane<T, KIND, WHOLE>::kTerms;
+// ---- whole samples in registers.  ROWS: of a thread; THREADS: at most (registers spill at 1024, of more than 2048
+// channels, and at four rows)
+template <class T, int KIND, bool WHOLE, int ROWS, int THREADS>
+__global__ __launch_bounds__(THREADS) void group_whole_bwd(GroupArgs a) {
+  constexpr int kRows = ROWS, kTerms = Lane<T, KIND, WHOLE>::kTerms;
   extern __shared__ __attribute__((aligned(16))) float box[];
   const Lane<T, KIND, WHOLE> l(a);
   const int samples = l.lines / a.line_n, row0 = l.line % a.line_n;
@@ -149,19 +150,20 @@ __global__ __launch_bounds__(1024) void group_sums_bwd(GroupArgs a) {
     mean[j] = s.x;
     rs[j] = s.y;
   });
+  Rows8<T, KIND, kRows> nx, ny;
+  auto fetch = [&](int r0) {
+    nx.load(l.cols, a.x, n * a.xb, a.xr, r0, l.lines, end);
+    ny.load(l.cols, a.dy, n * a.dyb, a.dyr, r0, l.lines, end);
+  };
+  fetch(begin + l.line);
   for (int r0 = begin + l.line; r0 < end; r0 += l.lines * kRows) {
-    Raw8<T> x[kRows], dy[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int row = r0 + r * l.lines;
-      x[r] = row < end ? l.cols.load(a.x, n * a.xb + row * a.xr + l.cols.c0) : zero8<T>();
-      dy[r] = row < end ? l.cols.load(a.dy, n * a.dyb + row * a.dyr + l.cols.c0) : zero8<T>();
-    }
+    const Rows8<T, KIND, kRows> x = nx, dy = ny;
+    fetch(r0 + l.lines * kRows);
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       if (r0 + r * l.lines >= end) break;
       float xn[8], g[8];
-      slope(x[r], dy[r], mean, rs, w, b, a.act, xn, g);
+      slope(x.v[r], dy.v[r], mean, rs, w, b, a.act, xn, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dw[j] = fmaf(g[j], xn[j], dw[j]);
@@ -202,8 +204,10 @@ __global__ __launch_bounds__(1024) void group_apply_bwd(GroupArgs a) {
   constexpr int kTerms = Lane<T, KIND, WHOLE>::kTerms, kRows = 2;
   extern __shared__ __attribute__((aligned(16))) float box[];  // [groups][2]
   const Lane<T, KIND, WHOLE> l(a);
-  const int64_t n = blockIdx.x / a.splits;
-  const int split = int(blockIdx.x - n * a.splits), len = valid_rows(a, n);
+  // (from the last run to the first: those are in the last-level cache from the sums)
+  const unsigned run = gridDim.x - 1 - blockIdx.x;
+  const int64_t n = run / a.splits;
+  const int split = int(run - n * a.splits), len = valid_rows(a, n);
   const int begin = split * a.rows, end = min(begin + a.rows, a.p);
   const float inv = len > 0 ? 1.f / (float(len) * float(a.cg)) : 0.f;
   const float* chan = a.chan + n * 2 * a.c;
@@ -236,21 +240,21 @@ __global__ __launch_bounds__(1024) void group_apply_bwd(GroupArgs a) {
     m[0][j] = box[2 * g];
     m[1][j] = box[2 * g + 1];
   });
+  Rows8<T, KIND, kRows> nx, ny;
+  auto fetch = [&](int r0) {
+    nx.load(l.cols, a.x, n * a.xb, a.xr, r0, l.lines, min(end, len));
+    ny.load(l.cols, a.dy, n * a.dyb, a.dyr, r0, l.lines, min(end, len));
+  };
+  fetch(begin + l.line);
   for (int r0 = begin + l.line; r0 < end; r0 += l.lines * kRows) {
-    Raw8<T> x[kRows], dy[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int row = r0 + r * l.lines;
-      const bool there = row < min(end, len);
-      x[r] = there ? l.cols.load(a.x, n * a.xb + row * a.xr + l.cols.c0) : zero8<T>();
-      dy[r] = there ? l.cols.load(a.dy, n * a.dyb + row * a.dyr + l.cols.c0) : zero8<T>();
-    }
+    const Rows8<T, KIND, kRows> x = nx, dy = ny;
+    fetch(r0 + l.lines * kRows);
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int row = r0 + r * l.lines;
       if (row >= end) break;
       float xn[8], g[8], o[8];
-      slope(x[r], dy[r], mean, rs, w, b, a.act, xn, g);
+      slope(x.v[r], dy.v[r], mean, rs, w, b, a.act, xn, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         constexpr bool one = WHOLE;
@@ -267,7 +271,10 @@ struct RunWhole {
   static int run(const cc3d_group_plan& p, const GroupArgs& a, hipStream_t s) {
     const int threads = cc3d::group_threads(a.c);
     const int lds = std::max(sample_lds(a, WHOLE, 2, threads), 8 * threads / a.lanes * a.c);
-    return launch_lds(&group_whole_bwd<T, KIND, WHOLE>, p.workers, threads, lds, s, a);
+    auto go = [&](auto* kernel) { return launch_lds(kernel, p.workers, threads, lds, s, a); };
+    if (a.p == 1) return threads == 256 ? go(&group_whole_bwd<T, KIND, WHOLE, 1, 256>) : go(&group_whole_bwd<T, KIND, WHOLE, 1, 1024>);
+    return threads == 256 ? go(&group_whole_bwd<T, KIND, WHOLE, cc3d::kGroupRows, 256>)
+                          : go(&group_whole_bwd<T, KIND, WHOLE, cc3d::kGroupRows, 1024>);
   }
 };
 template <class T, int KIND, bool WHOLE>

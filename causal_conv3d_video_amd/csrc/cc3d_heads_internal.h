@@ -75,6 +75,7 @@ int launch_linear_backward(const cc3d_linear_plan& p, const cc3d_linear_args_t& 
 // --- rotary
 
 constexpr int kRotaryThreads = 256;
+constexpr int kRotaryRow = 4096;  // channels that pass through LDS at a time
 int launch_rotary(const cc3d_rotary_plan& p, const cc3d_rotary_args_t& a, bool backward, void* stream);
 
 // --- group norm

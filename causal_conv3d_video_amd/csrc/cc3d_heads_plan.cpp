@@ -245,7 +245,7 @@ extern "C" cc3d_status_t group_norm_plan(const cc3d_group_desc_t* d, cc3d_group_
     int64_t line_n = 1;
     while (line_n * cc3d::kGroupRows < d->p) line_n *= 2;
     // (every workgroup of the backward call leaves a row of partial sums)
-    workers = std::min<int64_t>(ceildiv(d->n, lines / line_n), 4 * kUnits);
+    workers = std::min<int64_t>(ceildiv(d->n, lines / line_n), 8 * kUnits);
   } else {
     // Runs of rows: eight workgroups of 256 threads a compute unit, at least two steps of a thread each.
     splits = std::max<int64_t>(1, std::min<int64_t>(ceildiv(8 * kUnits * 256 / threads, d->n),
