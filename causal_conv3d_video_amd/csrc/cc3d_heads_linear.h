@@ -237,6 +237,13 @@ struct Mat<bf16_s> {
     for (int i = 0; i < 4; ++i) v |= (r.q[0][i] & 0x7f807f80u) + 0x00800080u;
     return v & 0x80008000u;
   }
+  // zeros in the place of those
+  static __device__ __forceinline__ Frag finite(Frag v) {
+    u32x4_s w = __builtin_bit_cast(u32x4_s, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] &= ~((((w[i] & 0x7f807f80u) + 0x00800080u) >> 15 & 0x00010001u) * 0xffffu);
+    return __builtin_bit_cast(Frag, w);
+  }
 };
 
 template <>
@@ -293,6 +300,11 @@ struct Mat<float> {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v |= (r.q[i / 4][i % 4] & 0x7f800000u) + 0x00800000u;
     return v & 0x80000000u;
+  }
+  static __device__ __forceinline__ Frag finite(Frag v) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.x[i] = __builtin_fabsf(v.x[i]) < __builtin_inff() ? v.x[i] : 0.f;
+    return v;
   }
 };
 
@@ -404,7 +416,7 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
   constexpr int kStepK = kThreads / (DP / 8), kStepV = kThreads / (CB / 8);
   static_assert(kVecK * kThreads * 8 == TOK * DP && kVecV * kThreads * 8 == TOK * CB, "threads");
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ int odd[2];  // a block of k or v holds an infinity or NaN
+  __shared__ int odd[2];  // a block of v holds an infinity or NaN
   T* lds = reinterpret_cast<T*>(smem);
   const int tid = threadIdx.x, lane = tid % 64, wave = pin(tid / 64), il = lane % 32, hh = lane / 32;
 
@@ -578,7 +590,6 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
     for (int y = 0; y < kVecK; ++y) {
       const int j = krow + y * kStepK;
       if (!whole) kn[y] = kc.finish(kn[y], j >= none, c_all);
-      full |= M::full(kn[y]);
       M::put(lds + L::kK + j * kRowK + kcol, kn[y]);
       if constexpr (OUT) {
         if (!whole) qn[y] = kc.finish(qn[y], j >= none, c_all);
@@ -589,7 +600,7 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
     for (int y = 0; y < kVecV; ++y) {
       const int j = vrow + y * kStepV;
       if (!whole) vn[y] = vc.finish(vn[y], j >= none, width);
-      full |= M::full(vn[y]);
+      if constexpr (OUT) full |= M::full(vn[y]);
       M::put(lds + L::kV + j * kRowV + vcol, vn[y]);
       if constexpr (DEC) {
         if (!whole) xn[y] = vc.finish(xn[y], j >= none, width);
@@ -709,15 +720,20 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
         // ---- the products meet v
         const T* vt = M::col_at(lds + L::kV, kRowV, lane) + 32 * wave;
         const T* pp = lds + L::kP + lane * 8;
+        auto meet = [&](auto&& get) {
 #pragma unroll
-        for (int y = 0; y < kTs; ++y) {
-          const Frag vf = M::col(vt + 16 * y * kRowV, kRowV);
-          if (y < 2) o[0] = M::mma(vf, M::row(pp + y * 512), o[0]);
-          if constexpr (kIt > 1) o[1] = M::mma(vf, M::row(pp + (y + 2) * 512), o[1]);
-        }
-        if (strange) {
-          // an infinity or NaN among the block's v meets no product of an earlier token, not even a zero one
-          before();
+          for (int y = 0; y < kTs; ++y) {
+            const Frag vf = get(M::col(vt + 16 * y * kRowV, kRowV));
+            if (y < 2) o[0] = M::mma(vf, M::row(pp + y * 512), o[0]);
+            if constexpr (kIt > 1) o[1] = M::mma(vf, M::row(pp + (y + 2) * 512), o[1]);
+          }
+        };
+        if (!strange) {
+          meet([](Frag f) { return f; });
+        } else {
+          // An infinity or NaN among the block's v meets no product of an earlier token, not even a zero one: zero in the
+          // sums for all, and added by itself to the tokens from its own on.
+          meet([](Frag f) { return M::finite(f); });
 #pragma unroll
           for (int it = 0; it < kIt; ++it)
             for (int j = 0; j < 32 * it + 32; ++j) {
@@ -726,7 +742,10 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
               const float p = to_f32(lds[L::kP + ((pair * 2 + jl / 16) * 64 + jl % 16 / 8 * 32 + il) * 8 + j % 8]);
               const T* row = lds + L::kV + j * kRowV + 32 * wave + 8 * hh;
 #pragma unroll
-              for (int b = 0; b < 16; ++b) o[it][b] = fmaf(p, to_f32(row[16 * (b / 8) + b % 8]), o[it][b]);
+              for (int b = 0; b < 16; ++b) {
+                const float u = to_f32(row[16 * (b / 8) + b % 8]);
+                if (!(__builtin_fabsf(u) < __builtin_inff())) o[it][b] = fmaf(p, u, o[it][b]);
+              }
             }
         }
         const int64_t t = o_at + int64_t(p0) * o_row;
