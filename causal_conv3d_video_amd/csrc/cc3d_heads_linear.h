@@ -36,10 +36,11 @@
 //
 // Rounding.  bf16 operands of a product are exact; what is computed and then
 // multiplied again is rounded: f (q.k) to bf16 (half a step, 2^-8 at most, beside the
-// result's own), the state to bf16 for the product with q (the same), and f v, which
-// is added to the state, to two bf16 (rounded, and the rest: 2^-16): a state is an
-// fp32 result and is carried.  The decay's gradient, fp32 too, takes the state
-// as two bf16 as well and multiplies both products of its pairs in fp32.  fp32 tensors
+// result's own), the state to bf16 for the product with q (the same).  What is added
+// to a state, f v, is kept whole, as three bf16: a state is an fp32 result and is
+// carried (as two, 2^-18 each, 8192 tokens of 16 heads of 128 took 78
+// instead of 83 us and a state was 1.6e-6 off).  The decay's gradient, fp32 too, takes
+// the state as three bf16 as well and multiplies both products of its pairs in fp32.  fp32 tensors
 // use the fp32 matrix products throughout.
 //
 // The decay's gradient is the sum over all blocks of what depends on g there, S the
@@ -149,10 +150,14 @@ __device__ __forceinline__ unsigned pack2(float lo, float hi) {
 // r, 0 and r is r, but 0 where r is no number).
 __device__ __forceinline__ float rest(float v, float hi) { return __builtin_amdgcn_fmed3f(v - hi, 0.f, v - hi); }
 
-// Two values rounded to bf16 and the rests, rounded too: v = hi + lo but for 2^-16 of it.
-__device__ __forceinline__ void split2(float v, float w, unsigned& hi, unsigned& lo) {
-  hi = pack2(v, w);
-  lo = pack2(rest(v, __uint_as_float(hi << 16)), rest(w, __uint_as_float(hi & 0xffff0000u)));
+// Two values as sums of three bf16 each: rounded, the rest rounded, and what that
+// leaves (24 bits hold three times eight).
+__device__ __forceinline__ void split2(float v, float w, unsigned (&part)[3]) {
+  part[0] = pack2(v, w);
+  v = rest(v, __uint_as_float(part[0] << 16));
+  w = rest(w, __uint_as_float(part[0] & 0xffff0000u));
+  part[1] = pack2(v, w);
+  part[2] = pack2(v - __uint_as_float(part[1] << 16), w - __uint_as_float(part[1] & 0xffff0000u));
 }
 
 // Row (or column) m of 32 of a product's result holds place(m) of what it is
@@ -174,7 +179,7 @@ struct Mat<bf16_s> {
   // more than twice where that is 12 or 36 words (of 64).
   static constexpr int kPad = 8;
   static constexpr int pad_both(int width) { return width % 128 == 0 ? 24 : 8; }
-  static constexpr int kParts = 2;  // of what is rounded on its way into a state
+  static constexpr int kParts = 3;  // of what is rounded on its way into a state
   static __device__ __forceinline__ f32x16_h mma(Frag a, Frag b, f32x16_h c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
@@ -203,30 +208,30 @@ struct Mat<bf16_s> {
   }
   template <int g>
   static __device__ __forceinline__ void split(const f32x16_h& v, Frag (&out)[kParts]) {
-    u32x4_s hi, lo;
+    u32x4_s part[kParts];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      unsigned x, y;
-      split2(v[8 * g + 2 * i], v[8 * g + 2 * i + 1], x, y);
-      hi[i] = x;
-      lo[i] = y;
+      unsigned w[kParts];
+      split2(v[8 * g + 2 * i], v[8 * g + 2 * i + 1], w);
+#pragma unroll
+      for (int x = 0; x < kParts; ++x) part[x][i] = w[x];
     }
-    out[0] = __builtin_bit_cast(Frag, hi);
-    out[1] = __builtin_bit_cast(Frag, lo);
+#pragma unroll
+    for (int x = 0; x < kParts; ++x) out[x] = __builtin_bit_cast(Frag, part[x]);
   }
   // f[i] times the eight terms, in kParts
   static __device__ __forceinline__ void scaled(Frag v, const float (&f)[8], Frag (&out)[kParts]) {
     const u32x4_s w = __builtin_bit_cast(u32x4_s, v);
-    u32x4_s hi, lo;
+    u32x4_s part[kParts];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      unsigned x, y;
-      split2(__uint_as_float(w[i] << 16) * f[2 * i], __uint_as_float(w[i] & 0xffff0000u) * f[2 * i + 1], x, y);
-      hi[i] = x;
-      lo[i] = y;
+      unsigned u[kParts];
+      split2(__uint_as_float(w[i] << 16) * f[2 * i], __uint_as_float(w[i] & 0xffff0000u) * f[2 * i + 1], u);
+#pragma unroll
+      for (int x = 0; x < kParts; ++x) part[x][i] = u[x];
     }
-    out[0] = __builtin_bit_cast(Frag, hi);
-    out[1] = __builtin_bit_cast(Frag, lo);
+#pragma unroll
+    for (int x = 0; x < kParts; ++x) out[x] = __builtin_bit_cast(Frag, part[x]);
   }
   static __device__ __forceinline__ void put(bf16_s* p, Frag v) { *reinterpret_cast<u32x4_s*>(p) = __builtin_bit_cast(u32x4_s, v); }
   static __device__ __forceinline__ void put(bf16_s* p, const Raw8<bf16_s>& r) { *reinterpret_cast<u32x4_s*>(p) = r.q[0]; }

@@ -52,9 +52,9 @@ extern "C" {
  * Tokens are taken 64 at a time with matrix products.  With bf16 tensors the
  * products of a token's q with the k of its 64 (and with the state before them)
  * are rounded to bf16 before they meet v (and q); what is added to a state, and
- * so h_out and dh_in, and what makes dlog_decay is kept to 16 bits or more.  A
- * value that is no number reaches its own token's results and later ones, as
- * the recurrence says, and none before it.
+ * so h_out and dh_in, and what makes dlog_decay is not.  A value that is no
+ * number reaches its own token's results and later ones, as the recurrence
+ * says, and none before it.
  * ------------------------------------------------------------------------ */
 typedef struct cc3d_linear_desc {
   int32_t n, t;                          /* sequences, tokens (up to 2^30); >= 1 */
