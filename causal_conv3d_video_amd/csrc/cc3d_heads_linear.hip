@@ -213,56 +213,90 @@ __global__ __launch_bounds__(256) void linear_join(JoinArgs a) {
 }
 
 struct HeadSum {
-  const float* part;  // [N][T][heads][D]
+  const float* part;  // [N][T][heads][per][D]
   void* out;
-  int64_t batch, row, el;  // el: N T (heads / per) D
-  int per, d, t, heads;    // heads: of the result
+  int64_t batch, row, rows;  // rows: N T heads
+  int per, d, lanes, t, heads;  // heads: of the result; lanes: of a row, four columns each (a power of two)
+};
+// dlog_decay's partial sums [n][heads][each]
+struct DecaySum {
+  const double* part;
+  float* out;
+  int n, heads, each;
 };
 struct HeadSums {
   HeadSum job[3];
+  DecaySum decay;
+  int jobs;
 };
 
-// Gradients of shared heads: sums over the heads that share one, in order.
-template <class T>
-__global__ __launch_bounds__(256) void linear_heads(HeadSums a) {
-  const HeadSum j = a.job[blockIdx.y];
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < j.el; i += int64_t(gridDim.x) * 256) {
-    const int64_t row = i / j.d, d = i - row * j.d;       // (n, t, head) and column
-    const int64_t tok = row / j.heads, head = row - tok * j.heads, n = tok / j.t;
-    const float* p = j.part + row * j.per * j.d + d;
-    float s = 0.f;
-    for (int x = 0; x < j.per; ++x) s += p[int64_t(x) * j.d];
-    static_cast<T*>(j.out)[n * j.batch + (tok - n * j.t) * j.row + head * j.d + d] = from_f32<T>(s);
-  }
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  return a >> 32 ? a / b : int64_t(unsigned(a) / unsigned(b));
 }
 
-// dlog_decay: the partial sums of one head (of two recurrences, n sequences each, in one row of 2 n), each
-// thread's in order, then a tree.
-__global__ __launch_bounds__(256) void linear_decay(const double* part, float* out, int n, int heads, int each) {
-  __shared__ double box[256];
-  const int h = blockIdx.x, tid = threadIdx.x;
-  double s = 0.0;
-  for (int64_t i = tid; i < int64_t(n) * each; i += 256) {
-    const int64_t b = i / each;
-    s += part[(b * heads + h) * each + (i - b * each)];
+// What the recurrences leave in parts.  Gradients of shared heads: sums over the heads
+// that share one, in order (2 by 2049 tokens, two gradients of 4 heads of 64 from 16: 8 us,
+// a value a thread 12).  Behind them dlog_decay, a head a workgroup: each thread's partial
+// sums in order, then a tree (5 us as a launch of its own).
+template <class T>
+__global__ __launch_bounds__(256) void linear_sums(HeadSums a) {
+  const int tid = threadIdx.x;
+  if (int(blockIdx.y) == a.jobs) {
+    __shared__ double box[256];
+    const DecaySum& j = a.decay;
+    for (int h = blockIdx.x; h < j.heads; h += gridDim.x) {
+      double s = 0.0;
+      for (int64_t i = tid; i < int64_t(j.n) * j.each; i += 256) {
+        const int64_t b = quotient(i, j.each);
+        s += j.part[(b * j.heads + h) * j.each + (i - b * j.each)];
+      }
+      box[tid] = s;
+      __syncthreads();
+      for (int half = 128; half > 0; half /= 2) {
+        if (tid < half) box[tid] += box[tid + half];
+        __syncthreads();
+      }
+      if (tid == 0) j.out[h] = float(box[0]);
+      __syncthreads();
+    }
+    return;
   }
-  box[tid] = s;
-  __syncthreads();
-  for (int half = 128; half > 0; half /= 2) {
-    if (tid < half) box[tid] += box[tid + half];
-    __syncthreads();
+  const HeadSum j = a.job[blockIdx.y];
+  const int each = 256 / j.lanes, c = tid % j.lanes * 4;
+  if (c >= j.d) return;
+  for (int64_t row = int64_t(blockIdx.x) * each + tid / j.lanes; row < j.rows; row += int64_t(gridDim.x) * each) {
+    const int64_t tok = quotient(row, j.heads), head = row - tok * j.heads, n = quotient(tok, j.t);
+    const float* p = j.part + row * j.per * j.d + c;
+    T* out = static_cast<T*>(j.out) + n * j.batch + (tok - n * j.t) * j.row + head * j.d + c;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (c + 4 <= j.d) {
+      for (int x = 0; x < j.per; ++x) {
+        const f32x4_s v = __builtin_bit_cast(f32x4_s, *reinterpret_cast<const u32x4_by4*>(p + int64_t(x) * j.d));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += v[i];
+      }
+    } else {
+      for (int x = 0; x < j.per; ++x)
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (c + i < j.d) s[i] += p[int64_t(x) * j.d + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < j.d) out[i] = from_f32<T>(s[i]);
   }
-  if (tid == 0) out[h] = float(box[0]);
 }
 
 constexpr int64_t kGrid = 1 << 16;  // workgroups of the kernels that walk their work in turns
 
-int run(cc3d::LinArgs& a, const cc3d_linear_desc_t& d, int pad, bool out, bool dec, hipStream_t s) {
+int run(cc3d::LinArgs& a, const cc3d_linear_desc_t& d, bool out, bool dec, hipStream_t s) {
   static cc3d::LinStart* const of[2][3] = {
       {cc3d::linear_f32_eights, cc3d::linear_f32_rest, cc3d::linear_f32_less},
       {cc3d::linear_bf16_eights, cc3d::linear_bf16_rest, cc3d::linear_bf16_less}};
   const int kind = std::min(d.dk, d.dv) < 8 ? kLess : d.dk % 8 || d.dv % 8 ? kRest : kEights;
-  return of[d.dtype == CC3D_BF16][kind](a, pad, out, dec, s);
+  int widest = 0;
+  for (int i = 0; i < a.runs; ++i) widest = std::max(widest, a.run[i].c);
+  return of[d.dtype == CC3D_BF16][kind](a, cc3d::linear_pad(widest), out, dec, s);
 }
 
 cc3d::LinArgs common(const cc3d_linear_plan& p, const cc3d_linear_args_t& c, int seg, int segs) {
@@ -345,15 +379,14 @@ int launch_linear_forward(const cc3d_linear_plan& p, const cc3d_linear_args_t& c
   r.from = c.h_in;
   r.to = c.h_out;
   r.segs = static_cast<float*>(c.workspace);
-  const int pad = linear_pad(d.dk);
   if (a.segs > 1) {
-    int e = run(a, d, pad, false, false, s);
+    int e = run(a, d, false, false, s);
     if (e) return e;
     JoinArgs j = join_of(a, int64_t(d.dk) * d.dv);
     j.way[0] = {c.h_in, r.segs, 0};
     if ((e = start_join(j, 1, s))) return e;
   }
-  return run(a, d, pad, true, false, s);
+  return run(a, d, true, false, s);
 }
 
 int launch_linear_backward(const cc3d_linear_plan& p, const cc3d_linear_args_t& c, void* stream) {
@@ -368,7 +401,6 @@ int launch_linear_backward(const cc3d_linear_plan& p, const cc3d_linear_args_t& 
   float* part_v = part_k + space.dk;
   double* decay = reinterpret_cast<double*>(part_v + space.dv);
   const int qper = d.heads / d.q_heads, kper = d.heads / d.k_heads, vper = d.heads / d.v_heads;
-  const int pad = linear_pad(std::max(d.dk, d.dv));
   const bool dec = c.dlog_decay;
   // results go to the caller's view, or where heads are shared to partial sums [N][T][heads][D]
   auto out = [&](LinRun& r, const cc3d_rows_t& v, int per, float* part) {
@@ -442,7 +474,7 @@ int launch_linear_backward(const cc3d_linear_plan& p, const cc3d_linear_args_t& 
       a.run[a.runs++] = v;
       j.way[ways++] = {c.dh_out, grads, 1};
     }
-    if (ways && (e = run(a, d, pad, false, false, s))) return e;
+    if (ways && (e = run(a, d, false, false, s))) return e;
     if (ways && (e = start_join(j, ways, s))) return e;
   }
   a.runs = 0;
@@ -450,34 +482,37 @@ int launch_linear_backward(const cc3d_linear_plan& p, const cc3d_linear_args_t& 
     for (const LinRun* r : {&q, &k}) {  // (one after the other: the second reads what the first leaves)
       a.runs = 1;
       a.run[0] = *r;
-      if ((e = run(a, d, pad, true, true, s))) return e;
+      if ((e = run(a, d, true, true, s))) return e;
     }
     a.runs = 0;
-    e = launch(linear_decay, d.heads, 256, 0, s, decay, c.dlog_decay, 2 * d.n, d.heads, int(parts / (int64_t(d.n) * d.heads)));
-    if (e) return e;
   } else {
     if (c.dq.p) a.run[a.runs++] = q;
     if (c.dk.p) a.run[a.runs++] = k;
   }
   if (c.dv.p || c.dh_in) a.run[a.runs++] = v;
-  if (a.runs && (e = run(a, d, pad, true, false, s))) return e;
+  if (a.runs && (e = run(a, d, true, false, s))) return e;
   HeadSums sums{};
-  int jobs = 0;
   int64_t most = 0;
   auto add = [&](const cc3d_rows_t& v, int per, const float* part, int heads, int width) {
     if (!v.p || per == 1) return;
-    const int64_t el = int64_t(d.n) * d.t * heads * width;
-    sums.job[jobs++] = HeadSum{part, v.p, v.batch, v.row, el, per, width, d.t, heads};
-    most = std::max(most, el);
+    const int64_t rows = int64_t(d.n) * d.t * heads;
+    int lanes = 1;
+    while (lanes * 4 < width) lanes *= 2;
+    sums.job[sums.jobs++] = HeadSum{part, v.p, v.batch, v.row, rows, per, width, lanes, d.t, heads};
+    most = std::max(most, (rows * lanes + 255) / 256);
   };
   add(c.dq, qper, part_q, d.q_heads, d.dk);
   add(c.dk, kper, part_k, d.k_heads, d.dk);
   add(c.dv, vper, part_v, d.v_heads, d.dv);
-  if (jobs) {
+  if (dec) {
+    sums.decay = DecaySum{decay, c.dlog_decay, 2 * d.n, d.heads, int(parts / (int64_t(d.n) * d.heads))};
+    most = std::max<int64_t>(most, d.heads);
+  }
+  if (sums.jobs || dec) {
     void* at[] = {&sums};
-    const void* kernel = d.dtype == CC3D_BF16 ? reinterpret_cast<const void*>(&linear_heads<bf16_s>)
-                                              : reinterpret_cast<const void*>(&linear_heads<float>);
-    const hipError_t err = hipLaunchKernel(kernel, dim3(unsigned(std::min((most + 255) / 256, kGrid)), unsigned(jobs)),
+    const void* kernel = d.dtype == CC3D_BF16 ? reinterpret_cast<const void*>(&linear_sums<bf16_s>)
+                                              : reinterpret_cast<const void*>(&linear_sums<float>);
+    const hipError_t err = hipLaunchKernel(kernel, dim3(unsigned(std::min(most, kGrid)), unsigned(sums.jobs + (dec ? 1 : 0))),
                                            dim3(256), at, 0, s);
     if (err != hipSuccess) (void)hipGetLastError();
     return int(err);
