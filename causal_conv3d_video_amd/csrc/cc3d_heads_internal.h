@@ -34,7 +34,8 @@ namespace cc3d {
 
 constexpr int kLinTokens = 64;   // segments are multiples of so many tokens
 constexpr int kLinShort = 32;    // forward calls of up to so many tokens take them one after another
-constexpr int kLinThreads = 256; // at most, of any launch
+constexpr int kLinUnits = 256;   // compute units of a card
+constexpr int kLinThreads = 512; // at most, of any launch
 
 // Widths as the kernels pad them; tokens of a block (fp32 rows of 256 columns fill
 // 160 KB of LDS with fewer); columns of a state that a workgroup holds, 32 a wave,

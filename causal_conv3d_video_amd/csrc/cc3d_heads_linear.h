@@ -15,8 +15,8 @@
 // and value width E (of v and o).
 //
 // A workgroup walks a segment of the time axis with the state of one head in
-// registers: each of its waves has 32 columns of E, all of C, as the 32 by 32
-// results of matrix products (fp32).  What is multiplied again never passes through
+// registers, as the 32 by 32 results of matrix products (fp32): 32 columns of E and
+// all of C a wave, or half of C (SPLIT).  What is multiplied again never passes through
 // LDS on its way: the eight results of a lane in 16 rows are made neighbours by the
 // order in which rows and columns are read (`place`), so that a lane's results,
 // rounded, are its operand of the next product.  That holds for the state, which
@@ -24,6 +24,16 @@
 // all waves want those that one computed.  Operands whose tokens lie along the
 // registers are read from LDS with the transposing load.  The next block's rows load
 // while one is computed.
+//
+// Two waves with half of C each hand each other their sums over it (q S of a tile
+// of 32 tokens, through LDS) and finish one tile of tokens each.  Both round f v, but
+// with two waves a SIMD one computes while the other waits: 2048 tokens of 256 heads
+// of 64 took 106 us with a wave for all of C and take 82; of 64 by 128 the decay's
+// recurrences, 2 by 2049 tokens of 16 heads, 37 and 43 us and 32 each.  Heads of 128 by
+// 128 do so where there is a workgroup a compute unit at most (8192 tokens of 16 heads in 77
+// us instead of 79, 512 of 256 heads 46 instead of 50): two workgroups of four
+// waves do better than one of eight (512 tokens of 1024 heads, 145 us and 181).
+// Runs without outputs have nothing to hand over and little to wait for.
 //
 // With tiles of 16 by 16, the state's copy in LDS and each wave with 16 tokens of a
 // block, a compute unit took 4.7 us for 64 tokens of a 128 by 128 head with its
@@ -391,32 +401,27 @@ __device__ __forceinline__ void store_cols(T* row, int col, int width, const flo
 
 // LDS of a workgroup, in elements of T: rows of q, of k and of v, the products q.k
 // as operands; with the decay's gradient, rows of x.
-template <class T, int DP, int CB, int TOK, bool OUT, bool DEC>
+template <class T, int DP, int CB, int TOK, int SPLIT, bool OUT, bool DEC>
 struct LinTiles {
   using M = Mat<T>;
   static constexpr int kRowQ = DP + M::kPad, kRowK = DP + M::pad_both(DP), kRowV = CB + M::pad_both(CB);
   static constexpr int kK = 0, kV = kK + TOK * kRowK, kQ = kV + TOK * kRowV, kP = kQ + (OUT ? TOK * kRowQ : 0);
   static constexpr int kPairs = TOK == 64 ? 3 : 1;  // tiles of 32 by 32 pairs of tokens
   static constexpr int kX = kP + (OUT ? kPairs * 2 * 64 * 8 : 0);
-  static constexpr int kTotal = kX + (DEC ? TOK * kRowV : 0);
+  static constexpr int kE = kX + (DEC ? TOK * kRowV : 0);  // tiles that two waves hand each other
+  static constexpr int kTotal = kE + (SPLIT > 1 ? CB / 32 * SPLIT * 1024 * 4 / int(sizeof(T)) : 0);
   static constexpr int kBytes = kTotal * int(sizeof(T)) > 4096 ? kTotal * int(sizeof(T)) : 4096;
 };
 
-// Waves a SIMD that the registers are held to: what the tiles let a compute unit
-// hold, where the state allows it.
-template <class T, int DP, int CB>
-constexpr int linear_waves() {
-  return sizeof(T) == 2 && (DP == 64 || (DP == 128 && CB == 128)) ? 2 : 1;
-}
-
-template <class T, int DP, int CB, int KIND, bool OUT, bool DEC>
-__global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_run(LinArgs a) {
+template <class T, int DP, int CB, int KIND, int SPLIT, bool OUT, bool DEC>
+__global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void linear_run(LinArgs a) {
   using M = Mat<T>;
   using Frag = typename M::Frag;
   constexpr int TOK = cc3d::linear_tokens(sizeof(T), DP);  // tokens of a block
-  using L = LinTiles<T, DP, CB, TOK, OUT, DEC>;
-  constexpr int kThreads = 2 * CB, kWaves = CB / 32, kRowQ = L::kRowQ, kRowK = L::kRowK, kRowV = L::kRowV;
-  constexpr int kMt = DP / 32, kSteps = DP / 16, kIt = TOK / 32, kTs = TOK / 16;  // tiles and steps of C, of the tokens
+  using L = LinTiles<T, DP, CB, TOK, SPLIT, OUT, DEC>;
+  constexpr int kThreads = 2 * CB * SPLIT, kWaves = CB / 32 * SPLIT, kRowQ = L::kRowQ, kRowK = L::kRowK, kRowV = L::kRowV;
+  constexpr int kSteps = DP / 16, kMt = DP / 32 / SPLIT, kIt = TOK / 32, kTs = TOK / 16;  // steps of C, a wave's tiles; of the tokens
+  constexpr int kOwn = SPLIT == 1 ? kIt : 1;  // tiles of tokens whose results are the wave's
   constexpr int kVecK = TOK * DP / 8 / kThreads, kVecV = TOK * CB / 8 / kThreads;  // eights that a thread stages
   constexpr int kStepK = kThreads / (DP / 8), kStepV = kThreads / (CB / 8);
   static_assert(kVecK * kThreads * 8 == TOK * DP && kVecV * kThreads * 8 == TOK * CB, "threads");
@@ -424,6 +429,9 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
   __shared__ int odd[2];  // a block of v holds an infinity or NaN
   T* lds = reinterpret_cast<T*>(smem);
   const int tid = threadIdx.x, lane = tid % 64, wave = pin(tid / 64), il = lane % 32, hh = lane / 32;
+  const int cw = wave / SPLIT, half = wave % SPLIT, c_half = half * (kMt * 32);  // its columns, its part of C
+  const bool own = SPLIT == 1 || kIt > 1 || half == 0;
+  auto tile = [&](int x) { return SPLIT == 1 ? x : kIt > 1 ? half : 0; };
 
   // Workgroups go to the eight dies in turn, each with a cache of its own: those
   // of one head and segment (its columns, its recurrences), which read the same
@@ -494,8 +502,8 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
 
   // ---- the state before the segment: result i of tile mt is c = 32 mt + 16 (i / 8) + 8 hh + i % 8 of the lane's column
   f32x16_h st[kMt];
-  const int col = 32 * wave + place(il);  // of the lane
-  const bool has = 32 * wave < width;     // the wave has columns
+  const int col = 32 * cw + place(il);  // of the lane
+  const bool has = 32 * cw < width;     // the wave has columns
   // (unconditional loads, for the same reason as those of the rows)
   auto load_state = [&](const float* p, f32x16_h (&v)[kMt]) {
     const bool in = col < width;
@@ -504,7 +512,7 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const int c = 32 * mt + 16 * g + 8 * hh;
+        const int c = c_half + 32 * mt + 16 * g + 8 * hh;
         if (KIND == kEights && sc == 1) {
           const u32x4_by4* w = reinterpret_cast<const u32x4_by4*>(p + min(c, c_all - 8));
           const f32x4_s lo = __builtin_bit_cast(f32x4_s, w[0]), hi = __builtin_bit_cast(f32x4_s, w[1]);
@@ -529,7 +537,7 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const int c = 32 * mt + 16 * g + 8 * hh;
+        const int c = c_half + 32 * mt + 16 * g + 8 * hh;
         if (KIND == kEights) {
           if (c >= c_all) continue;
           if (sc == 1) {
@@ -657,12 +665,15 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
         }
       }
       // ---- f[i+1] q S
-      f32x16_h o[kIt];
-      auto before = [&] {
+      // (a wave's part of C, of its own tile of tokens and of the other one's, which the other wave of its columns gets)
+      f32x16_h o[kOwn], give;
+      float* box = reinterpret_cast<float*>(lds + L::kE);
+      if (has) {
 #pragma unroll
-        for (int it = 0; it < kIt; ++it) o[it] = zero16();
+        for (int x = 0; x < kOwn; ++x) o[x] = zero16();
+        give = zero16();
 #pragma unroll
-        for (int y = 0; y < kSteps; ++y) {
+        for (int y = 0; y < kSteps / SPLIT; ++y) {
           Frag sf[M::kParts];
           if constexpr (DEC) {
             if (y % 2) M::template split<1>(st[y / 2], sf);
@@ -670,31 +681,25 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
           } else {
             sf[0] = y % 2 ? M::template of<1>(st[y / 2]) : M::template of<0>(st[y / 2]);
           }
+          const T* qp = q_row + c_half + 16 * y;
 #pragma unroll
-          for (int part = 0; part < (DEC ? M::kParts : 1); ++part)
+          for (int part = 0; part < (DEC ? M::kParts : 1); ++part) {
 #pragma unroll
-            for (int it = 0; it < kIt; ++it) o[it] = M::mma(sf[part], M::row(q_row + 32 * it * kRowQ + 16 * y), o[it]);
-        }
-#pragma unroll
-        for (int it = 0; it < kIt; ++it) {
-          const float lead = inter * fade(g2, max(32 * it + il - none + r_lead, 0));
-#pragma unroll
-          for (int b = 0; b < 16; ++b) o[it][b] *= lead;
-        }
-      };
-      if (has) before();
-      if constexpr (DEC) {
-        // ... what came in, by the tokens since; and the state that another recurrence had here
-        if (has) {
-#pragma unroll
-          for (int it = 0; it < kIt; ++it) {
-            const T* xrow = lds + L::kX + (32 * it + il) * kRowV + 32 * wave + 8 * hh;
-            const int tok = 32 * it + il - none;
-            float met = 0.f;
-#pragma unroll
-            for (int b = 0; b < 16; ++b) met = fmaf(o[it][b], to_f32(xrow[16 * (b / 8) + b % 8]), met);
-            sum += tok >= 0 ? float(tok + r_lead) * met : 0.f;
+            for (int x = 0; x < kOwn; ++x) o[x] = M::mma(sf[part], M::row(qp + 32 * tile(x) * kRowQ), o[x]);
+            if constexpr (SPLIT > 1 && kIt > 1) give = M::mma(sf[part], M::row(qp + 32 * (1 - half) * kRowQ), give);
           }
+        }
+        if (SPLIT > 1 && (kIt > 1 || half == 1)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x16_h& g = kIt > 1 ? give : o[0];
+            *reinterpret_cast<f32x4_s*>(box + wave * 1024 + (i * 64 + lane) * 4) = f32x4_s{g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]};
+          }
+        }
+      }
+      if constexpr (DEC) {
+        // the state that another recurrence had here
+        if (has) {
           const int64_t at = (((nh * ((a.t + TOK - 1) / TOK) + p0 / TOK) * blocks + block) * kWaves + wave) * (kMt * 1024) + lane * 4;
           if (put) {
 #pragma unroll
@@ -717,20 +722,51 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
             sum += float(m) * (1.f + (m == TOK ? whole_m1 : last_m1)) * met;
           }
         }
-        decay += double(sum);
       }
       __syncthreads();
       if (tid == 0) odd[turn ^ 1] = 0;
-      if (has && o_p) {
+      if (has && own) {
+        if constexpr (SPLIT > 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4_s u = *reinterpret_cast<const f32x4_s*>(box + (wave ^ 1) * 1024 + (i * 64 + lane) * 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[0][4 * i + j] += u[j];
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < kOwn; ++x) {
+          const float lead = inter * fade(g2, max(32 * tile(x) + il - none + r_lead, 0));
+#pragma unroll
+          for (int b = 0; b < 16; ++b) o[x][b] *= lead;
+        }
+        if constexpr (DEC) {
+          // the decay's gradient: what came in, by the tokens since
+#pragma unroll
+          for (int x = 0; x < kOwn; ++x) {
+            const int it = tile(x);
+            const T* xrow = lds + L::kX + (32 * it + il) * kRowV + 32 * cw + 8 * hh;
+            const int tok = 32 * it + il - none;
+            float met = 0.f;
+#pragma unroll
+            for (int b = 0; b < 16; ++b) met = fmaf(o[x][b], to_f32(xrow[16 * (b / 8) + b % 8]), met);
+            sum += tok >= 0 ? float(tok + r_lead) * met : 0.f;
+          }
+        }
+      }
+      if constexpr (DEC) decay += double(sum);
+      if (has && own && o_p) {
         // ---- the products meet v
-        const T* vt = M::col_at(lds + L::kV, kRowV, lane) + 32 * wave;
+        const T* vt = M::col_at(lds + L::kV, kRowV, lane) + 32 * cw;
         const T* pp = lds + L::kP + lane * 8;
         auto meet = [&](auto&& get) {
 #pragma unroll
           for (int y = 0; y < kTs; ++y) {
+            if (SPLIT > 1 && y >= 2 && half == 0) break;
             const Frag vf = get(M::col(vt + 16 * y * kRowV, kRowV));
-            if (y < 2) o[0] = M::mma(vf, M::row(pp + y * 512), o[0]);
-            if constexpr (kIt > 1) o[1] = M::mma(vf, M::row(pp + (y + 2) * 512), o[1]);
+#pragma unroll
+            for (int x = 0; x < kOwn; ++x)
+              if (y < 2 || tile(x)) o[x] = M::mma(vf, M::row(pp + (y + 2 * tile(x)) * 512), o[x]);
           }
         };
         if (!strange) {
@@ -740,22 +776,24 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
           // sums for all, and added by itself to the tokens from its own on.
           meet([](Frag f) { return M::finite(f); });
 #pragma unroll
-          for (int it = 0; it < kIt; ++it)
-            for (int j = 0; j < 32 * it + 32; ++j) {
+          for (int x = 0; x < kOwn; ++x)
+            for (int j = 0; j < 32 * tile(x) + 32; ++j) {
+              const int it = tile(x);
               const int jl = j % 32, pair = it + j / 32;
               if (j > 32 * it + il) continue;
               const float p = to_f32(lds[L::kP + ((pair * 2 + jl / 16) * 64 + jl % 16 / 8 * 32 + il) * 8 + j % 8]);
-              const T* row = lds + L::kV + j * kRowV + 32 * wave + 8 * hh;
+              const T* row = lds + L::kV + j * kRowV + 32 * cw + 8 * hh;
 #pragma unroll
               for (int b = 0; b < 16; ++b) {
                 const float u = to_f32(row[16 * (b / 8) + b % 8]);
-                if (!(__builtin_fabsf(u) < __builtin_inff())) o[it][b] = fmaf(p, u, o[it][b]);
+                if (!(__builtin_fabsf(u) < __builtin_inff())) o[x][b] = fmaf(p, u, o[x][b]);
               }
             }
         }
         const int64_t t = o_at + int64_t(p0) * o_row;
 #pragma unroll
-        for (int it = 0; it < kIt; ++it) {
+        for (int x = 0; x < kOwn; ++x) {
+          const int it = tile(x);
           const int tok = 32 * it + il - none;
           if (tok < 0) continue;
           const int64_t at = t + int64_t(unsigned(rev ? m - 1 - tok : tok) * uint64_t(o_row));
@@ -763,8 +801,8 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
           for (int g = 0; g < 2; ++g) {
             float u[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = o[it][8 * g + i];
-            const int e = 32 * wave + 16 * g + 8 * hh;
+            for (int i = 0; i < 8; ++i) u[i] = o[x][8 * g + i];
+            const int e = 32 * cw + 16 * g + 8 * hh;
             if (o_f32) store_cols<float, KIND>(reinterpret_cast<float*>(o_p) + at, e, width, u);
             else store_cols<T, KIND>(reinterpret_cast<T*>(o_p) + at, e, width, u);
           }
@@ -782,8 +820,8 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
         for (int b = 0; b < 16; ++b) {
           st[mt][b] = fmaf(st[mt][b], m1, st[mt][b]);
         }
-      const T* kt = M::col_at(lds + L::kK, kRowK, lane);
-      const T* vt = M::col_at(lds + L::kV, kRowV, lane) + 32 * wave;
+      const T* kt = M::col_at(lds + L::kK, kRowK, lane) + c_half;
+      const T* vt = M::col_at(lds + L::kV, kRowV, lane) + 32 * cw;
 #pragma unroll
       for (int y = 0; y < kTs; ++y) {
         const Frag vf = M::col(vt + 16 * y * kRowV, kRowV);
@@ -832,18 +870,18 @@ __global__ __launch_bounds__(2 * CB, (linear_waves<T, DP, CB>())) void linear_ru
   }
 }
 
-template <class T, int DP, int CB, int KIND, bool OUT, bool DEC>
+template <class T, int DP, int CB, int KIND, int SPLIT, bool OUT, bool DEC>
 int start_run(const LinArgs& a, int64_t workgroups, hipStream_t s) {
-  constexpr int lds = LinTiles<T, DP, CB, cc3d::linear_tokens(sizeof(T), DP), OUT, DEC>::kBytes;
+  constexpr int lds = LinTiles<T, DP, CB, cc3d::linear_tokens(sizeof(T), DP), SPLIT, OUT, DEC>::kBytes;
+  constexpr auto kernel = linear_run<T, DP, CB, KIND, SPLIT, OUT, DEC>;
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&linear_run<T, DP, CB, KIND, OUT, DEC>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) {
       (void)hipGetLastError();
       return int(e);
     }
   }
-  return launch(linear_run<T, DP, CB, KIND, OUT, DEC>, workgroups, 2 * CB, lds, s, a);
+  return launch(kernel, workgroups, 2 * CB * SPLIT, lds, s, a);
 }
 
 template <class T, int KIND>
@@ -859,9 +897,12 @@ int start_runs(LinArgs& a, int pad, bool out, bool dec, hipStream_t s) {
   const int64_t workgroups = (int64_t(a.units) + 7) / 8 * 8 * a.parts;
   auto go = [&](auto d, auto c) {
     constexpr int DP = decltype(d)::value, CB = decltype(c)::value;
-    if (!out) return start_run<T, DP, CB, KIND, false, false>(a, workgroups, s);
-    return dec ? start_run<T, DP, CB, KIND, true, true>(a, workgroups, s)
-               : start_run<T, DP, CB, KIND, true, false>(a, workgroups, s);
+    if (!out) return start_run<T, DP, CB, KIND, 1, false, false>(a, workgroups, s);
+    if (dec) return start_run<T, DP, CB, KIND, 2, true, true>(a, workgroups, s);
+    if constexpr (sizeof(T) == 2 && DP == 128 && CB == 128) {
+      if (workgroups > cc3d::kLinUnits) return start_run<T, DP, CB, KIND, 1, true, false>(a, workgroups, s);
+    }
+    return start_run<T, DP, CB, KIND, 2, true, false>(a, workgroups, s);
   };
   const std::integral_constant<int, 64> c64;
   const std::integral_constant<int, 128> c128;
