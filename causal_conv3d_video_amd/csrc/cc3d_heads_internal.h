@@ -7,6 +7,7 @@
 
 struct cc3d_linear_plan {
   cc3d_linear_desc_t d{};
+  bool steps = false;     // forward: the tokens one after another
   cc3d_seq_info_t info{};
   int32_t seg = 0, segs = 1;          // forward: tokens of a segment of the time axis (a multiple of 64), segments
   int32_t bwd_seg = 0, bwd_segs = 1;  // the same of the backward call
@@ -33,7 +34,7 @@ namespace cc3d {
 // --- linear attention
 
 constexpr int kLinTokens = 64;   // segments are multiples of so many tokens
-constexpr int kLinShort = 32;    // forward calls of up to so many tokens take them one after another
+constexpr int kLinFew = 32;      // tokens of a block in bf16 calls of no more
 constexpr int kLinUnits = 256;   // compute units of a card
 constexpr int kLinThreads = 512; // at most, of any launch
 

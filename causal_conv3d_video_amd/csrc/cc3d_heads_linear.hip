@@ -355,7 +355,7 @@ namespace cc3d {
 int launch_linear_forward(const cc3d_linear_plan& p, const cc3d_linear_args_t& c, void* stream) {
   const auto& d = p.d;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (d.t <= kLinShort) {
+  if (p.steps) {
     const ShortArgs a{c.q.p, c.k.p, c.v.p, c.o.p, c.q.batch, c.k.batch, c.v.batch, c.o.batch, c.q.row, c.k.row, c.v.row,
                       c.o.row, d.heads / d.q_heads, d.heads / d.k_heads, d.heads / d.v_heads, d.heads, d.t, d.dk, d.dv,
                       int((d.dv + 63) / 64), d.scale, c.log_decay, c.h_in, c.h_out, c.lengths};

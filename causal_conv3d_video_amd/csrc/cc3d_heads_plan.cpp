@@ -47,6 +47,17 @@ void split_time(int32_t t, int64_t units, int cols, int32_t* seg, int32_t* segs)
   *segs = int32_t(ceildiv(blocks, each));
 }
 
+// Forward calls that take their tokens one after another: one or two of them, up to
+// eight where the states are few enough that only latency counts, and in fp32, whose
+// matrix products are no faster than its vector ones, up to 32.  bf16, both ways (one
+// after another, and as a block): 128 sequences of 16 heads of 128, 71 and 61 us for 2
+// tokens and 98 and 65 for 8; 1560 of 6 heads of 64, 85 and 77 and 97 and 80; 64 of 12
+// heads of 64, 8.2 and 10.5 and 9.7 and 10.6.  fp32: 1560 of 6 heads of 64, 32 tokens, 207 and 260.
+bool linear_steps(const cc3d_linear_desc_t& d, int64_t workgroups) {
+  if (d.dtype != CC3D_BF16) return d.t <= 32;
+  return d.t <= 2 || (d.t <= 8 && workgroups <= 4 * kUnits);
+}
+
 }  // namespace
 
 extern "C" cc3d_status_t linear_attention_plan(const cc3d_linear_desc_t* d, cc3d_linear_plan_t* out) {
@@ -67,7 +78,8 @@ extern "C" cc3d_status_t linear_attention_plan(const cc3d_linear_desc_t* d, cc3d
   if (!cc3d::fits(units + 7 * blocks, cc3d::kLinThreads) || !cc3d::fits(short_units, cc3d::kLinThreads)) return refuse(CC3D_ERR_UNSUPPORTED);
   auto* p = make_plan<cc3d_linear_plan>(d);
   if (!p) return CC3D_ERR_NO_MEMORY;
-  if (d->t > cc3d::kLinShort) split_time(d->t, units, cc3d::linear_cols(d->dv), &p->seg, &p->segs);
+  p->steps = linear_steps(*d, short_units);
+  if (!p->steps) split_time(d->t, units, cc3d::linear_cols(d->dv), &p->seg, &p->segs);
   const int cols = cc3d::linear_cols(int(widest));
   // Backward: by dq's recurrence, which is a launch by itself where the decay's gradient is asked for (2 by 2049
   // tokens, 16 heads, 64 by 128: 154 us at 11 segments, 174 at 7, 186 at 17).
