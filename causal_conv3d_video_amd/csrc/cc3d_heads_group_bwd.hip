@@ -314,10 +314,13 @@ int launch_group_backward(const cc3d_group_plan& p, const cc3d_group_args_t& c, 
     return launch_sums(jobs, 2, stream);
   }
   if (!a.stats_in) {
-    float* stats = w + a.blocks * 2 * a.c + int64_t(a.n) * 2 * a.c;
-    if ((e = launch_group_stats(p, c, w, stats, stream))) return e;  // (its runs' moments where the sums come to be)
+    float* stats = w + p.bwd_stats;
+    if ((e = launch_group_stats(p, c, w, stats, stream))) return e;
     a.stats_in = stats;
   }
+  a.rows = p.bwd_rows;
+  a.splits = p.bwd_splits;
+  a.blocks = int64_t(a.n) * a.splits;
   a.part = w;
   a.chan = w + a.blocks * 2 * a.c;
   if ((e = pick_group<RunSums>(p.d, a, s))) return e;

@@ -26,6 +26,8 @@ struct cc3d_group_plan {
   cc3d_seq_info_t info{};
   int32_t splits = 0;      // workgroups per sample; 0: whole samples in a workgroup's registers
   int32_t rows = 0;        // positions of a split
+  int32_t bwd_splits = 0, bwd_rows = 0;  // the same of the backward call
+  int64_t bwd_stats = 0;   // split: where the statistics are in the backward call's workspace, in floats
   int64_t workers = 0;     // whole samples: workgroups
 };
 

@@ -252,18 +252,24 @@ extern "C" cc3d_status_t group_norm_plan(const cc3d_group_desc_t* d, cc3d_group_
     return refuse(CC3D_ERR_INVALID_ARG);
   if (d->c > 8192 || d->p > kMaxTokens || !within_span({d->n, d->p, d->c})) return refuse(CC3D_ERR_UNSUPPORTED);
   const int lanes = cc3d::group_lanes(d->c), threads = cc3d::group_threads(d->c), lines = threads / lanes;
-  int64_t splits = 0, rows = 0, workers = 0;
+  int64_t splits = 0, rows = 0, bwd_splits = 0, bwd_rows = 0, workers = 0;
   if (d->p <= lines * cc3d::kGroupRows) {
     int64_t line_n = 1;
     while (line_n * cc3d::kGroupRows < d->p) line_n *= 2;
     // (every workgroup of the backward call leaves a row of partial sums)
     workers = std::min<int64_t>(ceildiv(d->n, lines / line_n), 8 * kUnits);
   } else {
-    // Runs of rows: eight workgroups of 256 threads a compute unit, at least two steps of a thread each.
-    splits = std::max<int64_t>(1, std::min<int64_t>(ceildiv(8 * kUnits * 256 / threads, d->n),
-                                                    d->p / (2 * lines * cc3d::kGroupRows)));
-    rows = ceildiv(ceildiv(d->p, splits), lines) * lines;
-    splits = ceildiv(d->p, rows);
+    // Runs of rows: eight workgroups of 256 threads a compute unit, in the backward call, whose threads hold more,
+    // four (17 samples of 1560 positions, 515 fp32 channels, 48 us and 52 with eight; three of 57600, 384 channels of
+    // bf16, 150 both; four of 230400, 192 channels, forward, 219 and with four 231), at least two steps of a thread each.
+    auto cut = [&](int each, int64_t* runs, int64_t* of) {
+      *runs = std::max<int64_t>(1, std::min<int64_t>(ceildiv(each * kUnits * 256 / threads, d->n),
+                                                     d->p / (2 * lines * cc3d::kGroupRows)));
+      *of = ceildiv(ceildiv(d->p, *runs), lines) * lines;
+      *runs = ceildiv(d->p, *of);
+    };
+    cut(8, &splits, &rows);
+    cut(4, &bwd_splits, &bwd_rows);
     const int64_t others = std::max<int64_t>(ceildiv(int64_t(d->n) * d->groups, 4) * 256,
                                              int64_t(d->n) * ceildiv(2 * d->c, 64) * 1024);
     if (!cc3d::fits(int64_t(d->n) * splits, threads) || others > cc3d::kMaxThreads) return refuse(CC3D_ERR_UNSUPPORTED);
@@ -272,12 +278,17 @@ extern "C" cc3d_status_t group_norm_plan(const cc3d_group_desc_t* d, cc3d_group_
   if (!p) return CC3D_ERR_NO_MEMORY;
   p->splits = int32_t(splits);
   p->rows = int32_t(rows);
+  p->bwd_splits = int32_t(bwd_splits);
+  p->bwd_rows = int32_t(bwd_rows);
   p->workers = workers;
-  p->info.chunks = p->info.backward_chunks = int32_t(std::max<int64_t>(splits, 1));
+  p->info.chunks = int32_t(std::max<int64_t>(splits, 1));
+  p->info.backward_chunks = int32_t(std::max<int64_t>(bwd_splits, 1));
   const int64_t stats = int64_t(d->n) * d->groups * 2;
   if (splits) {
     p->info.workspace_bytes = (stats * splits + stats) * 4;
-    p->info.backward_workspace_bytes = ((splits + 1) * d->n * 2 * d->c + stats) * 4;
+    // (the forward runs' moments lie where the sums come to be)
+    p->bwd_stats = std::max((bwd_splits + 1) * d->n * 2 * d->c, splits * stats);
+    p->info.backward_workspace_bytes = (p->bwd_stats + stats) * 4;
   } else {
     p->info.backward_workspace_bytes = workers * 2 * d->c * 4;
   }

@@ -43,7 +43,7 @@ int main() {
             cc3d_seq_info_t info;
             expect(linear_attention_plan_info(p, &info) == CC3D_OK, "linear info");
             expect(info.workspace_bytes >= 0 && info.backward_workspace_bytes > 0, "linear sizes");
-            expect(t <= cc3d::kLinShort ? p->segs == 1 : p->seg % cc3d::kLinTokens == 0 && int64_t(p->seg) * p->segs >= t &&
+            expect(p->steps ? p->segs == 1 : p->seg % cc3d::kLinTokens == 0 && int64_t(p->seg) * p->segs >= t &&
                                                              int64_t(p->seg) * (p->segs - 1) < t, "linear segments");
             expect(p->bwd_seg % cc3d::kLinTokens == 0 && int64_t(p->bwd_seg) * p->bwd_segs >= t &&
                        int64_t(p->bwd_seg) * (p->bwd_segs - 1) < t, "linear backward segments");
@@ -107,6 +107,9 @@ int main() {
           expect(group_norm_plan_info(p, &info) == CC3D_OK && info.backward_workspace_bytes > 0, "group info");
           expect(p->splits ? int64_t(p->rows) * p->splits >= p0 && int64_t(p->rows) * (p->splits - 1) < p0 : p->workers >= 1,
                  "group runs");
+          expect(!p->bwd_splits == !p->splits && (!p->splits || (int64_t(p->bwd_rows) * p->bwd_splits >= p0 &&
+                 int64_t(p->bwd_rows) * (p->bwd_splits - 1) < p0 && p->bwd_stats >= int64_t(p->splits) * n * g * 2)),
+                 "group runs backward");
           cc3d_group_args_t a{};
           a.x = {at(0), int64_t(p0) * c, c};
           a.y = {at(1), int64_t(p0) * c, c};
