@@ -872,6 +872,7 @@ __global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void line
 template <class T, int DP, int CB, int TOK, int KIND, int SPLIT, bool OUT, bool DEC>
 int start_run(const LinArgs& a, int64_t workgroups, hipStream_t s) {
   constexpr int lds = LinTiles<T, DP, CB, TOK, SPLIT, OUT, DEC>::kBytes;
+  static_assert(lds + 8 <= 160 * 1024, "LDS of a compute unit");
   constexpr auto kernel = linear_run<T, DP, CB, TOK, KIND, SPLIT, OUT, DEC>;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -897,7 +898,11 @@ int start_runs(LinArgs& a, int pad, bool out, bool dec, hipStream_t s) {
   auto go = [&](auto d, auto c) {
     constexpr int DP = decltype(d)::value, CB = decltype(c)::value, TOK = cc3d::linear_tokens(sizeof(T), DP);
     if (!out) return start_run<T, DP, CB, TOK, KIND, 1, false, false>(a, workgroups, s);
-    if (dec) return start_run<T, DP, CB, TOK, KIND, 2, true, true>(a, workgroups, s);
+    if (dec) {
+      // (128 by 128 in fp32 leave no room for the handed tiles)
+      constexpr int kSplit = LinTiles<T, DP, CB, TOK, 2, true, true>::kBytes + 8 <= 160 * 1024 ? 2 : 1;
+      return start_run<T, DP, CB, TOK, KIND, kSplit, true, true>(a, workgroups, s);
+    }
     // (a block of 32 tokens in place of one of 64: 17 tokens of 1560 sequences, 6 heads of 64, in 87 us instead
     // of 109; of 128 sequences, 16 heads of 128, in 68 instead of 75)
     if constexpr (sizeof(T) == 2 && DP <= 128) {

@@ -94,6 +94,10 @@ LINEAR = [
     (2, 300, 2, (2, 2, 2), 64, 64, F32, 0, 0, True, None),
     (1, 515, 5, (5, 1, 1), 50, 100, F32, 0, 2, True, "some"),
     (3, 700, 2, (1, 2, 2), 128, 128, BF, 1, 0, True, "some"),
+    (2, 130, 2, (2, 1, 2), 128, 128, F32, 1, 0, True, "some"),
+    (1, 90, 3, (3, 3, 3), 70, 125, F32, 0, 1, True, "some"),
+    (2, 100, 2, (2, 2, 1), 256, 40, F32, 1, 0, True, "some"),
+    (2, 90, 1, (1, 1, 1), 200, 100, BF, 1, 0, True, "some"),
     (33, 70, 8, (2, 8, 8), 128, 128, BF, 1, 0, True, "some"),  # more heads than compute units
 ]
 
