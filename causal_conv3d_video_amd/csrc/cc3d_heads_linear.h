@@ -898,15 +898,18 @@ int start_runs(LinArgs& a, int pad, bool out, bool dec, hipStream_t s) {
   auto go = [&](auto d, auto c) {
     constexpr int DP = decltype(d)::value, CB = decltype(c)::value, TOK = cc3d::linear_tokens(sizeof(T), DP);
     if (!out) return start_run<T, DP, CB, TOK, KIND, 1, false, false>(a, workgroups, s);
+    // (a block of 32 tokens in place of one of 64: 17 tokens of 1560 sequences, 6 heads of 64, in 87 us instead
+    // of 109; of 128 sequences, 16 heads of 128, in 68 instead of 75; with the decay's gradient 6 of 977, 6 heads of 16
+    // by 50, in 174 instead of 258)
+    if constexpr (sizeof(T) == 2 && DP <= 128) {
+      if (a.t <= cc3d::kLinFew)
+        return dec ? start_run<T, DP, CB, 32, KIND, 1, true, true>(a, workgroups, s)
+                   : start_run<T, DP, CB, 32, KIND, 1, true, false>(a, workgroups, s);
+    }
     if (dec) {
       // (128 by 128 in fp32 leave no room for the handed tiles)
       constexpr int kSplit = LinTiles<T, DP, CB, TOK, 2, true, true>::kBytes + 8 <= 160 * 1024 ? 2 : 1;
       return start_run<T, DP, CB, TOK, KIND, kSplit, true, true>(a, workgroups, s);
-    }
-    // (a block of 32 tokens in place of one of 64: 17 tokens of 1560 sequences, 6 heads of 64, in 87 us instead
-    // of 109; of 128 sequences, 16 heads of 128, in 68 instead of 75)
-    if constexpr (sizeof(T) == 2 && DP <= 128) {
-      if (a.t <= cc3d::kLinFew) return start_run<T, DP, CB, 32, KIND, 1, true, false>(a, workgroups, s);
     }
     if constexpr (sizeof(T) == 2 && DP == 128 && CB == 128) {
       if (workgroups > cc3d::kLinUnits) return start_run<T, DP, CB, TOK, KIND, 1, true, false>(a, workgroups, s);
