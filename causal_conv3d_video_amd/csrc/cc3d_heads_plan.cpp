@@ -33,11 +33,11 @@ namespace {
 // Segments of the time axis, whole blocks of 64 tokens, where `units` workgroups
 // alone leave compute units idle: as many as make one workgroup of four waves or two
 // of two (64 columns of a state and fewer) a compute unit, rounded down.  8192 tokens
-// of 16 heads of 128 in 71 us at 16 segments, 73 at 32 and 104 at 8; of 64 in 42 at 32,
-// 50 at 16.  Two segments cost their second walk over the tokens and gain little: 192
-// heads of 128, 1024 tokens, 67 us whole and 94 in two, 256 heads of 64 of 2048 tokens
-// 99 and 105; 128 of 128, 2048 tokens, 124 and 126, in four 117.  512 tokens of 4 heads
-// in 17 us block by block and 28 in two.
+// of 16 heads of 128 in 70 to 75 us at 16 segments, 77 at 32 and 109 at 8; of 64 in 41 at
+// 32, 43 at 16.  Two segments cost their second walk over the tokens and gain little: 192
+// heads of 128, 1024 tokens, 69 us whole and 99 in two, 256 heads of 64 of 2048 tokens
+// 75 and 91; 128 of 128, 2048 tokens, 126 and 132, in four 123.  512 tokens of 4 heads
+// in 16 us block by block and 25 in two.
 void split_time(int32_t t, int64_t units, int cols, int32_t* seg, int32_t* segs) {
   const int64_t blocks = ceildiv(t, cc3d::kLinTokens), want = cols == 64 ? 2 * kUnits : kUnits;
   int64_t pieces = std::min(want / units, blocks);
@@ -82,7 +82,7 @@ extern "C" cc3d_status_t linear_attention_plan(const cc3d_linear_desc_t* d, cc3d
   if (!p->steps) split_time(d->t, units, cc3d::linear_cols(d->dv), &p->seg, &p->segs);
   const int cols = cc3d::linear_cols(int(widest));
   // Backward: by dq's recurrence, which is a launch by itself where the decay's gradient is asked for (2 by 2049
-  // tokens, 16 heads, 64 by 128: 154 us at 11 segments, 174 at 7, 186 at 17).
+  // tokens, 16 heads, 64 by 128: 129 us at 11 segments, 131 at 7, 152 at 17).
   const int64_t of_k = cc3d::linear_blocks(d->dk, cols), of_v = cc3d::linear_blocks(d->dv, cols);
   split_time(d->t, nh * of_k, cc3d::linear_cols(d->dk), &p->bwd_seg, &p->bwd_segs);
   p->bwd_fits = cc3d::fits((nh + 7) * (2 * of_k + of_v), cc3d::kLinThreads);  // (where it is split it is far below)
