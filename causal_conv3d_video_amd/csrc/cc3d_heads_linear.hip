@@ -174,6 +174,7 @@ struct JoinArgs {
   struct Way {
     const float* from;  // [N][H][size], or null
     float* segs;        // [N][H][segments - 1][size]: what a segment adds; becomes the state between two
+    float* copy;        // of `from`, or null
     int rev;            // from the last segment to the first
   } way[2];
   int64_t items, size;  // states of all heads, floats of one
@@ -196,6 +197,7 @@ __global__ __launch_bounds__(256) void linear_join(JoinArgs a) {
     float* p = w.segs + (nh * between + (w.rev ? between - 1 : 0)) * a.size + off;
     const int64_t step = w.rev ? -a.size : a.size;
     float s = w.from ? w.from[item] : 0.f;
+    if (w.copy) w.copy[item] = s;
     for (int x0 = 0; x0 < between; x0 += 8) {
       float u[8];
 #pragma unroll
@@ -383,7 +385,10 @@ int launch_linear_forward(const cc3d_linear_plan& p, const cc3d_linear_args_t& c
     int e = run(a, d, false, false, s);
     if (e) return e;
     JoinArgs j = join_of(a, int64_t(d.dk) * d.dv);
-    j.way[0] = {c.h_in, r.segs, 0};
+    // (the last segment may be done before the first one reads its state: not from where the last one's goes)
+    float* copy = c.h_in && c.h_in == c.h_out ? r.segs + j.items * (a.segs - 1) : nullptr;
+    j.way[0] = {c.h_in, r.segs, copy, 0};
+    if (copy) r.from = copy;
     if ((e = start_join(j, 1, s))) return e;
   }
   return run(a, d, true, false, s);
@@ -468,11 +473,11 @@ int launch_linear_backward(const cc3d_linear_plan& p, const cc3d_linear_args_t& 
     int ways = 0;
     if (forth) {
       a.run[a.runs++] = q;
-      j.way[ways++] = {c.h_in, states, 0};
+      j.way[ways++] = {c.h_in, states, nullptr, 0};
     }
     if (back) {
       a.run[a.runs++] = v;
-      j.way[ways++] = {c.dh_out, grads, 1};
+      j.way[ways++] = {c.dh_out, grads, nullptr, 1};
     }
     if (ways && (e = run(a, d, false, false, s))) return e;
     if (ways && (e = start_join(j, ways, s))) return e;

@@ -88,7 +88,8 @@ extern "C" cc3d_status_t linear_attention_plan(const cc3d_linear_desc_t* d, cc3d
   p->bwd_fits = cc3d::fits((nh + 7) * (2 * of_k + of_v), cc3d::kLinThreads);  // (where it is split it is far below)
   p->info.chunks = p->segs;
   p->info.backward_chunks = p->bwd_segs;
-  p->info.workspace_bytes = nh * (p->segs - 1) * d->dk * d->dv * 4;
+  // (states between segments, and a copy of h_in for calls in place)
+  p->info.workspace_bytes = p->segs > 1 ? nh * p->segs * d->dk * d->dv * 4 : 0;
   p->info.backward_workspace_bytes = cc3d::linear_bwd_space(*p).total * 4;
   *out = p;
   return CC3D_OK;

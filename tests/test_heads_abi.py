@@ -89,7 +89,7 @@ def test_codes_that_python_does_not_make():
 def test_plan_sizes():
     assert linear(t=32, h=2).info["workspace_bytes"] == 0            # short calls take token after token
     p = linear(t=8192, h=2, dk=64, dv=64)
-    assert p.info["chunks"] > 1 and p.info["workspace_bytes"] == 2 * (p.info["chunks"] - 1) * 64 * 64 * 4
+    assert p.info["chunks"] > 1 and p.info["workspace_bytes"] == 2 * p.info["chunks"] * 64 * 64 * 4
     assert linear(n=4096, t=64, h=2).info["workspace_bytes"] == 0    # enough heads to fill the card
     # a state for each block of 64 tokens, padded, and shared heads' sums
     assert p.info["backward_workspace_bytes"] >= 2 * 128 * 64 * 64 * 4

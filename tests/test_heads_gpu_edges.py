@@ -148,6 +148,49 @@ def test_state_in_place(cuda_device, t):
     same(state, want["h_out"])
 
 
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (50, 40)])
+@pytest.mark.parametrize("ragged", [[1, 2900, 65, 0], [3000, 64, 130, 1]])
+def test_state_in_place_of_short_sequences_in_a_long_call(cuda_device, ragged, dk, dv):
+    """The time axis is split, and its last parts have no tokens: their state goes where the first part's came from."""
+    c = Linear(4, 3000, 4, dk, dv, ragged=ragged)
+    assert c.plan.info["chunks"] > 3
+    want = c.forward()
+    for _ in range(5):
+        state, o = c.i["h_in"].clone(), nan(4, 3000, 4, dv, dtype=BF)
+        cc3d.linear_attention_forward(c.plan, c.i["q"], c.i["k"], c.i["v"], o, log_decay=c.i["log_decay"], h_in=state, h_out=state,
+                                      lengths=c.lengths, workspace=c.space)
+        torch.cuda.synchronize()
+        same(o, want["o"])
+        same(state, want["h_out"])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_buffer_holds_q_k_and_v(cuda_device, dtype):
+    """q, k and v as parts of one projection's rows, rotary in place there, and their gradients as parts of another."""
+    n, t, h, d = 2, 150, 4, 32
+    c = Linear(n, t, h, d, d, dtype=dtype)
+    plan = cc3d.rotary_plan(cc3d.make_rotary_desc(n, t, h, h, d, dtype=dtype))
+    qo, ko = nan(n, t, h, d, dtype=dtype), nan(n, t, h, d, dtype=dtype)
+    cc3d.rotary_forward(plan, c.i["q"], c.i["k"], qo, ko)
+    want, back = c.forward(q=qo, k=ko), c.backward(q=qo, k=ko)
+    rows = torch.cat([c.i[x].reshape(n, t, h * d) for x in ("q", "k", "v")], 2)
+    q, k, v = (rows[..., h * d * i:h * d * (i + 1)] for i in range(3))
+    cc3d.rotary_forward(plan, q, k, q, k)
+    got = c.forward(q=q, k=k, v=v)
+    grads = nan(n, t, 3 * h * d, dtype=dtype)
+    dq, dk, dv = (grads[..., h * d * i:h * d * (i + 1)] for i in range(3))
+    dlog, dh = nan(h), nan(n, h, d, d)
+    cc3d.linear_attention_backward(c.plan, q, k, v, c.i["do"], log_decay=c.i["log_decay"], h_in=c.i["h_in"], dh_out=c.i["dh_out"],
+                                   dq=dq, dk=dk, dv=dv, dlog_decay=dlog, dh_in=dh, workspace=c.back_space)
+    torch.cuda.synchronize()
+    for x in ("o", "h_out"):
+        same(got[x], want[x], x)
+    for x, g in (("dq", dq), ("dk", dk), ("dv", dv)):
+        same(g.unflatten(-1, (h, d)), back[x], x)
+    same(dlog, back["dlog_decay"])
+    same(dh, back["dh_in"])
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_streamed_chunks_follow_one_call(cuda_device, dtype):
     """Chunks of 1, 5, 64, 130 and 1 tokens against one call over 201: each is within its own bound of the 64-bit form."""
