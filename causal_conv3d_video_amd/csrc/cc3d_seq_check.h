@@ -140,6 +140,7 @@ class Check {
         if (!(r_[i].out || r_[j].out)) continue;
         bool same = false;
         for (int k = 0; k < same_n_; ++k) same |= r_[i].base == same_[k] && identical(r_[i], r_[j]);
+        if (same && alike(r_[i]) > 2) return false;  // a third use of it: another input that is read, or written twice
         if (!same && intersect(r_[i], r_[j])) return false;
       }
     return true;
@@ -149,6 +150,11 @@ class Check {
   static constexpr int kMax = 32, kMaxSame = 2;
   static bool identical(const Region& a, const Region& b) {
     return a.base == b.base && a.batch == b.batch && a.row == b.row && a.n == b.n && a.t == b.t && a.width == b.width;
+  }
+  int alike(const Region& r) const {
+    int count = 0;
+    for (int i = 0; i < n_; ++i) count += identical(r_[i], r);
+    return count;
   }
   void add(const Region& r) {
     if (n_ < kMax) r_[n_++] = r;

@@ -181,6 +181,16 @@ def test_rotary_argument_refusals(fn):
     _status(fn, plan, _rotary()[1])                                    # k in a plan without k heads
 
 
+@pytest.mark.parametrize("fn", ["rotary_forward", "rotary_backward"])
+def test_rotary_refuses_one_buffer_for_q_and_k_that_is_written(fn):
+    n, t, h, d = 2, 10, 4, 8
+    for q, k, q_out, k_out in ((0, 0, 0, 0), (0, 0, 0, 1), (0, 0, 1, 0), (0, 1, 0, 0), (0, 1, 1, 1), (0, 1, 2, 2), (0, 1, 1, 0)):
+        plan, a = rotary(n, t, h, h, d), heads.RotaryArgs()
+        for name, slot in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)):
+            setattr(a, name, _rows(slot, t * h * d, h * d))
+        _status(fn, plan, a)
+
+
 def _group(**kw):
     n, p, c, g = 2, 3000, 16, 4
     plan = group(n, p, c, g, **kw)
