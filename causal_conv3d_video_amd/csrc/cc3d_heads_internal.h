@@ -36,7 +36,7 @@ namespace cc3d {
 // --- linear attention
 
 constexpr int kLinTokens = 64;   // segments are multiples of so many tokens
-constexpr int kLinFew = 32;      // tokens of a block in bf16 calls of no more
+constexpr int kLinFew = 32;      // tokens of a block in calls of no more
 constexpr int kLinUnits = 256;   // compute units of a card
 constexpr int kLinThreads = 512; // at most, of any launch
 

@@ -900,8 +900,8 @@ int start_runs(LinArgs& a, int pad, bool out, bool dec, hipStream_t s) {
     if (!out) return start_run<T, DP, CB, TOK, KIND, 1, false, false>(a, workgroups, s);
     // (a block of 32 tokens in place of one of 64: 17 tokens of 1560 sequences, 6 heads of 64, in 87 us instead
     // of 109; of 128 sequences, 16 heads of 128, in 68 instead of 75; with the decay's gradient 6 of 977, 6 heads of 16
-    // by 50, in 174 instead of 258)
-    if constexpr (sizeof(T) == 2 && DP <= 128) {
+    // by 50, in 174 instead of 258, 4 of 1541, 6 heads of 16 by 64 in fp32, in 491 instead of 972)
+    if constexpr (DP <= 128) {
       if (a.t <= cc3d::kLinFew)
         return dec ? start_run<T, DP, CB, 32, KIND, 1, true, true>(a, workgroups, s)
                    : start_run<T, DP, CB, 32, KIND, 1, true, false>(a, workgroups, s);
