@@ -184,8 +184,8 @@ struct JoinArgs {
   const int* lengths;
 };
 
-// States across segments: after[s] = f[tokens of s] before[s] + added[s].  Eight
-// segments' loads are in flight.
+// States across segments: after[s] = f[tokens of s] before[s] + added[s], the factor
+// and its product in 64 bits.  Eight segments' loads are in flight.
 __global__ __launch_bounds__(256) void linear_join(JoinArgs a) {
   const JoinArgs::Way w = a.way[blockIdx.y];
   const int between = a.segs - 1;
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(256) void linear_join(JoinArgs a) {
     const int64_t nh = item / a.size, off = item - nh * a.size, n = nh / a.heads;
     const float g = a.log_decay ? a.log_decay[nh - n * a.heads] : 0.f;
     const int len = valid_tokens(a.lengths, int(n), a.t);
-    const float whole = fade_m1(g, a.seg);
+    const double whole = fade64(g, a.seg);
     // (slot x lies between segments x and x + 1)
     float* p = w.segs + (nh * between + (w.rev ? between - 1 : 0)) * a.size + off;
     const int64_t step = w.rev ? -a.size : a.size;
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(256) void linear_join(JoinArgs a) {
         if (x0 + x >= between) break;
         const int segment = w.rev ? between - x0 - x : x0 + x;
         const int tokens = min(max(len - segment * a.seg, 0), a.seg);
-        s = fmaf(s, tokens == a.seg ? whole : fade_m1(g, tokens), s) + u[x];
+        s = float(fma(double(s), tokens == a.seg ? whole : fade64(g, tokens), double(u[x])));
         p[(x0 + x) * step] = s;
       }
     }

@@ -1,0 +1,81 @@
+"""linear_attention's decay on the GPU where nothing covers it: old states that
+fade strongly beside little or nothing that is added.
+
+Bounds.  A state that only fades is rounded once a block and once a segment,
+by half a step of 2^-24, and its factor once or twice.  Calls of up to 32
+tokens may take them one after another: a factor each, off by its exponent's
+rounding (|g| log2(e) / 2 steps of 2^-24, times ln 2) and the exponential's one
+or two units, and a rounding of the product: old_depth.
+"""
+import pytest
+import torch
+
+import causal_conv3d_video_amd as cc3d
+import heads_oracle as ho
+from test_heads_gpu import BF, DEV, F32, d64, near
+from test_heads_gpu_edges import Linear
+from test_seq_gpu import dev, nan, space
+
+pytestmark = pytest.mark.gpu
+
+
+def old_depth(t, g):
+    return 12 + t / 32 + min(t, 32) * (3 + float(g.abs().max()))
+
+
+def positive(gen, *shape):
+    return dev(0.5 + torch.rand(*shape, generator=gen))
+
+
+# exp(g t) from 1e-4 to 1e-20 and beyond
+FADES = [(1, -14.0), (1, -1.0), (2, -7.0), (9, -1.5), (20, -0.9), (40, -0.4), (64, -0.2), (64, -0.25), (64, -0.3), (100, -0.2),
+         (100, -0.3), (130, -0.1), (64, -0.001), (1000, -0.02), (3000, -0.005), (3000, -0.012)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("t,g", FADES)
+@pytest.mark.parametrize("dk,dv", [(16, 16), (50, 100), (128, 128), (256, 40)])
+def test_old_states_fade_to_their_last_bits(cuda_device, dk, dv, t, g, dtype):
+    """h_out from h_in with nothing added, dh_in from dh_out with nothing asked of the tokens, and the decay's gradient of
+    both, whole calls and (few heads, many tokens) split ones."""
+    gen = torch.Generator().manual_seed(100)
+    c = Linear(2, t, 2, dk, dv, dtype=dtype)
+    decay = torch.tensor([g, 0.7 * g])
+    h, dh = positive(gen, 2, 2, dk, dv), positive(gen, 2, 2, dk, dv)
+    f = torch.exp(d64(decay) * t)[None, :, None, None]
+    for none in ("k", "v"):
+        got = c.forward(**{none: torch.zeros_like(c.i[none]), "h_in": h, "log_decay": dev(decay)})
+        torch.cuda.synchronize()
+        want = d64(h).cpu() * f
+        near(got["h_out"], want, old_depth(t, decay) * ho.EPS32 * want, "h_out")
+    zero = {"do": torch.zeros_like(c.i["do"]), "k": torch.zeros_like(c.i["k"])}
+    got = c.backward(("dh_in", "dlog_decay"), h_in=h, dh_out=dh, log_decay=dev(decay), **zero)
+    torch.cuda.synchronize()
+    want = d64(dh).cpu() * f
+    near(got["dh_in"], want, old_depth(t, decay) * ho.EPS32 * want, "dh_in")
+    # sum over tokens of <dh f[t-1-i], f f[i] h>: all terms are positive; sums of dk dv products along 16 terms a tile
+    # of a lane's columns and then in 64 bits, the factors of both states
+    want = t * (f * d64(h).cpu() * d64(dh).cpu()).sum((0, 2, 3))
+    near(got["dlog_decay"], want, (2 * old_depth(t, decay) + max(dk, dv) + 8) * ho.EPS32 * want, "dlog_decay")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_streamed_fades_follow_one_call(cuda_device, dtype):
+    """Single tokens and one call over all of them fade a state alike."""
+    gen = torch.Generator().manual_seed(101)
+    t, h, d = 90, 2, 32
+    decay = torch.tensor([-0.3, -0.21])
+    state = positive(gen, 1, h, d, d)
+    want = d64(state).cpu() * torch.exp(d64(decay) * t)[None, :, None, None]
+    zero = torch.zeros(1, t, h, d, dtype=dtype, device=DEV)
+    o, h_out = nan(1, t, h, d, dtype=dtype), nan(1, h, d, d)
+    plan = cc3d.linear_attention_plan(cc3d.make_linear_attention_desc(1, t, h, d, d, dtype=dtype))
+    cc3d.linear_attention_forward(plan, zero, zero, zero, o, log_decay=dev(decay), h_in=state, h_out=h_out, workspace=space(plan))
+    one = cc3d.linear_attention_plan(cc3d.make_linear_attention_desc(1, 1, h, d, d, dtype=dtype))
+    for p in range(t):
+        x = zero[:, p:p + 1]
+        cc3d.linear_attention_forward(one, x, x, x, o[:, p:p + 1], log_decay=dev(decay), h_in=state, h_out=state)
+    torch.cuda.synchronize()
+    near(h_out, want, old_depth(t, decay) * ho.EPS32 * want, "one call")
+    # (a factor's rounding each token, the exponential's few units, and the product's)
+    near(state, want, 6 * t * ho.EPS32 * want, "token by token")
