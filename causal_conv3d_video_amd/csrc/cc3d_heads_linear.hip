@@ -208,7 +208,8 @@ __global__ __launch_bounds__(256) void linear_join(JoinArgs a) {
         if (x0 + x >= between) break;
         const int segment = w.rev ? between - x0 - x : x0 + x;
         const int tokens = min(max(len - segment * a.seg, 0), a.seg);
-        s = float(fma(double(s), tokens == a.seg ? whole : fade64(g, tokens), double(u[x])));
+        const double f = tokens == a.seg ? whole : fade64(g, tokens);
+        s = f == 0.0 && __builtin_fabsf(s) == __builtin_inff() && lasting(g) ? s + u[x] : float(fma(double(s), f, double(u[x])));
         p[(x0 + x) * step] = s;
       }
     }

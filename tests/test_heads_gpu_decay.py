@@ -13,7 +13,7 @@ import torch
 import causal_conv3d_video_amd as cc3d
 import heads_oracle as ho
 from test_heads_gpu import BF, DEV, F32, d64, near
-from test_heads_gpu_edges import Linear
+from test_heads_gpu_edges import INF, Linear, same
 from test_seq_gpu import dev, nan, space
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +79,32 @@ def test_streamed_fades_follow_one_call(cuda_device, dtype):
     near(h_out, want, old_depth(t, decay) * ho.EPS32 * want, "one call")
     # (a factor's rounding each token, the exponential's few units, and the product's)
     near(state, want, 6 * t * ho.EPS32 * want, "token by token")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("g", [0.0, -0.01, -0.5, -2.0, -20.0])
+@pytest.mark.parametrize("t,ragged", [(1, None), (20, None), (70, None), (130, [130, 0, 64, 7]), (3000, [3000, 0, 1, 700])])
+def test_infinite_states_stay_infinite(cuda_device, t, ragged, g, dtype):
+    """An infinity among h_in (dh_out) fades to an infinity, through blocks and segments with tokens and without; whatever it
+    does not reach keeps its bits."""
+    n = len(ragged) if ragged else 2
+    c = Linear(n, t, 2, 24, 40, dtype=dtype, ragged=ragged)
+    decay = torch.full((2,), g, device=DEV)
+    assert t < 3000 or min(c.plan.info["chunks"], c.plan.info["backward_chunks"]) > 3
+    for name, call in (("h_in", c.forward), ("dh_out", lambda **kw: c.backward(("dk", "dv", "dh_in"), **kw))):
+        clean = call(log_decay=decay)
+        x = c.i[name].clone()
+        x[:, 0, 3, 5], x[:, 0, 11, 5] = INF, -INF
+        got = call(log_decay=decay, **{name: x})
+        torch.cuda.synchronize()
+        out = "h_out" if name == "h_in" else "dh_in"
+        assert bool((got[out][:, 0, 3, 5] == INF).all()) and bool((got[out][:, 0, 11, 5] == -INF).all()), name
+        got[out][:, 0, [3, 11], 5] = clean[out][:, 0, [3, 11], 5]
+        for k in got:
+            same(got[k][..., 1, :, :] if k == out else got[k][:, :, 1], clean[k][..., 1, :, :] if k == out else clean[k][:, :, 1], k)
+        same(got[out], clean[out], out)
+        if name == "h_in" and g > -2:
+            # column 5 of what the state met
+            rest = [e for e in range(40) if e != 5]
+            same(got["o"][..., rest], clean["o"][..., rest])
+            assert not bool(torch.isfinite(got["o"][0, :, 0, 5]).any())
