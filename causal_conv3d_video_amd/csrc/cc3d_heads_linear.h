@@ -502,8 +502,8 @@ __global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void line
   Raw8<T> kn[kVecK], vn[kVecV], qn[OUT ? kVecK : 1], xn[DEC ? kVecV : 1];
   const int krow = tid / (DP / 8), kcol = tid % (DP / 8) * 8, vrow = tid / (CB / 8), vcol = tid % (CB / 8) * 8;
   const Cols8<T, KIND> kc(kcol, c_all), vc(vcol, width);
-  auto fetch = [&](int p0) {
-    const int m = min(TOK, end - p0);
+  auto fetch = [&](int p0, int blk) {
+    const int m = min(blk, end - p0);
     const int64_t t = p0;
     const T *kb = k + t * kr, *vb = v + t * vr;
     auto place_of = [&](int j, int stride, const Cols8<T, KIND>& c) {
@@ -525,9 +525,26 @@ __global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void line
       for (int y = 0; y < kVecV; ++y) xn[y] = vc.load(by(xb, place_of(vrow + y * kStepV, xr, vc)), width);
     }
   };
-  // blocks of the segment's tokens, from the last one where time is reversed
-  const int count = (max(end - begin, 0) + TOK - 1) / TOK, first = begin + (rev ? (count - 1) * TOK : 0), step = rev ? -TOK : TOK;
-  if (count > 0) fetch(first);
+  // Blocks of the segment's tokens, from the last one where time is reversed.  Where states grow so fast that
+  // products of three factors over 64 tokens may be no fp32 numbers, a block has fewer tokens (and `apart` is the
+  // farthest that two of them are): rows of zeros in front of them are to stay zeros, whatever they are multiplied
+  // by.  With the decay's gradient, whose states lie TOK tokens apart, those products are held at `top`
+  // instead where those of valid tokens are within it.
+  const float g = a.log_decay ? a.log_decay[h] : 0.f, g2 = g * kLog2e;
+  const int all = max(end - begin, 0);
+  int blk = TOK, apart = TOK;
+  float top = __builtin_inff();
+  if constexpr (DEC) {
+    if (g2 * float(min(all, TOK)) < 126.f) top = 0x1.fffffep127f;
+    if (g2 != g2) top = g2;
+  } else if (g2 * float(TOK) > 36.f) {
+    blk = pin(max(int(36.f / g2), 1));
+    apart = blk - 1;
+  }
+  auto held = [&](float f) { return DEC ? __builtin_amdgcn_fmed3f(f, -top, top) : f; };
+  const int count = blk == TOK ? (all + TOK - 1) / TOK : (all + blk - 1) / blk;
+  const int first = begin + (rev ? (count - 1) * blk : 0), step = rev ? -blk : blk;
+  if (count > 0) fetch(first, blk);
 
   // ---- the state before the segment: result i of tile mt is c = 32 mt + 16 (i / 8) + 8 hh + i % 8 of the lane's column
   f32x16_h st[kMt];
@@ -601,22 +618,21 @@ __global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void line
   // ---- factors, all of them f of a number of tokens, never of less than none.  Token j of a block (from its end)
   // adds f[TOK-1-j] = f[16 (TOK/16-1-j/16)] f[15-j%16], and tokens i of the second tile and j of the first are
   // f[il+1] f[31-jl] apart: a few by step, in scalar registers, times a few by lane.
-  const float g = a.log_decay ? a.log_decay[h] : 0.f, g2 = g * kLog2e;
-  Fades fades(g, TOK, count > 0 ? (end - begin - 1) % TOK + 1 : 0);
+  Fades fades(g, blk, count > 0 ? all - (count - 1) * blk : 0);
   fades.hi = pin(fades.hi);
   fades.lo = pin(fades.lo);
   fades.inverse = pin(fades.inverse);
   fades.last = pin(fades.last);
   float fq[8], diag[OUT ? 16 : 1], f_lane = 0.f, f_step[kTs];
 #pragma unroll
-  for (int b = 0; b < 8; ++b) fq[b] = fade(g2, 15 - 8 * hh - b);
+  for (int b = 0; b < 8; ++b) fq[b] = fade(g2, min(15 - 8 * hh - b, apart));
 #pragma unroll
-  for (int y = 0; y < kTs; ++y) f_step[y] = pin(fade(g2, 16 * y));
+  for (int y = 0; y < kTs; ++y) f_step[y] = pin(fade(g2, min(16 * y, apart)));
   const float f_last = pin(r.update) * fade(g2, 1 - r_lead), inter = pin(r.inter), score = pin(r.score);
   if constexpr (OUT) {
 #pragma unroll
-    for (int b = 0; b < 16; ++b) diag[b] = score * fade(g2, max(il - (16 * (b / 8) + 8 * hh + b % 8), 0));
-    f_lane = score * fade(g2, il + 1);
+    for (int b = 0; b < 16; ++b) diag[b] = held(score * fade(g2, min(max(il - (16 * (b / 8) + 8 * hh + b % 8), 0), apart)));
+    f_lane = score * fade(g2, min(il + 1, apart));
   }
   if (tid < 2) odd[tid] = 0;
   __syncthreads();
@@ -625,7 +641,7 @@ __global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void line
   const bool keeps = OUT ? (rev ? s == 0 : s + 1 == a.segs) && r.to : true;  // the state after the segment is asked for
   int turn = 0;
   for (int b0 = 0, p0 = first; b0 < count; ++b0, p0 += step, turn ^= 1) {
-    const int m = min(TOK, end - p0), none = TOK - m;
+    const int m = min(blk, end - p0), none = TOK - m;
     const bool more = b0 + 1 < count;
     // (what follows from these is cheap, and would be kept in registers over all blocks)
     asm volatile("" : "+v"(fq[0]), "+v"(fq[1]), "+v"(fq[2]), "+v"(fq[3]), "+v"(fq[4]), "+v"(fq[5]), "+v"(fq[6]), "+v"(fq[7]));
@@ -655,7 +671,7 @@ __global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void line
     }
     if (OUT && full) odd[turn] = 1;
     __syncthreads();
-    if (more) fetch(p0 + step);
+    if (more) fetch(p0 + step, blk);
     const bool strange = pin(odd[turn]) != 0;
 
     const T* q_row = lds + L::kQ + il * kRowQ + 8 * hh;
@@ -673,7 +689,7 @@ __global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void line
         for (int y = 0; y < kSteps; ++y) pr = M::mma(M::row(kp + 16 * y), M::row(qp + 16 * y), pr);
         if (pair == 1) {
 #pragma unroll
-          for (int b = 0; b < 16; ++b) pr[b] *= f_lane * f_step[1 - b / 8] * fq[b % 8];
+          for (int b = 0; b < 16; ++b) pr[b] *= held(f_lane * f_step[1 - b / 8] * fq[b % 8]);
         } else {
 #pragma unroll
           for (int b = 0; b < 16; ++b) pr[b] = 16 * (b / 8) + 8 * hh + b % 8 <= il ? pr[b] * diag[b] : 0.f;
@@ -846,7 +862,7 @@ __global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void line
 
     // ---- the state after the block, 16 tokens at a time
     if (has) {
-      const float fade_st = pin(fades.next(m == TOK));
+      const float fade_st = pin(fades.next(m == blk));
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
@@ -858,7 +874,7 @@ __global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void line
         const Frag vf = M::col(vt + 16 * y * kRowV, kRowV);
         float fy[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) fy[i] = fq[i] * (f_step[kTs - 1 - y] * f_last);
+        for (int i = 0; i < 8; ++i) fy[i] = held(fq[i] * (f_step[kTs - 1 - y] * f_last));
         Frag f[M::kParts];
         M::scaled(vf, fy, f);
 #pragma unroll

@@ -209,7 +209,9 @@ __global__ __launch_bounds__(256) void linear_join(JoinArgs a) {
         const int segment = w.rev ? between - x0 - x : x0 + x;
         const int tokens = min(max(len - segment * a.seg, 0), a.seg);
         const double f = tokens == a.seg ? whole : fade64(g, tokens);
-        s = f == 0.0 && __builtin_fabsf(s) == __builtin_inff() && lasting(g) ? s + u[x] : float(fma(double(s), f, double(u[x])));
+        // (no state grows to none, however fast)
+        const bool as_it_is = s == 0.f || (f == 0.0 && __builtin_fabsf(s) == __builtin_inff() && lasting(g));
+        s = as_it_is ? s + u[x] : float(fma(double(s), f, double(u[x])));
         p[(x0 + x) * step] = s;
       }
     }

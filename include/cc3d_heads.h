@@ -37,7 +37,9 @@ extern "C" {
  * q, k and v may have fewer heads than o, each a divisor of `heads`: head h
  * uses head h / (heads / q_heads) of q, and likewise of k and v.  log_decay
  * NULL: zeros (no decay); minus infinity forgets at once; growth (> 0) is
- * taken as it comes.  h_in NULL: zeros.  h_out may be the same buffer as h_in.
+ * taken as it comes while exp(log_decay) is an fp32 number (with dlog_decay:
+ * while that over the tokens of a sequence is, or over 64 of them).  An infinite
+ * state stays one.  h_in NULL: zeros.  h_out may be the same buffer as h_in.
  * A step of a decode loop is a call with T = 1.
  *
  * Backward, with G the gradient of S (started from dh_out, NULL: zeros):

@@ -108,3 +108,61 @@ def test_infinite_states_stay_infinite(cuda_device, t, ragged, g, dtype):
             rest = [e for e in range(40) if e != 5]
             same(got["o"][..., rest], clean["o"][..., rest])
             assert not bool(torch.isfinite(got["o"][0, :, 0, 5]).any())
+
+
+def growing_case(n, t, h, dk, dv, dtype, g, ragged, seed, zeros=0):
+    c = Linear(n, t, h, dk, dv, dtype=dtype, ragged=ragged, seed=seed)
+    i = dict(c.i)
+    i["log_decay"] = torch.linspace(g, 0.6 * g, h, device=DEV)
+    if zeros:  # tokens that add nothing
+        for x in ("k", "v"):
+            i[x] = i[x].clone()
+            i[x][:, :zeros] = 0
+        i["h_in"] = None
+    args = [d64(i[x].cpu()) for x in ("q", "k", "v", "log_decay")] + [float(c.plan.desc.scale)]
+    return c, i, args
+
+
+# n, t, valid tokens, g, tokens of zeros before: states grow to 1e3 to 1e35 and fit fp32
+GROWTH = [(1, 5, None, 1.6, 0), (1, 1, None, 3.0, 0), (1, 1, None, 60.0, 0), (2, 2, None, 30.0, 0), (1, 12, None, 5.0, 0),
+          (1, 20, None, 3.5, 0), (1, 40, None, 1.5, 0), (1, 33, None, 2.1, 0), (3, 64, [64, 5, 1], 1.1, 0), (4, 100, [1, 5, 0, 40], 1.5, 0),
+          (4, 3000, [1, 20, 0, 40], 1.6, 0), (1, 20, None, 5.0, 8), (1, 64, None, 2.0, 40), (1, 130, None, 2.0, 100),
+          (2, 3000, [1995, 2000], 2.5, 1980), (2, 3000, [3000, 3000], 2.5, 2970)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv", [(16, 16), (50, 100), (128, 128)])
+@pytest.mark.parametrize("n,t,ragged,g,zeros", GROWTH)
+def test_strong_growth(cuda_device, n, t, ragged, g, zeros, dk, dv, dtype):
+    """Decays far above one, where the growth over a block of 64 tokens is no fp32 number and the states are."""
+    c, i, args = growing_case(n, t, 2, dk, dv, dtype, g, ragged, 110, zeros)
+    got = c.forward(**{k: i[k] for k in ("k", "v", "log_decay", "h_in")})
+    torch.cuda.synchronize()
+    args += [None if i["h_in"] is None else d64(i["h_in"].cpu()), ragged, 2]
+    want, last = ho.linear(*args)
+    mag, mag_last = ho.linear(*args, mag=True)
+    assert float(mag_last.abs().max()) < 3e37
+    depth, bf = ho.linear_depth(t, dk, dv), dtype == BF
+    near(got["o"], want, ho.linear_bound(mag, want, dtype, depth, 2.0 ** -8 if bf else 0.0), "o")
+    near(got["h_out"], last, ho.linear_bound(mag_last, last, F32, depth, 0.0), "h_out")
+
+
+# (the products of states and their gradients grow as often as both do together)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv", [(16, 16), (50, 100), (128, 128)])
+@pytest.mark.parametrize("n,t,ragged,g", [(1, 1, None, 3.0), (1, 1, None, 60.0), (1, 5, None, 1.6), (1, 20, None, 3.2), (1, 33, None, 1.9),
+                                          (1, 40, None, 1.5), (4, 100, [1, 5, 0, 40], 1.5), (4, 3000, [1, 20, 0, 40], 1.6)])
+def test_strong_growth_backward(cuda_device, n, t, ragged, g, dk, dv, dtype):
+    c, i, args = growing_case(n, t, 2, dk, dv, dtype, g, ragged, 111)
+    args += [d64(i[x].cpu()) for x in ("do", "h_in", "dh_out")] + [ragged, 2]
+    want, mag = ho.linear_grad(*args), ho.linear_grad(*args, mag=True)
+    assert max(float(x.max()) for x in mag.values()) < 3e37
+    depth, bf = 2 * ho.linear_depth(t, dk, dv) + 2, dtype == BF
+    for ask in (("dq", "dk", "dv", "dlog_decay", "dh_in"), ("dq", "dk", "dv", "dh_in")):
+        got = c.backward(ask, log_decay=i["log_decay"])
+        torch.cuda.synchronize()
+        for x in ask:
+            f32 = x in ("dh_in", "dlog_decay")
+            near(got[x], want[x], ho.linear_bound(mag[x], want[x], F32 if f32 else dtype, depth + n * t * (x == "dlog_decay"),
+                                                  2.0 ** -8 if bf and not f32 else 0.0), x)
+
