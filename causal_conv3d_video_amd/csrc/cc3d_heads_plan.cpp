@@ -21,6 +21,8 @@ bool within_span(std::initializer_list<int64_t> sizes) {
 constexpr int64_t kMaxHeadRow = (int64_t(1) << 24) - 1;
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
+// No position is as far: offsets are 32 bits, tokens of a call up to 2^30.
+constexpr double kFarthest = 4294967296.0;
 
 }  // namespace
 
@@ -168,7 +170,7 @@ extern "C" cc3d_status_t rotary_plan(const cc3d_rotary_desc_t* d, cc3d_rotary_pl
   if (!d || d->n < 1 || d->t < 1 || d->q_heads < 1 || d->k_heads < 0 || d->d < 1 || d->rot < 2 || d->rot % 2 ||
       d->first < 0 || d->first > d->d - d->rot ||
       (d->layout != CC3D_ROTARY_HALF && d->layout != CC3D_ROTARY_INTERLEAVED) || d->scaling < CC3D_ROTARY_UNSCALED ||
-      d->scaling > CC3D_ROTARY_PARTS || !known_dtype(d->dtype) || !positive(d->theta) || !std::isfinite(d->amplitude) ||
+      d->scaling > CC3D_ROTARY_PARTS || !known_dtype(d->dtype) || !positive(d->theta) || !std::isfinite(float(d->amplitude)) ||
       (d->scaling != CC3D_ROTARY_UNSCALED && !positive(d->factor)) || (d->scaling == CC3D_ROTARY_BASE && d->rot < 4) ||
       (d->scaling == CC3D_ROTARY_PARTS &&
        !(positive(d->original) && std::isfinite(d->fast) && d->slow >= 0.0 && d->fast > d->slow)))
@@ -182,10 +184,7 @@ extern "C" cc3d_status_t rotary_plan(const cc3d_rotary_desc_t* d, cc3d_rotary_pl
   const int64_t tokens =
       std::max<int64_t>(1, std::min<int64_t>({ceildiv(4 * cc3d::kRotaryThreads, each), all / (4 * kUnits), 16}));
   if (!cc3d::fits(ceildiv(all, tokens), cc3d::kRotaryThreads)) return refuse(CC3D_ERR_UNSUPPORTED);
-  auto* p = make_plan<cc3d_rotary_plan>(d);
-  if (!p) return CC3D_ERR_NO_MEMORY;
-  p->tokens = int32_t(tokens);
-  p->info.chunks = p->info.backward_chunks = 1;
+  double each_turns[128];
   double theta = d->theta;
   if (d->scaling == CC3D_ROTARY_BASE) theta *= std::pow(d->factor, double(d->rot) / (d->rot - 2));
   for (int j = 0; j < d->rot / 2; ++j) {
@@ -196,8 +195,14 @@ extern "C" cc3d_status_t rotary_plan(const cc3d_rotary_desc_t* d, cc3d_rotary_pl
       const double keep = std::min(1.0, std::max(0.0, (turns - d->slow) / (d->fast - d->slow)));
       f = f * keep + f / d->factor * (1.0 - keep);
     }
-    p->turns[j] = f / kTwoPi;
+    each_turns[j] = f / kTwoPi;
+    if (!std::isfinite(each_turns[j] * kFarthest)) return refuse(CC3D_ERR_INVALID_ARG);
   }
+  auto* p = make_plan<cc3d_rotary_plan>(d);
+  if (!p) return CC3D_ERR_NO_MEMORY;
+  p->tokens = int32_t(tokens);
+  p->info.chunks = p->info.backward_chunks = 1;
+  std::copy(each_turns, each_turns + d->rot / 2, p->turns);
   *out = p;
   return CC3D_OK;
 }

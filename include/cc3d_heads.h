@@ -107,7 +107,9 @@ cc3d_status_t linear_attention_backward(cc3d_linear_plan_t plan, const cc3d_line
  *   PARTS   pairs that make more than `fast` turns in `original` tokens keep
  *           f, those with fewer than `slow` take f / factor, between the two
  *           the mean, weighted by (turns - slow) / (fast - slow)
- * Angles are reduced in 64 bits: far positions turn as exactly as near ones.
+ * Angles are reduced in 64 bits: position p's are off by p * 2^-52 or so, less
+ * than fp32 results show up to 2^27.  A descriptor whose frequencies are no
+ * numbers (a factor of 1e-310) is refused.
  * The backward call turns gradients of q_out and k_out back.  An output may be
  * its input's very view.
  * ------------------------------------------------------------------------ */
@@ -133,7 +135,7 @@ typedef struct cc3d_rotary_desc {
   double theta;               /* > 0 */
   double factor;              /* > 0; not used without scaling */
   double original, fast, slow; /* PARTS: > 0, fast > slow >= 0 */
-  double amplitude;           /* finite */
+  double amplitude;           /* a finite fp32 number */
 } cc3d_rotary_desc_t;
 
 typedef struct cc3d_rotary_args {
