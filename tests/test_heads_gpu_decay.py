@@ -166,3 +166,23 @@ def test_strong_growth_backward(cuda_device, n, t, ragged, g, dk, dv, dtype):
             near(got[x], want[x], ho.linear_bound(mag[x], want[x], F32 if f32 else dtype, depth + n * t * (x == "dlog_decay"),
                                                   2.0 ** -8 if bf and not f32 else 0.0), x)
 
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_streamed_states_keep_32_bits(cuda_device, dtype):
+    """The state of chunks of 3, 64, 40, 1 and 17 tokens: nothing of what is added to it is rounded to the tensors' type."""
+    sizes = [3, 64, 40, 1, 17]
+    t = sum(sizes)
+    c = Linear(2, t, 3, 40, 24, dtype=dtype, seed=140)
+    i = c.i
+    args = [d64(i[x].cpu()) for x in ("q", "k", "v", "log_decay")] + [float(c.plan.desc.scale), d64(i["h_in"].cpu()), None, 3]
+    last, mag = ho.linear(*args)[1], ho.linear(*args, mag=True)[1]
+    state, at = i["h_in"].clone(), 0
+    for m in sizes:
+        plan = cc3d.linear_attention_plan(cc3d.make_linear_attention_desc(2, m, 3, 40, 24, dtype=dtype))
+        q, k, v = (i[x][:, at:at + m] for x in ("q", "k", "v"))
+        cc3d.linear_attention_forward(plan, q, k, v, nan(2, m, 3, 24, dtype=dtype), log_decay=i["log_decay"], h_in=state,
+                                      h_out=state, workspace=space(plan))
+        at += m
+    torch.cuda.synchronize()
+    near(state, last, ho.linear_bound(mag, last, F32, ho.linear_depth(t, 40, 24) + 8 * len(sizes), 0.0), "state")
