@@ -49,14 +49,18 @@ void split_time(int32_t t, int64_t units, int cols, int32_t* seg, int32_t* segs)
   *segs = int32_t(ceildiv(blocks, each));
 }
 
-// Forward calls that take their tokens one after another: one or two of them, up to
-// eight where the states are few enough that only latency counts, and in fp32, whose
-// matrix products are no faster than its vector ones, up to 32.  bf16, both ways (one
-// after another, and as a block): 128 sequences of 16 heads of 128, 71 and 61 us for 2
-// tokens and 98 and 65 for 8; 1560 of 6 heads of 64, 85 and 77 and 97 and 80; 64 of 12
-// heads of 64, 8.2 and 10.5 and 9.7 and 10.6.  fp32: 1560 of 6 heads of 64, 32 tokens, 207 and 260.
+// Forward calls that take their tokens one after another, in fp32 throughout, instead of as a
+// block.  Both ways, in this order, us:
+//   bf16, up to two, where the states' bytes are most of it: 1560 sequences of 6 heads of 64, 84 and 80 for 2
+//   tokens; 128 of 16 of 128, 72 and 63; 512 of 4 of 256, 283 and 327.  Up to eight where the states are so
+//   few that only latency counts: 64 of 12 of 64, 8.5 and 10.8 for 2 and 9.8 and 11.1 for 8; 16 of 4 of 256,
+//   15 and 17 for 8.
+//   fp32, whose matrix products are no faster than its vector ones: up to 20 tokens, 161 and 162 for 20 and
+//   205 and 174 for 32 of 1560 by 6 heads of 64; 573 and 614, and 727 and 639, of 512 by 16 of 128; 59 and 61, and
+//   76 and 64, of 300 by 6 of 50 by 100.  Of wider q and k, whose rows take twice the registers, up to 12:
+//   20 and 25 for 12 tokens and 34 and 25 for 32 of 16 by 4 of 256; 506 and 473, and 977 and 486, of 512 by 4.
 bool linear_steps(const cc3d_linear_desc_t& d, int64_t workgroups) {
-  if (d.dtype != CC3D_BF16) return d.t <= 32;
+  if (d.dtype != CC3D_BF16) return d.t <= (d.dk <= 128 ? 20 : 12);
   return d.t <= 2 || (d.t <= 8 && workgroups <= 4 * kUnits);
 }
 
