@@ -42,21 +42,26 @@ extern "C" {
  * state stays one.  h_in NULL: zeros.  h_out may be the same buffer as h_in.
  * A step of a decode loop is a call with T = 1.
  *
- * Backward, with G the gradient of S (started from dh_out, NULL: zeros):
+ * Backward, with G the gradient of S (dh_out NULL: zeros):
  *   G[t] = scale * q[t]^T do[t] + exp(log_decay) * G[t+1]
+ *   G of the last valid token = scale * q^T do + dh_out
  *   dq = scale * S do;  dk = G v;  dv = k G;  dh_in = exp(log_decay) * G[0]
  *   dlog_decay = sum over sequences and tokens of <G[t], exp(log_decay) S[t-1]>
  * Gradients of shared heads are sums over the heads that share them.  The
  * states are computed again from h_in; nothing is kept by the forward call.
- * Any gradient may be left out.  Views whose tokens are 2^24 elements or more
- * apart are refused as unsupported (but with T = 1).
+ * Any gradient may be left out; the workspace is of the plan's size all the same
+ * (for dlog_decay, a padded state for every 64 tokens, or 32 of fp32 heads wider
+ * than 128; and the shared heads' parts).  Views whose tokens are 2^24 elements or
+ * more apart are refused as unsupported (but with T = 1).
  *
- * Tokens are taken 64 at a time with matrix products.  With bf16 tensors the
- * products of a token's q with the k of its 64 (and with the state before them)
- * are rounded to bf16 before they meet v (and q); what is added to a state, and
- * so h_out and dh_in, and what makes dlog_decay is not.  A value that is no
- * number reaches its own token's results and later ones, as the recurrence
- * says, and none before it.
+ * Tokens are taken 64 at a time with matrix products (few at a time one after
+ * another).  With bf16 tensors the products of a token's q with the k of its 64
+ * are rounded to bf16 before they meet v, and the state before the 64 before it
+ * meets q; what is added to a state, and so h_out and dh_in, and what makes
+ * dlog_decay is not.  Where dlog_decay is asked for, the state keeps its bits for
+ * dq and dk too, so their last bits are not those of a call without it.  A value
+ * that is no number reaches its own token's results and later ones and none
+ * before it; where the recurrence has an infinity there, they may have no number.
  * ------------------------------------------------------------------------ */
 typedef struct cc3d_linear_desc {
   int32_t n, t;                          /* sequences, tokens (up to 2^30); >= 1 */
