@@ -149,15 +149,20 @@ struct Fades {
   float hi, lo, inverse;  // of a whole block, in two parts
   float last;             // of the block that may be less
   float drift = 0.f;      // of the factors so far, relative
-  __device__ __forceinline__ Fades(float g, int whole, int rest) {
-    const double f = fade64(g, whole);
+  // (an exponential in 64 bits costs a short call's workgroups 1% and more: only those that are used)
+  __device__ __forceinline__ Fades(float g, int whole, int rest, bool more) : hi(0.f), lo(0.f), inverse(0.f) {
     const float least = lasting(g) ? 0x1p-149f : 0.f;
-    hi = float(f);
-    if (hi < least) hi = least;
-    last = float(fade64(g, rest));
+    if (more || rest == whole) {
+      const double f = fade64(g, whole);
+      hi = float(f);
+      if (hi < least) hi = least;
+      if (f > 1e-30 && f < 1e30) {
+        lo = float(f - double(hi));
+        inverse = __builtin_amdgcn_rcpf(hi);
+      }
+    }
+    last = rest == whole ? hi : float(fade64(g, rest));
     if (last < least) last = least;
-    lo = f > 1e-30 && hi < __builtin_inff() ? float(f - double(hi)) : 0.f;
-    inverse = f > 1e-30 ? float(1.0 / f) : 0.f;
   }
   __device__ __forceinline__ float next(bool is_whole) {
     if (!is_whole) return last;
@@ -622,7 +627,7 @@ __global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void line
   // ---- factors, all of them f of a number of tokens, never of less than none.  Token j of a block (from its end)
   // adds f[TOK-1-j] = f[16 (TOK/16-1-j/16)] f[15-j%16], and tokens i of the second tile and j of the first are
   // f[il+1] f[31-jl] apart: a few by step, in scalar registers, times a few by lane.
-  Fades fades(g, blk, count > 0 ? all - (count - 1) * blk : 0);
+  Fades fades(g, blk, count > 0 ? all - (count - 1) * blk : 0, count > 1);
   fades.hi = pin(fades.hi);
   fades.lo = pin(fades.lo);
   fades.inverse = pin(fades.inverse);

@@ -184,8 +184,8 @@ struct JoinArgs {
   const int* lengths;
 };
 
-// States across segments: after[s] = f[tokens of s] before[s] + added[s], the factor
-// and its product in 64 bits.  Eight segments' loads are in flight.
+// States across segments: after[s] = f[tokens of s] before[s] + added[s] in 64 bits.  Eight
+// segments' loads are in flight.
 __global__ __launch_bounds__(256) void linear_join(JoinArgs a) {
   const JoinArgs::Way w = a.way[blockIdx.y];
   const int between = a.segs - 1;
@@ -193,12 +193,19 @@ __global__ __launch_bounds__(256) void linear_join(JoinArgs a) {
     const int64_t nh = item / a.size, off = item - nh * a.size, n = nh / a.heads;
     const float g = a.log_decay ? a.log_decay[nh - n * a.heads] : 0.f;
     const int len = valid_tokens(a.lengths, int(n), a.t);
-    const double whole = fade64(g, a.seg);
+    // (never zero while a token's is not, nor an infinity: infinite states stay so, and no state stays none)
+    const double least = lasting(g) ? 0x1p-1074 : 0.0;
+    auto fade_of = [&](int tokens) {
+      const double f = fade64(g, tokens);
+      return f < least ? least : f > 0x1.fffffffffffffp1023 ? 0x1.fffffffffffffp1023 : f;
+    };
+    const double whole = fade_of(a.seg);
     // (slot x lies between segments x and x + 1)
     float* p = w.segs + (nh * between + (w.rev ? between - 1 : 0)) * a.size + off;
     const int64_t step = w.rev ? -a.size : a.size;
-    float s = w.from ? w.from[item] : 0.f;
-    if (w.copy) w.copy[item] = s;
+    const float from = w.from ? w.from[item] : 0.f;
+    if (w.copy) w.copy[item] = from;
+    double s = from;
     for (int x0 = 0; x0 < between; x0 += 8) {
       float u[8];
 #pragma unroll
@@ -208,11 +215,8 @@ __global__ __launch_bounds__(256) void linear_join(JoinArgs a) {
         if (x0 + x >= between) break;
         const int segment = w.rev ? between - x0 - x : x0 + x;
         const int tokens = min(max(len - segment * a.seg, 0), a.seg);
-        const double f = tokens == a.seg ? whole : fade64(g, tokens);
-        // (no state grows to none, however fast)
-        const bool as_it_is = s == 0.f || (f == 0.0 && __builtin_fabsf(s) == __builtin_inff() && lasting(g));
-        s = as_it_is ? s + u[x] : float(fma(double(s), f, double(u[x])));
-        p[(x0 + x) * step] = s;
+        s = fma(s, tokens == a.seg ? whole : fade_of(tokens), double(u[x]));
+        p[(x0 + x) * step] = float(s);
       }
     }
   }

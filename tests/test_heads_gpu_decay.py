@@ -186,3 +186,21 @@ def test_streamed_states_keep_32_bits(cuda_device, dtype):
         at += m
     torch.cuda.synchronize()
     near(state, last, ho.linear_bound(mag, last, F32, ho.linear_depth(t, 40, 24) + 8 * len(sizes), 0.0), "state")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("t", [1, 20, 70, 3000])
+def test_a_decay_that_is_no_number_stays_with_its_head(cuda_device, t, dtype):
+    c = Linear(2, t, 3, 24, 40, dtype=dtype)
+    decay = c.i["log_decay"].clone()
+    decay[1] = float("nan")
+    for call in (c.forward, c.backward):
+        clean, got = call(), call(log_decay=decay)
+        torch.cuda.synchronize()
+        for k, v in got.items():
+            heads = {"h_out": 1, "dh_in": 1, "dlog_decay": 0}.get(k, 2)
+            pick = lambda x, h: x.select(heads, h)
+            for h in (0, 2):
+                same(pick(v, h), pick(clean[k], h), k)
+            if k in ("o", "h_out", "dh_in", "dlog_decay"):
+                assert bool(torch.isnan(pick(v, 1)).all()), k
