@@ -486,6 +486,7 @@ __global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void line
   const int h = pin(int(unit % a.heads)), n = pin(int(unit / a.heads));
   const int64_t nh = int64_t(n) * a.heads + h;
   const int e0 = block * CB;
+  const float g = a.log_decay ? a.log_decay[h] : 0.f;  // (in flight beside the length: the first rows wait for both)
   const int len = pin(valid_tokens(a.lengths, n, a.t));
   const int begin = s * a.seg, end = pin(min(begin + a.seg, len));
   const int c_all = pin(r.c), width = pin(min(CB, r.e - e0));
@@ -539,7 +540,7 @@ __global__ __launch_bounds__(2 * CB * SPLIT, (sizeof(T) == 2 ? 2 : 1)) void line
   // farthest that two of them are): rows of zeros in front of them are to stay zeros, whatever they are multiplied
   // by.  With the decay's gradient, whose states lie TOK tokens apart, those products are held at `top`
   // instead where those of valid tokens are within it.
-  const float g = a.log_decay ? a.log_decay[h] : 0.f, g2 = g * kLog2e;
+  const float g2 = g * kLog2e;
   const int all = max(end - begin, 0);
   int blk = TOK, apart = TOK;
   float top = __builtin_inff();
